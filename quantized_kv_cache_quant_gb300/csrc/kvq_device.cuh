@@ -224,6 +224,64 @@ __device__ __forceinline__ uint16_t f32x2_to_fp8x2(float lo, float hi) {
     return f32x2_to_e5m2x2(lo, hi);
 }
 
+// The two fp16x2 operands of one word of four FP8 bytes: bytes 0-1 and bytes
+// 2-3. An E5M2 byte is the top byte of the fp16 of the same value, so each
+// half is one byte permute straight from the word (no extraction of the 16-bit
+// half first); E4M3 converts each 16-bit half with its conversion instruction.
+template <int FMT>
+__device__ __forceinline__ uint32_t fp8_lo_pair(uint32_t w) {
+  if constexpr (FMT == 1)
+    return __byte_perm(w, 0u, 0x1404u);
+  else
+    return fp8x2_to_f16x2<FMT>(static_cast<uint16_t>(w & 0xFFFFu));
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t fp8_hi_pair(uint32_t w) {
+  if constexpr (FMT == 1)
+    return __byte_perm(w, 0u, 0x3424u);
+  else
+    return fp8x2_to_f16x2<FMT>(static_cast<uint16_t>(w >> 16));
+}
+
+// x / scale, the IEEE fp32 quotient of the formula. MODE 0: the IEEE division
+// itself. MODE 1 and 2: from y = RN(1/scale) and one correction step, which is
+// bit-identical for scales in [2^-96, 2^96]; MODE 1 also passes an infinite x
+// through (a static scale may meet infinities), MODE 2 leaves that test out: a
+// dynamic scale amax / 448 is only that finite when the tensor holds no
+// infinity or NaN (either one makes amax, hence the scale, non-finite).
+template <int MODE>
+__device__ __forceinline__ float scaled(float x, float scale, float y) {
+  if constexpr (MODE == 0) {
+    (void)y;
+    return __fdiv_rn(x, scale);
+  } else if constexpr (MODE == 1) {
+    return div_rn_by_rcp_signed(x, scale, y);
+  } else {
+    return copysignf(div_rn_by_rcp(x, scale, y), x);
+  }
+}
+
+// scaled<MODE> of both halves of an fp16 pair, the reciprocal path in packed
+// fp32 operations (the same steps, so the same quotients).
+template <int MODE>
+__device__ __forceinline__ float2 scaled_pair(uint32_t xh2, float scale, float y) {
+  const float2 x = __half22float2(bits_h2(xh2));
+  if constexpr (MODE == 0) {
+    (void)y;
+    return make_float2(__fdiv_rn(x.x, scale), __fdiv_rn(x.y, scale));
+  } else {
+    const float2 q0 = __fmul2_rn(x, make_float2(y, y));
+    const float2 r = __ffma2_rn(q0, make_float2(-scale, -scale), x);
+    const float2 q = __ffma2_rn(r, make_float2(y, y), q0);
+    float2 o = make_float2(copysignf(q.x, x.x), copysignf(q.y, x.y));
+    if constexpr (MODE == 1) {
+      if (isinf(x.x)) o.x = x.x;
+      if (isinf(x.y)) o.y = x.y;
+    }
+    return o;
+  }
+}
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));

@@ -1,0 +1,81 @@
+// Launch interface between the host layer of the speculative-decoding calls
+// (spec_api.cu) and their kernels.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace kvq {
+
+constexpr int kSpecMaxBatch = 4096;  // KVQ_SPEC_MAX_BATCH
+constexpr int kTreeMax = 256;        // KVQ_TREE_MAX
+constexpr int kTreeMaxGqa = 64;      // KVQ_TREE_MAX_GQA
+
+struct BlocksResizeArgs {
+  int32_t* block_table;
+  int32_t* n_held;
+  const int32_t* target_tokens;
+  int32_t* free_blocks;
+  int32_t* free_count;
+  int32_t* granted;  // or null
+  int batch, max_blocks, block_tokens, num_blocks;
+};
+cudaError_t launch_blocks_resize(const BlocksResizeArgs& a, cudaStream_t s);
+
+struct SlotMapArgs {
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+  int32_t* offsets;
+  int64_t* slots;
+  int32_t* seq_ids;    // or null
+  int32_t* positions;  // or null
+  int batch, max_blocks, block_tokens, num_blocks, n_rows;
+};
+cudaError_t launch_slot_map(const SlotMapArgs& a, cudaStream_t s);
+
+struct Fp8AppendArgs {
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  long long k_stride, v_stride;  // fp16 elements between tokens
+  const int64_t* slots;
+  int n_tokens, kv_heads, head_dim, num_blocks, per_head, fmt;
+  uint8_t* k_pool;
+  uint8_t* v_pool;
+  const float* k_scale;
+  const float* v_scale;
+};
+cudaError_t launch_fp8_append(const Fp8AppendArgs& a, cudaStream_t s);
+
+struct Fp8AcceptArgs {
+  uint8_t* k_pool;
+  uint8_t* v_pool;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* path;
+  const int32_t* n_accepted;
+  int32_t* new_lens;
+  int batch, max_blocks, path_len, kv_heads, head_dim, num_blocks;
+};
+cudaError_t launch_fp8_accept(const Fp8AcceptArgs& a, cudaStream_t s);
+
+struct TreeArgs {
+  const uint16_t* q;
+  long long q_stride;  // fp16 elements between rows of q
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* tree_offsets;
+  const uint64_t* tree_mask;
+  int mask_words;
+  int n_tokens, batch, q_heads, kv_heads, head_dim, max_blocks, num_blocks, max_tree, max_seq_len, per_head, fmt;
+  float scale_log2;  // softmax scale * log2(e)
+  void* out;
+  int out_fp32;
+};
+cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s);
+
+}  // namespace kvq
