@@ -26,6 +26,12 @@ kvq_status check_pool(const fp8_pool* p) {
   return KVQ_OK;
 }
 
+// Tree attention workspace: [status word | 256 B][counters][flags of the
+// partial results][(m, l) of their rows][o of their rows].
+constexpr size_t kTreeCounters = kvq::kWsHeader;
+constexpr size_t kTreeFlags = kTreeCounters + kvq::kTreeMaxBlocks * sizeof(uint32_t);
+constexpr size_t kTreePartials = kTreeFlags + 2 * kvq::kTreeMaxBlocks * sizeof(int);
+
 // A key pool and a value pool that belong together.
 kvq_status check_pools(const fp8_pool* k, const fp8_pool* v) {
   kvq_status st = check_pool(k);
@@ -150,7 +156,7 @@ size_t fp8_tree_workspace_bytes(int32_t batch, int32_t kv_heads, int32_t q_heads
       q_heads % kv_heads != 0 || q_heads / kv_heads > KVQ_TREE_MAX_GQA || (head_dim != 64 && head_dim != 128) ||
       max_tree <= 0 || max_tree > KVQ_TREE_MAX)
     return 0;
-  return 256;
+  return kTreePartials + static_cast<size_t>(kvq::kTreePartRows) * (head_dim + 2) * sizeof(float);
 }
 
 kvq_status fp8_tree_attention(const uint16_t* q, int64_t q_row_stride, int32_t n_tokens, const fp8_pool* k,
@@ -205,5 +211,11 @@ kvq_status fp8_tree_attention(const uint16_t* q, int64_t q_row_stride, int32_t n
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   a.out = out;
   a.out_fp32 = out_fp32;
+  uint8_t* const base = static_cast<uint8_t*>(ws);
+  a.status = reinterpret_cast<uint32_t*>(base);
+  a.counters = reinterpret_cast<uint32_t*>(base + kTreeCounters);
+  a.part_flag = reinterpret_cast<int*>(base + kTreeFlags);
+  a.part_ml = reinterpret_cast<float*>(base + kTreePartials);
+  a.part_o = a.part_ml + static_cast<size_t>(kvq::kTreePartRows) * 2;
   return from_cuda(kvq::launch_tree_attention(a, static_cast<cudaStream_t>(stream)));
 }

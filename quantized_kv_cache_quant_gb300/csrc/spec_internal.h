@@ -75,7 +75,17 @@ struct TreeArgs {
   float scale_log2;  // softmax scale * log2(e)
   void* out;
   int out_fp32;
+  uint32_t* status;
+  uint32_t* counters;  // [kTreeMaxBlocks], zero between calls
+  int* part_flag;      // [2 * kTreeMaxBlocks]
+  float* part_ml;      // [2 * kTreeMaxBlocks, R, 2]
+  float* part_o;       // [2 * kTreeMaxBlocks, R, D]
 };
+// Thread blocks of a tree attention launch at most (they leave two partial
+// results each), and the rows of their partial results in all: R rows times
+// two slots times the blocks of every kernel stay within kTreePartRows.
+constexpr int kTreeMaxBlocks = 1024;
+constexpr int kTreePartRows = 81920;
 cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s);
 
 }  // namespace kvq

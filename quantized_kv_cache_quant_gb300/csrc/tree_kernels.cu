@@ -1,105 +1,331 @@
 // Attention of a tree of drafted tokens over the paged FP8 cache (kvq_spec.h).
-#include "kvq_device.cuh"
-#include "kvq_internal.h"
-#include "spec_internal.h"
+#include "tree_plan.cuh"
 
 namespace kvq {
 namespace {
 
 constexpr int kBlock = 16;  // tokens of an FP8 pool block
-constexpr int kThreads = 128;
 
-// One thread block per (query row, query head): chunks of 128 tokens, a thread
-// per token for the scores, a thread per channel for the value sums, running
-// maximum and sum of the softmax.
-template <int D, int FMT>
-__global__ void __launch_bounds__(kThreads) tree_simple_kernel(TreeArgs a) {
-  __shared__ float qs[D], ps[kThreads], red[8];
-  __shared__ int blk_s[kThreads / kBlock + 1];
-  const int n = blockIdx.x, hq = blockIdx.y, tid = threadIdx.x;
-  const int gq = a.q_heads / a.kv_heads, h = hq / gq;
-  if (n < a.tree_offsets[0] || n >= a.tree_offsets[a.batch]) return;
-  int lo = 0, hi = a.batch;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.tree_offsets[mid] <= n) lo = mid;
-    else hi = mid;
+// ---------------------------------------------------------------------------
+// Few rows: 16 query rows a tile on mma.sync m16n8k16, the rows on the MMA's
+// 16-row side. Four warps; warp w takes every fourth block of the segment
+// through its own ring of bulk copies, with its own running maximum, sum and
+// outputs, joined at the end of the segment.
+//   q.k^T: A = q (channels permuted as the keys' order), B = the keys as fp16
+//   p.V  : A = p rounded to fp16 (WIDE: and what the rounding left, on a
+//          second product), B = the values as fp16
+// p carries a factor 2^kBias so that weights down to 2^-24 of the largest stay
+// normal fp16 numbers.
+// ---------------------------------------------------------------------------
+constexpr int kRows = 16;
+constexpr int kUnit = 64;    // tokens of a unit: one block a warp
+constexpr int kStages = 4;
+constexpr float kBias = 10.0f;
+
+template <int D>
+struct TreeSmem {
+  static constexpr int BAR_BYTES = 128;
+  static constexpr int STAGE = 2 * kBlock * D;
+  static constexpr int RING = 4 * kStages * STAGE;
+  static constexpr int COMBINE = (4 * kRows * (D + 2) + 2 * kRows) * 4;
+  static constexpr int AREA = RING > COMBINE ? RING : COMBINE;
+  static constexpr int BYTES = BAR_BYTES + AREA;
+};
+
+template <int D, int FMT, bool WIDE>
+__global__ void __launch_bounds__(128) tree_rows16_kernel(TreeArgs a) {
+  using S = TreeSmem<D>;
+  constexpr int KS = D / 16, NT = D / 8, CH = D / 32;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ unsigned long long plan_s[34];
+  __shared__ int nan_s, last_s;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
+  uint8_t* area = smem + S::BAR_BYTES;
+  float* o_s = reinterpret_cast<float*>(area);   // [4][16][D]
+  float* m_s = o_s + 4 * kRows * D;              // [4][16]
+  float* l_s = m_s + 4 * kRows;                  // [4][16]
+  float* merge_s = l_s + 4 * kRows;              // [2][16]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
+  const int gq = a.q_heads / a.kv_heads;
+  uint64_t* bar = bars + warp * kStages;
+  uint8_t* ring = area + warp * kStages * S::STAGE;
+  if (lane == 0) {
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) mbar_init(&bar[s], 1);
+    fence_mbar_init();
   }
-  const int b = lo, first = a.tree_offsets[b];
-  const int nodes = min(min(a.tree_offsets[b + 1] - first, a.max_tree), a.max_blocks * kBlock);
-  if (n - first >= nodes) return;
-  const int len = min(max(a.seq_lens[b], 0), a.max_blocks * kBlock - nodes);
-  const int total = len + nodes;
-  const __half* q = reinterpret_cast<const __half*>(a.q) + n * a.q_stride + hq * D;
-  if (tid < D) qs[tid] = __half2float(q[tid]) * (a.k_scale[a.per_head ? h : 0] * a.scale_log2);
-  const uint64_t* mask = a.tree_mask + static_cast<long long>(n) * a.mask_words;
-  float m_run = -INFINITY, l_run = 0.0f, o = 0.0f;
-  for (int t0 = 0; t0 < total; t0 += kThreads) {
-    __syncthreads();
-    if (tid < kThreads / kBlock && t0 + tid * kBlock < total) {
-      const int e = a.block_table[static_cast<long long>(b) * a.max_blocks + t0 / kBlock + tid];
-      blk_s[tid] = min(max(e, 0), a.num_blocks - 1);
+  const TreeSlice slice = tree_slice<kRows, kUnit>(a, plan_s, 2);
+  if (static_cast<int>(blockIdx.x) >= slice.blocks) return;
+
+  long long at = slice.begin, before = slice.before;
+  int b = slice.b;
+  unsigned it = 0;         // blocks this warp has taken through its ring
+  bool dead = false;       // a wait ran out: no more copies
+  TreeSegment seg;
+  while (next_segment<kRows, kUnit>(a, slice, at, b, before, seg)) {
+    const int h = seg.h, len = seg.r.len, total = len + seg.r.nodes, row0 = seg.tile * kRows;
+    const int rows = min(kRows, seg.r.nodes * gq - row0);
+    const int nblk = (total + kBlock - 1) / kBlock;
+    const int j_begin = seg.u0 * 4, j_end = min(seg.u1 * 4, nblk);
+    const int n_mine = (!dead && j_end - j_begin > warp) ? (j_end - j_begin - warp + 3) / 4 : 0;
+    const int32_t* table = a.block_table + static_cast<long long>(seg.b) * a.max_blocks;
+    auto phys = [&](int j) -> long long {
+      return min(max(table[j_begin + warp + 4 * j], 0), a.num_blocks - 1);
+    };
+    auto issue = [&](int j, long long blk) {
+      const long long off = (blk * a.kv_heads + h) * (kBlock * D);
+      const int s = (it + j) % kStages;
+      uint8_t* dst = ring + s * S::STAGE;
+      mbar_arrive_expect_tx(&bar[s], S::STAGE);
+      bulk_g2s(dst, a.k_pool + off, kBlock * D, &bar[s]);
+      bulk_g2s(dst + kBlock * D, a.v_pool + off, kBlock * D, &bar[s]);
+    };
+    if (lane == 0) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      for (int j = 0; j < kStages && j < n_mine; ++j) issue(j, phys(j));
     }
-    __syncthreads();
-    const int t = t0 + tid;
-    bool sees = t < total;
-    if (t >= len && t < total) sees = (mask[(t - len) >> 6] >> ((t - len) & 63)) & 1;
-    float s = -INFINITY;
-    if (sees) {
-      const int row = t % kBlock;
-      const uint8_t* kb = a.k_pool + (static_cast<long long>(blk_s[tid / kBlock]) * a.kv_heads + h) * (kBlock * D);
-      s = 0.0f;
-      for (int c = 0; c < D; c += 2) {
-        const int byte = ((row / 8 * (D / 64) + c / 64) * 32 + 4 * (row % 8) + c % 16 / 4) * 16 + c % 64 / 16 * 4 + c % 4;
-        const float2 kf = __half22float2(bits_h2(fp8x2_to_f16x2<FMT>(*reinterpret_cast<const uint16_t*>(kb + byte))));
-        s = fmaf(qs[c], kf.x, s);
-        s = fmaf(qs[c + 1], kf.y, s);
+    if (tid == 0) nan_s = 0;
+
+    // query rows g and g + 8 of the tile, A fragments of m16n8k16
+    uint32_t qa[KS][4];
+    const uint64_t* mask[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = row0 + g + 8 * e;
+      const bool ok = g + 8 * e < rows;
+      const int n = seg.r.first + (ok ? r / gq : 0);
+      mask[e] = a.tree_mask + static_cast<long long>(n) * a.mask_words;
+      const __half* qrow = reinterpret_cast<const __half*>(a.q) + n * a.q_stride +
+                           static_cast<long long>(h * gq + (ok ? r % gq : 0)) * D;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const uint2 w = ok ? *reinterpret_cast<const uint2*>(qrow + 16 * ks + 4 * tig) : make_uint2(0u, 0u);
+        qa[ks][e] = w.x;
+        qa[ks][2 + e] = w.y;
       }
     }
-    const float wm = warp_max(s);
-    if ((tid & 31) == 0) red[tid >> 5] = wm;
-    __syncthreads();
-    const float m_new = fmaxf(m_run, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float alpha = m_run == -INFINITY ? 0.0f : fast_exp2(m_run - m_new);
-    const float p = sees ? fast_exp2(s - m_new) : 0.0f;
-    ps[tid] = sees ? p : -1.0f;  // -1: not seen (its value bytes are not read)
-    const float ws = warp_sum(p);
-    if ((tid & 31) == 0) red[4 + (tid >> 5)] = ws;
-    __syncthreads();
-    l_run = l_run * alpha + (red[4] + red[5]) + (red[6] + red[7]);
-    m_run = m_new;
-    if (tid < D) {
-      o *= alpha;
-      const int c = tid;
-      for (int i = 0; i < kThreads && t0 + i < total; ++i) {
-        if (ps[i] < 0.0f) continue;
-        const int row = i % kBlock;
-        const uint8_t* vb = a.v_pool + (static_cast<long long>(blk_s[i / kBlock]) * a.kv_heads + h) * (kBlock * D);
-        const int byte = (c / 32 * 32 + 4 * (c % 8) + row % 8 / 2) * 16 + c % 32 / 8 * 4 + row / 8 * 2 + row % 2;
-        o = fmaf(ps[i], __low2float(bits_h2(fp8x2_to_f16x2<FMT>(vb[byte]))), o);
+    const float kmul = a.k_scale[a.per_head ? h : 0] * a.scale_log2;
+    const float vscale = a.v_scale[a.per_head ? h : 0];
+
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.0f, 0.0f};
+    float o_acc[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o_acc[i][0] = o_acc[i][1] = o_acc[i][2] = o_acc[i][3] = 0.0f;
+    bool nan_met = false;
+
+    int j = 0;
+    bool timed_out = false;
+    for (; j < n_mine; ++j) {
+      const int s = (it + j) % kStages;
+      const long long next_blk = (lane == 0 && j + kStages < n_mine) ? phys(j + kStages) : 0;
+      if (__any_sync(0xffffffffu, !mbar_wait_bounded(&bar[s], ((it + j) / kStages) & 1))) {
+        timed_out = true;
+        break;
+      }
+      const uint4* kb = reinterpret_cast<const uint4*>(ring + s * S::STAGE);
+      const uint4* vb = reinterpret_cast<const uint4*>(ring + s * S::STAGE + kBlock * D);
+      const int tok_base = (j_begin + warp + 4 * j) * kBlock;
+      uint32_t kw[2 * KS];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const uint4 x = kb[c * 32 + lane];
+        kw[4 * c] = x.x;
+        kw[4 * c + 1] = x.y;
+        kw[4 * c + 2] = x.z;
+        kw[4 * c + 3] = x.w;
+      }
+      float sacc[2][4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        sacc[nt][0] = sacc[nt][1] = sacc[nt][2] = sacc[nt][3] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint32_t w = kw[nt * KS + ks];
+          mma16816(sacc[nt], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], fp8_lo_pair<FMT>(w), fp8_hi_pair<FMT>(w));
+        }
+      }
+      uint32_t vw[NT];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const uint4 x = vb[c * 32 + lane];
+        vw[4 * c] = x.x;
+        vw[4 * c + 1] = x.y;
+        vw[4 * c + 2] = x.z;
+        vw[4 * c + 3] = x.w;
+      }
+      // scores of rows g (sc[0]) and g + 8 (sc[1]): tokens 2tig, 2tig + 1, 8 + 2tig, 9 + 2tig
+      float sc[2][4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[e][i] = sacc[i >> 1][2 * e + (i & 1)] * kmul;
+      if (tok_base + kBlock > len) {  // the tree's own tokens, and rows behind them
+        uint32_t keep = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tok = tok_base + 8 * (i >> 1) + 2 * tig + (i & 1);
+          if (tok < total) keep |= 0xFFu << (8 * i);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (!tree_sees(mask[e], tok, len, total)) sc[e][i] = -INFINITY;
+        }
+        // context tokens are seen by every row: their NaN codes stay as they are
+        uint32_t tree_bytes = keep;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (tok_base + 8 * (i >> 1) + 2 * tig + (i & 1) < len) tree_bytes &= ~(0xFFu << (8 * i));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t bad = fp8_nonfinite<FMT>(vw[nt]) & tree_bytes;
+          nan_met |= bad != 0;
+          vw[nt] &= keep & ~bad;
+        }
+      }
+      uint32_t A[4], L[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float mx = quad_max(fmaxf(fmaxf(sc[e][0], sc[e][1]), fmaxf(sc[e][2], sc[e][3])));
+        const float m_new = fmaxf(m_run[e], mx);
+        if (m_new != m_run[e]) {
+          const float alpha = fast_exp2(m_run[e] - m_new);
+          l_run[e] *= alpha;
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            o_acc[i][2 * e] *= alpha;
+            o_acc[i][2 * e + 1] *= alpha;
+          }
+          m_run[e] = m_new;
+        }
+        const float sub = (m_new == -INFINITY ? 0.0f : m_new) - kBias;
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = fast_exp2(sc[e][i] - sub);
+        l_run[e] += (p[0] + p[1]) + (p[2] + p[3]);
+        const __half2 h0 = __floats2half2_rn(p[0], p[1]), h1 = __floats2half2_rn(p[2], p[3]);
+        A[e] = h2_bits(h0);
+        A[2 + e] = h2_bits(h1);
+        if constexpr (WIDE) {
+          const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+          L[e] = pack_rn_f16x2(p[0] - f0.x, p[1] - f0.y);
+          L[2 + e] = pack_rn_f16x2(p[2] - f1.x, p[3] - f1.y);
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint32_t b0 = fp8_lo_pair<FMT>(vw[nt]), b1 = fp8_hi_pair<FMT>(vw[nt]);
+        mma16816(o_acc[nt], A[0], A[1], A[2], A[3], b0, b1);
+        if constexpr (WIDE) mma16816(o_acc[nt], L[0], L[1], L[2], L[3], b0, b1);
+      }
+      __syncwarp();
+      if (lane == 0 && j + kStages < n_mine) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        issue(j + kStages, next_blk);
       }
     }
+    if (timed_out) {
+      if (lane == 0) report_timeout(a.status);
+      for (int jj = j; jj < n_mine && jj < j + kStages; ++jj)
+        (void)mbar_wait_bounded(&bar[(it + jj) % kStages], ((it + jj) / kStages) & 1);
+      dead = true;
+      m_run[0] = m_run[1] = -INFINITY;
+      l_run[0] = l_run[1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) o_acc[i][0] = o_acc[i][1] = o_acc[i][2] = o_acc[i][3] = 0.0f;
+    }
+    it += n_mine;
+    l_run[0] = quad_sum(l_run[0]);
+    l_run[1] = quad_sum(l_run[1]);
+
+    __syncthreads();  // all rings are drained: their memory takes the warps' results
+    if (nan_met) nan_s = 1;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = warp * kRows + g + 8 * e;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        *reinterpret_cast<float2*>(o_s + r * D + 8 * nt + 2 * tig) = make_float2(o_acc[nt][2 * e], o_acc[nt][2 * e + 1]);
+      if (tig == 0) {
+        m_s[r] = m_run[e];
+        l_s[r] = l_run[e];
+      }
+    }
+    __syncthreads();
+    constexpr int V = D / 4;
+    const bool whole = seg.parts == 1;
+    for (int i = tid; i < rows * V; i += 128) {
+      const int r = i / V, c4 = i % V;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) M = fmaxf(M, m_s[w * kRows + r]);
+      float L = 0.0f;
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        // (a warp without a maximum has the sum 0, or NaN, which stays)
+        const float f = M == -INFINITY ? 1.0f : fast_exp2(m_s[w * kRows + r] - M);
+        const float4 x = *reinterpret_cast<const float4*>(o_s + (w * kRows + r) * D + 4 * c4);
+        L = fmaf(l_s[w * kRows + r], f, L);
+        o.x = fmaf(x.x, f, o.x);
+        o.y = fmaf(x.y, f, o.y);
+        o.z = fmaf(x.z, f, o.z);
+        o.w = fmaf(x.w, f, o.w);
+      }
+      if (whole) {
+        const float f = L == 0.0f ? 0.0f : vscale / L;
+        tree_store4<D, FMT>(a, seg, gq, row0 + r, c4, nan_s != 0, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
+      } else {
+        const long long row = static_cast<long long>(seg.slot) * kRows + r;
+        *reinterpret_cast<float4*>(a.part_o + row * D + 4 * c4) = o;
+        if (c4 == 0) *reinterpret_cast<float2*>(a.part_ml + row * 2) = make_float2(M, L);
+      }
+    }
+    if (!whole) {
+      if (tid == 0) a.part_flag[seg.slot] = nan_s;
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) last_s = atomicAdd(a.counters + seg.first_block, 1u) == static_cast<uint32_t>(seg.parts - 1);
+      __syncthreads();
+      if (last_s) {
+        __threadfence();
+        if (tid == 0) a.counters[seg.first_block] = 0u;
+        tree_merge<kRows, D, FMT>(a, seg, slice, gq, rows, vscale, merge_s);
+      }
+    }
+    __syncthreads();  // the next segment's copies overwrite what was read here
   }
-  if (tid < D) {
-    const float r = l_run == 0.0f ? 0.0f : o / l_run * a.v_scale[a.per_head ? h : 0];
-    const long long at = (static_cast<long long>(n) * a.q_heads + hq) * D + tid;
-    if (a.out_fp32) reinterpret_cast<float*>(a.out)[at] = r;
-    else reinterpret_cast<__half*>(a.out)[at] = __float2half_rn(r);
-  }
+}
+
+template <int D, int FMT, bool WIDE>
+cudaError_t launch_rows16(const TreeArgs& a, cudaStream_t s) {
+  constexpr int smem = TreeSmem<D>::BYTES;
+  auto kern = tree_rows16_kernel<D, FMT, WIDE>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  int per_sm = 0;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 128, smem);
+  if (e != cudaSuccess) return e;
+  int grid = device_sm_count() * (per_sm > 0 ? per_sm : 1);
+  if (grid > kTreeMaxBlocks) grid = kTreeMaxBlocks;
+  kern<<<grid, 128, smem, s>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s) {
-  const dim3 grid(a.n_tokens, a.q_heads);
-  switch (a.head_dim * 10 + a.fmt) {
-    case 1280: tree_simple_kernel<128, 0><<<grid, kThreads, 0, s>>>(a); break;
-    case 1281: tree_simple_kernel<128, 1><<<grid, kThreads, 0, s>>>(a); break;
-    case 640: tree_simple_kernel<64, 0><<<grid, kThreads, 0, s>>>(a); break;
-    case 641: tree_simple_kernel<64, 1><<<grid, kThreads, 0, s>>>(a); break;
+  static_assert(2 * kTreeMaxBlocks * kRows <= kTreePartRows, "partial results fit the workspace");
+  switch (a.head_dim * 100 + a.fmt * 10 + (a.out_fp32 ? 1 : 0)) {
+    case 12800: return launch_rows16<128, 0, false>(a, s);
+    case 12801: return launch_rows16<128, 0, true>(a, s);
+    case 12810: return launch_rows16<128, 1, false>(a, s);
+    case 12811: return launch_rows16<128, 1, true>(a, s);
+    case 6400: return launch_rows16<64, 0, false>(a, s);
+    case 6401: return launch_rows16<64, 0, true>(a, s);
+    case 6410: return launch_rows16<64, 1, false>(a, s);
+    case 6411: return launch_rows16<64, 1, true>(a, s);
     default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
 }
 
 }  // namespace kvq

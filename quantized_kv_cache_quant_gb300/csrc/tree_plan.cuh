@@ -1,0 +1,283 @@
+// How tree attention's work is cut, and how the pieces of one result are
+// joined; shared by its kernels.
+//
+// The query rows of request b and kv head h are its T nodes x gq query heads
+// (row r: node r / gq, head r % gq), in tiles of R rows. A (b, h, tile) is a
+// "pair"; its work is ceil((len + T) / unit) units of tokens. The units of all
+// pairs follow one another (b, then h, then tile: tiles that read the same
+// keys run next to one another and meet in L2) and are cut into equal slices,
+// one per thread block, whatever the requests' lengths. Lengths live on the
+// device, so every thread block finds its slice itself with one scan over the
+// requests. A block that holds only part of a pair leaves a partial result,
+// its first segment's in slot 2c, its last one's in 2c + 1; the last block of
+// the pair to finish joins them, always in the same order. A block begins at
+// most one pair that it does not end, so the pair's counter is that block's.
+#pragma once
+
+#include "kvq_device.cuh"
+#include "kvq_internal.h"
+#include "spec_internal.h"
+
+namespace kvq {
+
+struct TreeRequest {
+  int first, nodes, len;  // first row, rows, tokens before them
+  int units, tiles;       // per (head, tile); tiles of R rows
+};
+
+template <int R, int UNIT>
+__device__ __forceinline__ TreeRequest tree_request(const TreeArgs& a, int b) {
+  TreeRequest r;
+  const int gq = a.q_heads / a.kv_heads, cap = min(a.max_blocks * 16, a.max_seq_len);
+  r.first = min(max(a.tree_offsets[b], 0), a.n_tokens);
+  const long long rows = static_cast<long long>(a.tree_offsets[b + 1]) - r.first;
+  r.nodes = static_cast<int>(min(max(rows, 0ll), static_cast<long long>(min(min(a.max_tree, cap), a.n_tokens - r.first))));
+  r.len = min(max(a.seq_lens[b], 0), cap - r.nodes);
+  r.tiles = (r.nodes * gq + R - 1) / R;
+  r.units = r.nodes > 0 ? (r.len + r.nodes + UNIT - 1) / UNIT : 0;
+  return r;
+}
+
+struct TreeSlice {
+  long long total;   // units of all pairs
+  int blocks;        // slices that share them
+  long long begin, end;
+  int b;             // request of the first unit
+  long long before;  // units of the requests before b
+
+  __device__ __forceinline__ long long start_of(int c) const { return static_cast<long long>(c) * total / blocks; }
+  __device__ __forceinline__ int block_of(long long u) const { return static_cast<int>(((u + 1) * blocks - 1) / total); }
+};
+
+// The slice of thread block blockIdx.x. sm: 32 + 2 words of 8 bytes of shared
+// memory that nothing else uses until the next __syncthreads after the call.
+// min_units: slices get at least about so many units.
+template <int R, int UNIT>
+__device__ __forceinline__ TreeSlice tree_slice(const TreeArgs& a, unsigned long long* sm, int min_units) {
+  TreeSlice s;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  auto units_of = [&](int b) -> unsigned long long {
+    if (b >= a.batch) return 0ull;
+    const TreeRequest r = tree_request<R, UNIT>(a, b);
+    return static_cast<unsigned long long>(r.units) * r.tiles * a.kv_heads;
+  };
+  // one chunk of blockDim.x requests: exclusive prefix of v, the chunk's sum in `sum`
+  auto scan = [&](unsigned long long v, unsigned long long& sum) -> unsigned long long {
+    unsigned long long inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    if (lane == 31) sm[warp] = inc;
+    __syncthreads();
+    unsigned long long w = lane < warps ? sm[lane] : 0ull, before = 0ull;
+    sum = 0ull;
+    for (int i = 0; i < warps; ++i) {
+      const unsigned long long x = __shfl_sync(0xffffffffu, w, i);
+      if (i < warp) before += x;
+      sum += x;
+    }
+    __syncthreads();
+    return before + inc - v;
+  };
+  const unsigned long long mine = units_of(threadIdx.x);
+  unsigned long long sum;
+  const unsigned long long mine_at = scan(mine, sum);
+  unsigned long long total = sum;
+  for (int b0 = blockDim.x; b0 < a.batch; b0 += blockDim.x) {
+    (void)scan(units_of(b0 + threadIdx.x), sum);
+    total += sum;
+  }
+  s.total = static_cast<long long>(total);
+  s.blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), (s.total + min_units - 1) / min_units));
+  s.begin = s.end = s.before = 0;
+  s.b = 0;
+  if (static_cast<int>(blockIdx.x) >= s.blocks) return s;
+  s.begin = s.start_of(blockIdx.x);
+  s.end = s.start_of(blockIdx.x + 1);
+  const unsigned long long u = static_cast<unsigned long long>(s.begin);
+  auto claim = [&](int b, unsigned long long at, unsigned long long n) {
+    if (at <= u && u < at + n) {
+      sm[32] = static_cast<unsigned long long>(b);
+      sm[33] = at;
+    }
+  };
+  claim(threadIdx.x, mine_at, mine);
+  unsigned long long carry = 0;
+  if (a.batch > static_cast<int>(blockDim.x)) {
+    (void)scan(mine, carry);
+    for (int b0 = blockDim.x; b0 < a.batch; b0 += blockDim.x) {
+      const unsigned long long n = units_of(b0 + threadIdx.x);
+      const unsigned long long at = carry + scan(n, sum);
+      claim(b0 + threadIdx.x, at, n);
+      carry += sum;
+    }
+  }
+  __syncthreads();
+  s.b = static_cast<int>(sm[32]);
+  s.before = static_cast<long long>(sm[33]);
+  __syncthreads();
+  return s;
+}
+
+// One pair's share of a slice.
+struct TreeSegment {
+  int b, h, tile;
+  TreeRequest r;
+  long long pair_begin;    // the pair's first unit in the range of all
+  int u0, u1;              // units of the pair in this slice
+  int slot;                // 2 * block (+ 1): where a partial result goes
+  int first_block, parts;  // blocks that share the pair: first_block .. first_block + parts - 1
+};
+
+// Walks a slice's segments: `at` is the unit to go on from, b / before its request.
+template <int R, int UNIT>
+__device__ __forceinline__ bool next_segment(const TreeArgs& a, const TreeSlice& s, long long& at, int& b,
+                                             long long& before, TreeSegment& g) {
+  if (at >= s.end) return false;
+  g.r = tree_request<R, UNIT>(a, b);
+  long long n = static_cast<long long>(g.r.units) * g.r.tiles * a.kv_heads;
+  while (at >= before + n) {  // requests without nodes have no units
+    before += n;
+    ++b;
+    g.r = tree_request<R, UNIT>(a, b);
+    n = static_cast<long long>(g.r.units) * g.r.tiles * a.kv_heads;
+  }
+  const int pair = static_cast<int>((at - before) / g.r.units);
+  g.b = b;
+  g.h = pair / g.r.tiles;
+  g.tile = pair % g.r.tiles;
+  g.pair_begin = before + static_cast<long long>(pair) * g.r.units;
+  g.u0 = static_cast<int>(at - g.pair_begin);
+  g.u1 = static_cast<int>(min(s.end - g.pair_begin, static_cast<long long>(g.r.units)));
+  g.slot = 2 * static_cast<int>(blockIdx.x) + (at == s.begin ? 0 : 1);
+  g.first_block = s.block_of(g.pair_begin);
+  g.parts = s.block_of(g.pair_begin + g.r.units - 1) - g.first_block + 1;
+  at = g.pair_begin + g.u1;
+  return true;
+}
+
+// Whether node `node`'s mask (row of words) lets it see the token at `tok`:
+// every one before the tree, nodes by their bits, none behind the last node.
+__device__ __forceinline__ bool tree_sees(const uint64_t* mask, int tok, int len, int total) {
+  if (tok < len) return true;
+  if (tok >= total) return false;
+  const int j = tok - len;
+  return (mask[j >> 6] >> (j & 63)) & 1;
+}
+
+// Bytes of four FP8 codes that are NaN (or an E5M2 infinity, which no cast of this library writes): 0xFF each.
+template <int FMT>
+__device__ __forceinline__ uint32_t fp8_nonfinite(uint32_t w) {
+  const uint32_t mag = w & 0x7F7F7F7Fu;
+  return FMT == 0 ? __vcmpeq4(mag, 0x7F7F7F7Fu) : __vcmpgeu4(mag, 0x7C7C7C7Cu);
+}
+
+// Whether a value row that row `row`'s node sees holds a NaN at channel c. The
+// products take such codes of the tree's own tokens as 0 (a weight of 0 times
+// NaN would reach rows that do not see the token); where any was met, this
+// puts the NaN back into the rows that do see it.
+template <int D, int FMT>
+__device__ __noinline__ bool tree_meets_nan(const TreeArgs& a, const TreeSegment& g, int gq, int row, int c) {
+  const uint64_t* mask = a.tree_mask + static_cast<long long>(g.r.first + row / gq) * a.mask_words;
+  for (int j = 0; j < g.r.nodes; ++j) {
+    if (!((mask[j >> 6] >> (j & 63)) & 1)) continue;
+    const int tok = g.r.len + j, t = tok % 16;
+    const int blk = min(max(a.block_table[static_cast<long long>(g.b) * a.max_blocks + tok / 16], 0), a.num_blocks - 1);
+    const uint8_t* vb = a.v_pool + (static_cast<long long>(blk) * a.kv_heads + g.h) * (16 * D);
+    if (fp8_nonfinite<FMT>(vb[(c / 32 * 32 + 4 * (c % 8) + t % 8 / 2) * 16 + c % 32 / 8 * 4 + t / 8 * 2 + t % 2]) & 0xFFu)
+      return true;
+  }
+  return false;
+}
+
+// Output channels 4 c4 .. +3 of a pair's row.
+template <int D, int FMT>
+__device__ __forceinline__ void tree_store4(const TreeArgs& a, const TreeSegment& g, int gq, int row, int c4, bool nan_met,
+                                            float4 v) {
+  if (nan_met) {
+    float* e = &v.x;
+    for (int i = 0; i < 4; ++i)
+      if (tree_meets_nan<D, FMT>(a, g, gq, row, 4 * c4 + i)) e[i] = NAN;
+  }
+  const long long at = (static_cast<long long>(g.r.first + row / gq) * a.q_heads + g.h * gq + row % gq) * D + 4 * c4;
+  if (a.out_fp32)
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = v;
+  else
+    *reinterpret_cast<uint2*>(reinterpret_cast<__half*>(a.out) + at) = make_uint2(pack_rn_f16x2(v.x, v.y), pack_rn_f16x2(v.z, v.w));
+}
+
+// Join the `parts` partial results of a pair (rows [0, rows) of its tile), whole
+// thread block. Partial of slot s: o at part_o + s * R * D, (m, l) of row r at
+// part_ml + (s * R + r) * 2, flag at part_flag[s]. sm: 2 * R floats of shared
+// memory.
+template <int R, int D, int FMT>
+__device__ __forceinline__ void tree_merge(const TreeArgs& a, const TreeSegment& g, const TreeSlice& s, int gq, int rows,
+                                           float v_scale, float* sm) {
+  float* m_s = sm;
+  float* inv = sm + R;
+  __shared__ int flag_s;
+  const int tid = threadIdx.x;
+  auto slot_of = [&](int i) -> long long {
+    const int c = g.first_block + i;
+    return 2ll * c + ((i == 0 && s.start_of(c) != g.pair_begin) ? 1 : 0);
+  };
+  if (tid == 0) flag_s = 0;
+  __syncthreads();
+  for (int r = tid; r < rows; r += blockDim.x) {
+    float m = -INFINITY, l = 0.0f;
+    for (int i = 0; i < g.parts; ++i) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot_of(i) * R + r);
+      const float mn = fmaxf(m, ml.x);
+      // (a part without a maximum has the sum 0, or NaN, which stays)
+      l = mn == -INFINITY ? l + ml.y : l * fast_exp2(m - mn) + ml.y * fast_exp2(ml.x - mn);
+      m = mn;
+    }
+    m_s[r] = m;
+    inv[r] = l == 0.0f ? 0.0f : v_scale / l;
+  }
+  for (int i = tid; i < g.parts; i += blockDim.x)
+    if (__ldcg(a.part_flag + slot_of(i))) flag_s = 1;
+  __syncthreads();
+  constexpr int V = D / 4;  // float4 columns
+  constexpr int kRowsAtOnce = 4;
+  const int c4 = tid % V, r_step = blockDim.x / V;
+  for (int r0 = tid / V; r0 < rows; r0 += r_step * kRowsAtOnce) {
+    float4 acc[kRowsAtOnce];
+    float m[kRowsAtOnce];
+#pragma unroll
+    for (int k = 0; k < kRowsAtOnce; ++k) {
+      acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      m[k] = r0 + k * r_step < rows ? m_s[r0 + k * r_step] : -INFINITY;
+    }
+#pragma unroll 2
+    for (int i = 0; i < g.parts; ++i) {
+      const long long base = slot_of(i) * R;
+#pragma unroll
+      for (int k = 0; k < kRowsAtOnce; ++k) {
+        const int r = r0 + k * r_step;
+        if (r < rows) {
+          const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + (base + r) * D) + c4);
+          const float pm = __ldcg(a.part_ml + (base + r) * 2);
+          const float w = m[k] == -INFINITY ? 0.0f : fast_exp2(pm - m[k]);
+          acc[k].x = fmaf(o.x, w, acc[k].x);
+          acc[k].y = fmaf(o.y, w, acc[k].y);
+          acc[k].z = fmaf(o.z, w, acc[k].z);
+          acc[k].w = fmaf(o.w, w, acc[k].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRowsAtOnce; ++k) {
+      const int r = r0 + k * r_step;
+      if (r < rows) {
+        const float f = inv[r];
+        tree_store4<D, FMT>(a, g, gq, g.tile * R + r, c4, flag_s != 0,
+                            make_float4(acc[k].x * f, acc[k].y * f, acc[k].z * f, acc[k].w * f));
+      }
+    }
+  }
+}
+
+}  // namespace kvq
