@@ -87,5 +87,7 @@ struct TreeArgs {
 constexpr int kTreeMaxBlocks = 1024;
 constexpr int kTreePartRows = 81920;
 cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s);
+// The same on tcgen05: 128 or 256 query rows a tile.
+cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t s);
 
 }  // namespace kvq

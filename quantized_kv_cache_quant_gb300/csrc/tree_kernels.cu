@@ -27,7 +27,7 @@ struct TreeSmem {
   static constexpr int BAR_BYTES = 128;
   static constexpr int STAGE = 2 * kBlock * D;
   static constexpr int RING = 4 * kStages * STAGE;
-  static constexpr int COMBINE = (4 * kRows * (D + 2) + 2 * kRows) * 4;
+  static constexpr int COMBINE = (4 * kRows * (D + 2) + 2 * kRows + 1) * 4;
   static constexpr int AREA = RING > COMBINE ? RING : COMBINE;
   static constexpr int BYTES = BAR_BYTES + AREA;
 };
@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(128) tree_rows16_kernel(TreeArgs a) {
   float* o_s = reinterpret_cast<float*>(area);   // [4][16][D]
   float* m_s = o_s + 4 * kRows * D;              // [4][16]
   float* l_s = m_s + 4 * kRows;                  // [4][16]
-  float* merge_s = l_s + 4 * kRows;              // [2][16]
+  float* merge_s = l_s + 4 * kRows;              // [2][16] and a flag
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
   const int gq = a.q_heads / a.kv_heads;
@@ -273,7 +273,8 @@ __global__ void __launch_bounds__(128) tree_rows16_kernel(TreeArgs a) {
       }
       if (whole) {
         const float f = L == 0.0f ? 0.0f : vscale / L;
-        tree_store4<D, FMT>(a, seg, gq, row0 + r, c4, nan_s != 0, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
+        tree_store4<D>(a, seg, gq, row0 + r, c4, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
+        if (nan_s) tree_put_nan<D, FMT>(a, seg, gq, row0 + r, 4 * c4, 4 * c4 + 4);
       } else {
         const long long row = static_cast<long long>(seg.slot) * kRows + r;
         *reinterpret_cast<float4*>(a.part_o + row * D + 4 * c4) = o;
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(128) tree_rows16_kernel(TreeArgs a) {
       if (last_s) {
         __threadfence();
         if (tid == 0) a.counters[seg.first_block] = 0u;
-        tree_merge<kRows, D, FMT>(a, seg, slice, gq, rows, vscale, merge_s);
+        tree_merge<kRows, D, FMT>(a, seg, slice, gq, rows, vscale, merge_s, tid, 128, [] { __syncthreads(); });
       }
     }
     __syncthreads();  // the next segment's copies overwrite what was read here
@@ -314,6 +315,7 @@ cudaError_t launch_rows16(const TreeArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s) {
+  if (a.max_tree * (a.q_heads / a.kv_heads) > kRows) return launch_tree_tc(a, s);
   static_assert(2 * kTreeMaxBlocks * kRows <= kTreePartRows, "partial results fit the workspace");
   switch (a.head_dim * 100 + a.fmt * 10 + (a.out_fp32 ? 1 : 0)) {
     case 12800: return launch_rows16<128, 0, false>(a, s);

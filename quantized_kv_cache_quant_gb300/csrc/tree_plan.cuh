@@ -174,33 +174,9 @@ __device__ __forceinline__ uint32_t fp8_nonfinite(uint32_t w) {
   return FMT == 0 ? __vcmpeq4(mag, 0x7F7F7F7Fu) : __vcmpgeu4(mag, 0x7C7C7C7Cu);
 }
 
-// Whether a value row that row `row`'s node sees holds a NaN at channel c. The
-// products take such codes of the tree's own tokens as 0 (a weight of 0 times
-// NaN would reach rows that do not see the token); where any was met, this
-// puts the NaN back into the rows that do see it.
-template <int D, int FMT>
-__device__ __noinline__ bool tree_meets_nan(const TreeArgs& a, const TreeSegment& g, int gq, int row, int c) {
-  const uint64_t* mask = a.tree_mask + static_cast<long long>(g.r.first + row / gq) * a.mask_words;
-  for (int j = 0; j < g.r.nodes; ++j) {
-    if (!((mask[j >> 6] >> (j & 63)) & 1)) continue;
-    const int tok = g.r.len + j, t = tok % 16;
-    const int blk = min(max(a.block_table[static_cast<long long>(g.b) * a.max_blocks + tok / 16], 0), a.num_blocks - 1);
-    const uint8_t* vb = a.v_pool + (static_cast<long long>(blk) * a.kv_heads + g.h) * (16 * D);
-    if (fp8_nonfinite<FMT>(vb[(c / 32 * 32 + 4 * (c % 8) + t % 8 / 2) * 16 + c % 32 / 8 * 4 + t / 8 * 2 + t % 2]) & 0xFFu)
-      return true;
-  }
-  return false;
-}
-
 // Output channels 4 c4 .. +3 of a pair's row.
-template <int D, int FMT>
-__device__ __forceinline__ void tree_store4(const TreeArgs& a, const TreeSegment& g, int gq, int row, int c4, bool nan_met,
-                                            float4 v) {
-  if (nan_met) {
-    float* e = &v.x;
-    for (int i = 0; i < 4; ++i)
-      if (tree_meets_nan<D, FMT>(a, g, gq, row, 4 * c4 + i)) e[i] = NAN;
-  }
+template <int D>
+__device__ __forceinline__ void tree_store4(const TreeArgs& a, const TreeSegment& g, int gq, int row, int c4, float4 v) {
   const long long at = (static_cast<long long>(g.r.first + row / gq) * a.q_heads + g.h * gq + row % gq) * D + 4 * c4;
   if (a.out_fp32)
     *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = v;
@@ -208,24 +184,49 @@ __device__ __forceinline__ void tree_store4(const TreeArgs& a, const TreeSegment
     *reinterpret_cast<uint2*>(reinterpret_cast<__half*>(a.out) + at) = make_uint2(pack_rn_f16x2(v.x, v.y), pack_rn_f16x2(v.z, v.w));
 }
 
-// Join the `parts` partial results of a pair (rows [0, rows) of its tile), whole
-// thread block. Partial of slot s: o at part_o + s * R * D, (m, l) of row r at
-// part_ml + (s * R + r) * 2, flag at part_flag[s]. sm: 2 * R floats of shared
-// memory.
-template <int R, int D, int FMT>
+// The products take NaN codes of the tree's own value rows as 0 (a weight of 0
+// times NaN would reach rows that do not see the token). Where any was met,
+// this puts NaN into channels [c0, c1) of row `row` that such a code reaches
+// through a node the row sees; by the thread that stored them.
+template <int D, int FMT>
+__device__ __forceinline__ void tree_put_nan(const TreeArgs& a, const TreeSegment& g, int gq, int row, int c0, int c1) {
+  const int n = g.r.first + row / gq;
+  const uint64_t* mask = a.tree_mask + static_cast<long long>(n) * a.mask_words;
+  const long long at = (static_cast<long long>(n) * a.q_heads + g.h * gq + row % gq) * D;
+#pragma unroll 1
+  for (int j = 0; j < g.r.nodes; ++j) {
+    if (!((mask[j >> 6] >> (j & 63)) & 1)) continue;
+    const int tok = g.r.len + j, t = tok % 16;
+    const int blk = min(max(a.block_table[static_cast<long long>(g.b) * a.max_blocks + tok / 16], 0), a.num_blocks - 1);
+    const uint8_t* vb = a.v_pool + (static_cast<long long>(blk) * a.kv_heads + g.h) * (16 * D);
+#pragma unroll 1
+    for (int c = c0; c < c1; ++c) {
+      const uint32_t code = vb[(c / 32 * 32 + 4 * (c % 8) + t % 8 / 2) * 16 + c % 32 / 8 * 4 + t / 8 * 2 + t % 2];
+      if (fp8_nonfinite<FMT>(code) & 0xFFu) {
+        if (a.out_fp32) reinterpret_cast<float*>(a.out)[at + c] = NAN;
+        else reinterpret_cast<uint16_t*>(a.out)[at + c] = 0x7FFFu;
+      }
+    }
+  }
+}
+
+// Join the `parts` partial results of a pair (rows [0, rows) of its tile) by
+// `threads` threads that `sync` brings together, `tid` of them this one.
+// Partial of slot s: o at part_o + s * R * D, (m, l) of row r at part_ml + (s *
+// R + r) * 2, flag at part_flag[s]. sm: 2 * R + 1 words of shared memory.
+template <int R, int D, int FMT, class Sync>
 __device__ __forceinline__ void tree_merge(const TreeArgs& a, const TreeSegment& g, const TreeSlice& s, int gq, int rows,
-                                           float v_scale, float* sm) {
+                                           float v_scale, float* sm, int tid, int threads, Sync sync) {
   float* m_s = sm;
   float* inv = sm + R;
-  __shared__ int flag_s;
-  const int tid = threadIdx.x;
+  int& flag_s = *reinterpret_cast<int*>(sm + 2 * R);
   auto slot_of = [&](int i) -> long long {
     const int c = g.first_block + i;
     return 2ll * c + ((i == 0 && s.start_of(c) != g.pair_begin) ? 1 : 0);
   };
   if (tid == 0) flag_s = 0;
-  __syncthreads();
-  for (int r = tid; r < rows; r += blockDim.x) {
+  sync();
+  for (int r = tid; r < rows; r += threads) {
     float m = -INFINITY, l = 0.0f;
     for (int i = 0; i < g.parts; ++i) {
       const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot_of(i) * R + r);
@@ -237,12 +238,12 @@ __device__ __forceinline__ void tree_merge(const TreeArgs& a, const TreeSegment&
     m_s[r] = m;
     inv[r] = l == 0.0f ? 0.0f : v_scale / l;
   }
-  for (int i = tid; i < g.parts; i += blockDim.x)
+  for (int i = tid; i < g.parts; i += threads)
     if (__ldcg(a.part_flag + slot_of(i))) flag_s = 1;
-  __syncthreads();
+  sync();
   constexpr int V = D / 4;  // float4 columns
   constexpr int kRowsAtOnce = 4;
-  const int c4 = tid % V, r_step = blockDim.x / V;
+  const int c4 = tid % V, r_step = threads / V;
   for (int r0 = tid / V; r0 < rows; r0 += r_step * kRowsAtOnce) {
     float4 acc[kRowsAtOnce];
     float m[kRowsAtOnce];
@@ -273,9 +274,13 @@ __device__ __forceinline__ void tree_merge(const TreeArgs& a, const TreeSegment&
       const int r = r0 + k * r_step;
       if (r < rows) {
         const float f = inv[r];
-        tree_store4<D, FMT>(a, g, gq, g.tile * R + r, c4, flag_s != 0,
-                            make_float4(acc[k].x * f, acc[k].y * f, acc[k].z * f, acc[k].w * f));
+        tree_store4<D>(a, g, gq, g.tile * R + r, c4, make_float4(acc[k].x * f, acc[k].y * f, acc[k].z * f, acc[k].w * f));
       }
+    }
+    if (flag_s) {
+#pragma unroll 1
+      for (int r = r0; r < min(rows, r0 + kRowsAtOnce * r_step); r += r_step)
+        tree_put_nan<D, FMT>(a, g, gq, g.tile * R + r, 4 * c4, 4 * c4 + 4);
     }
   }
 }
