@@ -26,11 +26,12 @@ kvq_status check_pool(const fp8_pool* p) {
   return KVQ_OK;
 }
 
-// Tree attention workspace: [status word | 256 B][counters][flags of the
+// Tree attention workspace: [status word | 256 B][what to join][flags of the
 // partial results][(m, l) of their rows][o of their rows].
-constexpr size_t kTreeCounters = kvq::kWsHeader;
-constexpr size_t kTreeFlags = kTreeCounters + kvq::kTreeMaxBlocks * sizeof(uint32_t);
+constexpr size_t kTreeJoins = kvq::kWsHeader;
+constexpr size_t kTreeFlags = kTreeJoins + kvq::kTreeMaxBlocks * sizeof(kvq::TreeJoin);
 constexpr size_t kTreePartials = kTreeFlags + 2 * kvq::kTreeMaxBlocks * sizeof(int);
+static_assert(kTreePartials % 256 == 0, "the partial results are read as 16-byte vectors");
 
 // A key pool and a value pool that belong together.
 kvq_status check_pools(const fp8_pool* k, const fp8_pool* v) {
@@ -213,7 +214,7 @@ kvq_status fp8_tree_attention(const uint16_t* q, int64_t q_row_stride, int32_t n
   a.out_fp32 = out_fp32;
   uint8_t* const base = static_cast<uint8_t*>(ws);
   a.status = reinterpret_cast<uint32_t*>(base);
-  a.counters = reinterpret_cast<uint32_t*>(base + kTreeCounters);
+  a.joins = reinterpret_cast<kvq::TreeJoin*>(base + kTreeJoins);
   a.part_flag = reinterpret_cast<int*>(base + kTreeFlags);
   a.part_ml = reinterpret_cast<float*>(base + kTreePartials);
   a.part_o = a.part_ml + static_cast<size_t>(kvq::kTreePartRows) * 2;

@@ -418,8 +418,8 @@ __global__ void __launch_bounds__(512) fp8_accept_kernel(Fp8AcceptArgs a) {
 
 cudaError_t launch_blocks_resize(const BlocksResizeArgs& a, cudaStream_t s) {
   const int smem = 4 * a.batch * static_cast<int>(sizeof(int));
-  cudaError_t e = cudaFuncSetAttribute(blocks_resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       4 * kSpecMaxBatch * static_cast<int>(sizeof(int)));
+  static SharedMemoryOnce once;
+  cudaError_t e = once.set(blocks_resize_kernel, 4 * kSpecMaxBatch * static_cast<int>(sizeof(int)));
   if (e != cudaSuccess) return e;
   const bool small = static_cast<long long>(a.batch) * a.max_blocks <= 16384;
   cudaLaunchConfig_t cfg{};

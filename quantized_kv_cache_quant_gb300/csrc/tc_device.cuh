@@ -100,6 +100,15 @@ __device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint32_t a_tmem, uin
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accum)
       : "memory");
 }
+// The same with A from shared memory.
+__device__ __forceinline__ void tc_mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accum)
+      : "memory");
+}
 // One arrival on `bar` once every tcgen05.mma this thread issued before has completed.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
@@ -109,25 +118,83 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
 // Generic-proxy writes to shared memory become visible to bulk copies and MMAs.
 __device__ __forceinline__ void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+// True in one thread of a converged warp. A branch on it tells the compiler
+// that one thread runs what follows, which then keeps MMA operands in uniform
+// registers: with a branch on the lane number each MMA took 57 clocks to issue
+// (128 x 64 x 16 needs 32), with this one 32.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
 }
+
+// One arrival of the lanes where `on` holds. Predicated, not branched around: a
+// warp that a branch has split runs what follows twice, its next wait too.
+__device__ __forceinline__ void mbar_arrive_if(uint64_t* bar, bool on) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(
+                   smem_addr(bar)),
+               "r"(static_cast<uint32_t>(on))
+               : "memory");
+}
+
+// Whether phase `parity` has completed, without waiting (mbar_try_wait may
+// suspend the thread until it has).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+constexpr long long kRoleWaitClocks = 4000000000ll;  // about 2 s
 
 // Wait of a role of a thread block: false once any wait of the block has run
 // out (*dead set, the status word too), so that no role waits out its own
-// second after another has.
+// limit after another has. role_wait: one thread; role_wait_warp: a converged
+// warp, which stays so (the answer is the whole warp's, so no branch splits it).
 __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, volatile int* dead, uint32_t* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = global_ns();
-  while (true) {
+  long long t0 = 0;
+#pragma unroll 1
+  for (unsigned i = 0;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if (*dead) return false;
-    if (global_ns() - t0 > kWaitLimitNs) {
-      *dead = 1;
-      report_timeout(status);
-      return false;
+    if ((i & 255) == 255) {
+      if (t0 == 0) t0 = clock64();
+      if (*dead) return false;
+      if (clock64() - t0 > kRoleWaitClocks) {
+        *dead = 1;
+        report_timeout(status);
+        return false;
+      }
     }
   }
+}
+__device__ __forceinline__ bool role_wait_warp(uint64_t* bar, uint32_t parity, volatile int* dead, uint32_t* status) {
+  long long t0 = 0;
+#pragma unroll 1
+  for (unsigned i = 0;; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((i & 255) == 255) {
+      if (t0 == 0) t0 = clock64();
+      const bool late = clock64() - t0 > kRoleWaitClocks;
+      if (late && !*dead) {
+        *dead = 1;
+        report_timeout(status);
+      }
+      if (__any_sync(0xffffffffu, late || *dead)) return false;
+    }
+  }
+}
+
+// Maximum of three.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 __device__ __forceinline__ void named_barrier(int id, int threads) {

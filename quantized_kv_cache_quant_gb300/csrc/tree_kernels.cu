@@ -27,24 +27,27 @@ struct TreeSmem {
   static constexpr int BAR_BYTES = 128;
   static constexpr int STAGE = 2 * kBlock * D;
   static constexpr int RING = 4 * kStages * STAGE;
-  static constexpr int COMBINE = (4 * kRows * (D + 2) + 2 * kRows + 1) * 4;
+  static constexpr int COMBINE = 4 * kRows * (D + 2) * 4;
   static constexpr int AREA = RING > COMBINE ? RING : COMBINE;
   static constexpr int BYTES = BAR_BYTES + AREA;
 };
 
 template <int D, int FMT, bool WIDE>
-__global__ void __launch_bounds__(128) tree_rows16_kernel(TreeArgs a) {
+__global__ void __launch_bounds__(128) tree_rows16_kernel(const __grid_constant__ TreeArgs a) {
   using S = TreeSmem<D>;
   constexpr int KS = D / 16, NT = D / 8, CH = D / 32;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ unsigned long long plan_s[34];
-  __shared__ int nan_s, last_s;
+  __shared__ int nan_s;
+  // the arguments and the slice, for functions out of line (a reference to a kernel's parameters is read from global
+  // memory there)
+  __shared__ TreeArgs args_s;
+  __shared__ TreeSlice slice_s;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
   uint8_t* area = smem + S::BAR_BYTES;
   float* o_s = reinterpret_cast<float*>(area);   // [4][16][D]
   float* m_s = o_s + 4 * kRows * D;              // [4][16]
   float* l_s = m_s + 4 * kRows;                  // [4][16]
-  float* merge_s = l_s + 4 * kRows;              // [2][16] and a flag
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
   const int gq = a.q_heads / a.kv_heads;
@@ -55,15 +58,23 @@ __global__ void __launch_bounds__(128) tree_rows16_kernel(TreeArgs a) {
     for (int s = 0; s < kStages; ++s) mbar_init(&bar[s], 1);
     fence_mbar_init();
   }
+  if (tid == 0) tree_leave_none(a);
   const TreeSlice slice = tree_slice<kRows, kUnit>(a, plan_s, 2);
   if (static_cast<int>(blockIdx.x) >= slice.blocks) return;
 
-  long long at = slice.begin, before = slice.before;
-  int b = slice.b;
+  if (tid == 0) {
+    args_s = a;
+    slice_s = slice;
+  }
+  __syncthreads();
+  TreeWalk walk;
+  walk.at = slice.begin;
+  walk.before = slice.before;
+  walk.b = slice.b;
+  const TreeSegment& seg = walk.seg;
   unsigned it = 0;         // blocks this warp has taken through its ring
   bool dead = false;       // a wait ran out: no more copies
-  TreeSegment seg;
-  while (next_segment<kRows, kUnit>(a, slice, at, b, before, seg)) {
+  while (next_segment<kRows, kUnit>(args_s, slice_s, walk)) {
     const int h = seg.h, len = seg.r.len, total = len + seg.r.nodes, row0 = seg.tile * kRows;
     const int rows = min(kRows, seg.r.nodes * gq - row0);
     const int nblk = (total + kBlock - 1) / kBlock;
@@ -274,24 +285,16 @@ __global__ void __launch_bounds__(128) tree_rows16_kernel(TreeArgs a) {
       if (whole) {
         const float f = L == 0.0f ? 0.0f : vscale / L;
         tree_store4<D>(a, seg, gq, row0 + r, c4, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
-        if (nan_s) tree_put_nan<D, FMT>(a, seg, gq, row0 + r, 4 * c4, 4 * c4 + 4);
+        if (nan_s) tree_put_nan<D, FMT>(args_s, seg.b, h, seg.r.first, seg.r.nodes, len, row0 + r, 4 * c4, 4 * c4 + 4);
       } else {
         const long long row = static_cast<long long>(seg.slot) * kRows + r;
         *reinterpret_cast<float4*>(a.part_o + row * D + 4 * c4) = o;
         if (c4 == 0) *reinterpret_cast<float2*>(a.part_ml + row * 2) = make_float2(M, L);
       }
     }
-    if (!whole) {
-      if (tid == 0) a.part_flag[seg.slot] = nan_s;
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) last_s = atomicAdd(a.counters + seg.first_block, 1u) == static_cast<uint32_t>(seg.parts - 1);
-      __syncthreads();
-      if (last_s) {
-        __threadfence();
-        if (tid == 0) a.counters[seg.first_block] = 0u;
-        tree_merge<kRows, D, FMT>(a, seg, slice, gq, rows, vscale, merge_s, tid, 128, [] { __syncthreads(); });
-      }
+    if (!whole && tid == 0) {
+      a.part_flag[seg.slot] = nan_s;
+      if (seg.u0 == 0) tree_leave_join(args_s, seg, rows, row0);
     }
     __syncthreads();  // the next segment's copies overwrite what was read here
   }
@@ -301,18 +304,120 @@ template <int D, int FMT, bool WIDE>
 cudaError_t launch_rows16(const TreeArgs& a, cudaStream_t s) {
   constexpr int smem = TreeSmem<D>::BYTES;
   auto kern = tree_rows16_kernel<D, FMT, WIDE>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  static SharedMemoryOnce once;
   int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 128, smem);
+  cudaError_t e = once.set(kern, smem, 128, &per_sm);
   if (e != cudaSuccess) return e;
-  int grid = device_sm_count() * (per_sm > 0 ? per_sm : 1);
+  int grid = device_sm_count() * per_sm;
   if (grid > kTreeMaxBlocks) grid = kTreeMaxBlocks;
   kern<<<grid, 128, smem, s>>>(a);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_tree_join(a, grid, kRows, s);
+}
+
+// ---------------------------------------------------------------------------
+// Joining of partial results: block (c, y) takes what block c of the attention
+// left, rows 32 y .. +31, a warp four of them. Lanes weigh a row's parts (log2
+// units), then the rows' outputs are added up part by part, all four rows and
+// two parts in flight.
+// ---------------------------------------------------------------------------
+template <int D, int FMT>
+__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeArgs a, int tile_rows) {
+  constexpr int V = D / 32;  // floats of a row a lane holds
+  constexpr int kJoinRows = 4;
+  const TreeJoin j = a.joins[blockIdx.x];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r0 = 32 * blockIdx.y + kJoinRows * warp;
+  if (j.parts == 0 || r0 >= j.rows) return;
+  const int gq = a.q_heads / a.kv_heads;
+  const float v_scale = a.v_scale[a.per_head ? j.h : 0];
+  auto slot_of = [&](int i) { return i == 0 ? j.slot0 : (j.slot0 & ~1) + 2 * i; };
+  // (a part without a maximum has the sum 0, or NaN, which stays)
+  float M[kJoinRows], L[kJoinRows], w[kJoinRows], acc[kJoinRows][V];
+#pragma unroll
+  for (int k = 0; k < kJoinRows; ++k) {
+    M[k] = -INFINITY;
+    L[k] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[k][e] = 0.0f;
+  }
+  bool nan_met = false;
+  for (int i0 = 0; i0 < j.parts; i0 += 32) {
+    const int i = i0 + lane, n = min(32, j.parts - i0);
+    float2 ml[kJoinRows];
+#pragma unroll
+    for (int k = 0; k < kJoinRows; ++k) {  // (rows behind the last one are within the slot: tiles hold a multiple of 4)
+      ml[k] = make_float2(-INFINITY, 0.0f);
+      if (i < j.parts)
+        ml[k] = reinterpret_cast<const float2*>(a.part_ml)[static_cast<long long>(slot_of(i)) * tile_rows + r0 + k];
+    }
+    if (i < j.parts) nan_met |= a.part_flag[slot_of(i)] != 0;
+#pragma unroll
+    for (int k = 0; k < kJoinRows; ++k) {
+      const float Mn = fmaxf(M[k], warp_max(ml[k].x));
+      const float old = Mn == -INFINITY ? 1.0f : fast_exp2(M[k] - Mn);
+      w[k] = Mn == -INFINITY ? 1.0f : fast_exp2(ml[k].x - Mn);
+      L[k] = L[k] * old + warp_sum(ml[k].y * w[k]);
+      M[k] = Mn;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[k][e] *= old;
+    }
+#pragma unroll 2
+    for (int p = 0; p < n; ++p) {
+      const float* o = a.part_o + (static_cast<long long>(slot_of(i0 + p)) * tile_rows + r0) * D + V * lane;
+      float v[kJoinRows][V];
+#pragma unroll
+      for (int k = 0; k < kJoinRows; ++k) {
+        if constexpr (V == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(o + k * D);
+          v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(o + k * D);
+          v[k][0] = x.x, v[k][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kJoinRows; ++k) {
+        const float wp = __shfl_sync(0xffffffffu, w[k], p);
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[k][e] = fmaf(v[k][e], wp, acc[k][e]);
+      }
+    }
+  }
+  nan_met = __any_sync(0xffffffffu, nan_met);
+#pragma unroll
+  for (int k = 0; k < kJoinRows; ++k) {
+    if (r0 + k < j.rows) {
+      const float f = L[k] == 0.0f ? 0.0f : v_scale / L[k];
+      const int row = j.row0 + r0 + k, node = row / gq;
+      const long long at = (static_cast<long long>(j.first + node) * a.q_heads + j.h * gq + (row - node * gq)) * D + V * lane;
+#pragma unroll
+      for (int e = 0; e < V; e += 2) {
+        if (a.out_fp32)
+          *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + at + e) = make_float2(acc[k][e] * f, acc[k][e + 1] * f);
+        else
+          *reinterpret_cast<uint32_t*>(reinterpret_cast<__half*>(a.out) + at + e) = pack_rn_f16x2(acc[k][e] * f, acc[k][e + 1] * f);
+      }
+      if (nan_met) tree_put_nan<D, FMT>(a, j.b, j.h, j.first, j.nodes, j.len, row, V * lane, V * lane + V);
+    }
+  }
 }
 
 }  // namespace
+
+cudaError_t launch_tree_join(const TreeArgs& a, int blocks, int tile_rows, cudaStream_t s) {
+  // rows that a tile of these requests can have
+  const int most = a.max_tree * (a.q_heads / a.kv_heads), rows = most < tile_rows ? most : tile_rows;
+  const dim3 grid(blocks, (rows + 31) / 32);
+  switch (a.head_dim * 10 + a.fmt) {
+    case 1280: tree_join_kernel<128, 0><<<grid, 256, 0, s>>>(a, tile_rows); break;
+    case 1281: tree_join_kernel<128, 1><<<grid, 256, 0, s>>>(a, tile_rows); break;
+    case 640: tree_join_kernel<64, 0><<<grid, 256, 0, s>>>(a, tile_rows); break;
+    case 641: tree_join_kernel<64, 1><<<grid, 256, 0, s>>>(a, tile_rows); break;
+    default: return cudaErrorInvalidValue;
+  }
+  return cudaGetLastError();
+}
 
 cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s) {
   if (a.max_tree * (a.q_heads / a.kv_heads) > kRows) return launch_tree_tc(a, s);

@@ -128,13 +128,23 @@ struct TreeSegment {
   long long pair_begin;    // the pair's first unit in the range of all
   int u0, u1;              // units of the pair in this slice
   int slot;                // 2 * block (+ 1): where a partial result goes
-  int first_block, parts;  // blocks that share the pair: first_block .. first_block + parts - 1
+  int parts;               // blocks that share the pair
 };
 
-// Walks a slice's segments: `at` is the unit to go on from, b / before its request.
+struct TreeWalk {
+  long long at, before;
+  int b;
+  TreeSegment seg;
+};
+
+// Walks a slice's segments: w.at is the unit to go on from, w.b and w.before
+// its request. Out of line: the roles of a thread block share one copy (their
+// hot loops and five inlined copies together did not fit the instruction cache).
 template <int R, int UNIT>
-__device__ __forceinline__ bool next_segment(const TreeArgs& a, const TreeSlice& s, long long& at, int& b,
-                                             long long& before, TreeSegment& g) {
+__device__ __noinline__ bool next_segment(const TreeArgs& a, const TreeSlice& s, TreeWalk& w) {
+  long long at = w.at, before = w.before;
+  int b = w.b;
+  TreeSegment& g = w.seg;
   if (at >= s.end) return false;
   g.r = tree_request<R, UNIT>(a, b);
   long long n = static_cast<long long>(g.r.units) * g.r.tiles * a.kv_heads;
@@ -152,9 +162,10 @@ __device__ __forceinline__ bool next_segment(const TreeArgs& a, const TreeSlice&
   g.u0 = static_cast<int>(at - g.pair_begin);
   g.u1 = static_cast<int>(min(s.end - g.pair_begin, static_cast<long long>(g.r.units)));
   g.slot = 2 * static_cast<int>(blockIdx.x) + (at == s.begin ? 0 : 1);
-  g.first_block = s.block_of(g.pair_begin);
-  g.parts = s.block_of(g.pair_begin + g.r.units - 1) - g.first_block + 1;
-  at = g.pair_begin + g.u1;
+  g.parts = s.block_of(g.pair_begin + g.r.units - 1) - s.block_of(g.pair_begin) + 1;
+  w.at = g.pair_begin + g.u1;
+  w.before = before;
+  w.b = b;
   return true;
 }
 
@@ -189,16 +200,17 @@ __device__ __forceinline__ void tree_store4(const TreeArgs& a, const TreeSegment
 // this puts NaN into channels [c0, c1) of row `row` that such a code reaches
 // through a node the row sees; by the thread that stored them.
 template <int D, int FMT>
-__device__ __forceinline__ void tree_put_nan(const TreeArgs& a, const TreeSegment& g, int gq, int row, int c0, int c1) {
-  const int n = g.r.first + row / gq;
+__device__ __noinline__ void tree_put_nan(const TreeArgs& a, int b, int h, int first, int nodes, int len, int row, int c0,
+                                          int c1) {
+  const int gq = a.q_heads / a.kv_heads, n = first + row / gq;
   const uint64_t* mask = a.tree_mask + static_cast<long long>(n) * a.mask_words;
-  const long long at = (static_cast<long long>(n) * a.q_heads + g.h * gq + row % gq) * D;
+  const long long at = (static_cast<long long>(n) * a.q_heads + h * gq + row % gq) * D;
 #pragma unroll 1
-  for (int j = 0; j < g.r.nodes; ++j) {
+  for (int j = 0; j < nodes; ++j) {
     if (!((mask[j >> 6] >> (j & 63)) & 1)) continue;
-    const int tok = g.r.len + j, t = tok % 16;
-    const int blk = min(max(a.block_table[static_cast<long long>(g.b) * a.max_blocks + tok / 16], 0), a.num_blocks - 1);
-    const uint8_t* vb = a.v_pool + (static_cast<long long>(blk) * a.kv_heads + g.h) * (16 * D);
+    const int tok = len + j, t = tok % 16;
+    const int blk = min(max(a.block_table[static_cast<long long>(b) * a.max_blocks + tok / 16], 0), a.num_blocks - 1);
+    const uint8_t* vb = a.v_pool + (static_cast<long long>(blk) * a.kv_heads + h) * (16 * D);
 #pragma unroll 1
     for (int c = c0; c < c1; ++c) {
       const uint32_t code = vb[(c / 32 * 32 + 4 * (c % 8) + t % 8 / 2) * 16 + c % 32 / 8 * 4 + t / 8 * 2 + t % 2];
@@ -210,79 +222,23 @@ __device__ __forceinline__ void tree_put_nan(const TreeArgs& a, const TreeSegmen
   }
 }
 
-// Join the `parts` partial results of a pair (rows [0, rows) of its tile) by
-// `threads` threads that `sync` brings together, `tid` of them this one.
-// Partial of slot s: o at part_o + s * R * D, (m, l) of row r at part_ml + (s *
-// R + r) * 2, flag at part_flag[s]. sm: 2 * R + 1 words of shared memory.
-template <int R, int D, int FMT, class Sync>
-__device__ __forceinline__ void tree_merge(const TreeArgs& a, const TreeSegment& g, const TreeSlice& s, int gq, int rows,
-                                           float v_scale, float* sm, int tid, int threads, Sync sync) {
-  float* m_s = sm;
-  float* inv = sm + R;
-  int& flag_s = *reinterpret_cast<int*>(sm + 2 * R);
-  auto slot_of = [&](int i) -> long long {
-    const int c = g.first_block + i;
-    return 2ll * c + ((i == 0 && s.start_of(c) != g.pair_begin) ? 1 : 0);
-  };
-  if (tid == 0) flag_s = 0;
-  sync();
-  for (int r = tid; r < rows; r += threads) {
-    float m = -INFINITY, l = 0.0f;
-    for (int i = 0; i < g.parts; ++i) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot_of(i) * R + r);
-      const float mn = fmaxf(m, ml.x);
-      // (a part without a maximum has the sum 0, or NaN, which stays)
-      l = mn == -INFINITY ? l + ml.y : l * fast_exp2(m - mn) + ml.y * fast_exp2(ml.x - mn);
-      m = mn;
-    }
-    m_s[r] = m;
-    inv[r] = l == 0.0f ? 0.0f : v_scale / l;
-  }
-  for (int i = tid; i < g.parts; i += threads)
-    if (__ldcg(a.part_flag + slot_of(i))) flag_s = 1;
-  sync();
-  constexpr int V = D / 4;  // float4 columns
-  constexpr int kRowsAtOnce = 4;
-  const int c4 = tid % V, r_step = threads / V;
-  for (int r0 = tid / V; r0 < rows; r0 += r_step * kRowsAtOnce) {
-    float4 acc[kRowsAtOnce];
-    float m[kRowsAtOnce];
-#pragma unroll
-    for (int k = 0; k < kRowsAtOnce; ++k) {
-      acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      m[k] = r0 + k * r_step < rows ? m_s[r0 + k * r_step] : -INFINITY;
-    }
-#pragma unroll 2
-    for (int i = 0; i < g.parts; ++i) {
-      const long long base = slot_of(i) * R;
-#pragma unroll
-      for (int k = 0; k < kRowsAtOnce; ++k) {
-        const int r = r0 + k * r_step;
-        if (r < rows) {
-          const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + (base + r) * D) + c4);
-          const float pm = __ldcg(a.part_ml + (base + r) * 2);
-          const float w = m[k] == -INFINITY ? 0.0f : fast_exp2(pm - m[k]);
-          acc[k].x = fmaf(o.x, w, acc[k].x);
-          acc[k].y = fmaf(o.y, w, acc[k].y);
-          acc[k].z = fmaf(o.z, w, acc[k].z);
-          acc[k].w = fmaf(o.w, w, acc[k].w);
-        }
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kRowsAtOnce; ++k) {
-      const int r = r0 + k * r_step;
-      if (r < rows) {
-        const float f = inv[r];
-        tree_store4<D>(a, g, gq, g.tile * R + r, c4, make_float4(acc[k].x * f, acc[k].y * f, acc[k].z * f, acc[k].w * f));
-      }
-    }
-    if (flag_s) {
-#pragma unroll 1
-      for (int r = r0; r < min(rows, r0 + kRowsAtOnce * r_step); r += r_step)
-        tree_put_nan<D, FMT>(a, g, gq, g.tile * R + r, 4 * c4, 4 * c4 + 4);
-    }
-  }
+// What a block leaves for the joining kernel: the pair it began and did not
+// end (parts 0: none). A block begins at most one such pair.
+__device__ __forceinline__ void tree_leave_none(const TreeArgs& a) {
+  a.joins[blockIdx.x].parts = 0;
+}
+__device__ __forceinline__ void tree_leave_join(const TreeArgs& a, const TreeSegment& g, int rows, int row0) {
+  TreeJoin j;
+  j.parts = g.parts;
+  j.slot0 = g.slot;
+  j.rows = rows;
+  j.row0 = row0;
+  j.b = g.b;
+  j.h = g.h;
+  j.first = g.r.first;
+  j.nodes = g.r.nodes;
+  j.len = g.r.len;
+  a.joins[blockIdx.x] = j;
 }
 
 }  // namespace kvq

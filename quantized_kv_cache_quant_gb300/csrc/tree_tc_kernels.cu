@@ -8,17 +8,25 @@
 //            its own running maximum, sum and outputs, joined at the end.
 // While one stream's softmax runs on the CUDA cores the tensor core works for
 // the other one.
-//   S = Q K^T : A = Q in tensor memory (fp16, exact), B = the keys as fp16 in
-//               shared memory, accumulators 128 x 64 fp32 in tensor memory
-//   O += P V  : A = P in tensor memory (fp16, over S's columns; WIDE: and the
-//               rounding's remainder), B = the values as fp16
-// Roles: one warp copies pool blocks (bulk copies, 6 tiles ahead), four warps turn
-// FP8 bytes into fp16 operand tiles (each byte once per thread block, for all
-// its rows), one thread issues the MMAs, two groups of four warps do the
-// softmax, a thread per query row. A row's outputs are rescaled only when its
-// maximum has grown by more than 2^kSlack: weights then reach 2^(kBias +
-// kSlack) = 2^15, within fp16, and those down to 2^-21 of the largest stay
-// normal fp16 numbers.
+//   S = Q K^T : A = Q (fp16, exact) in tensor memory, or in shared memory where
+//               tensor memory has no room, B = the keys as fp16 in shared
+//               memory, accumulators 128 x 64 fp32 in tensor memory
+//   O += P V  : A = P in tensor memory (fp16; WIDE: and the rounding's
+//               remainder), B = the values as fp16
+// Tensor memory's 512 columns (D = 128): O 2 x 128, S 2 x 64, P 2 x 32 and Q 64,
+// or with WIDE P 2 x 64 and no Q. P beside S, not over it, is what lets a
+// stream's next scores run under its softmax: with P over S a tile took 1220
+// clocks (R = 128) and 2200 (R = 256) instead of the figures below.
+// Roles: one warp copies pool blocks (bulk copies, some tiles ahead), four warps
+// turn FP8 bytes into fp16 operand tiles (each byte once per thread block, for
+// all its rows), three threads issue the MMAs (scores, and each stream's outputs:
+// a wait costs an issuing thread some 100 clocks even when it is over, and one
+// thread with all the waits of a tile was what bounded the kernel), two groups of
+// four warps do the softmax, a thread per query row. Weights are 2^(score - m + kBias), m a maximum of
+// the row that is renewed (and the row's outputs rescaled) only when a tile's
+// weights sum to more than 2^15: all of them are within fp16 until then, those
+// down to 2^-21 of the largest are normal fp16 numbers, and a tile in which
+// nothing grows needs no maximum.
 //
 // Orders that the products do not see: the channels of Q and K follow the key
 // bytes' order, the tokens of a block that of the value bytes (column 4t + 2r +
@@ -32,32 +40,49 @@ namespace {
 
 constexpr int kBlock = 16;
 constexpr int kTile = 64;             // tokens of a tile (and of a work unit)
-constexpr int kStages = 6;            // tiles of pool bytes in flight
-constexpr int kBufs = 3;              // fp16 tiles of keys and of values
+constexpr int kMaxBufs = 4;           // fp16 tiles (keys and values)
 constexpr float kBias = 7.0f;
-constexpr float kSlack = 8.0f;
-constexpr int kThreads = 448;
-// warps: 0-3 and 4-7 softmax of stream 0 and 1, 8-11 conversion, 12 copies, 13 MMA
-constexpr int kConvertWarp = 8, kCopyWarp = 12, kMmaWarp = 13;
+constexpr float kMostSum = 32768.0f;  // of a tile's weights in a row: each is within fp16 then
+constexpr int kThreads = 512;
+// warps: 0-3 and 4-7 softmax of stream 0 and 1, 8-11 conversion, 12 copies, 13 the scores' MMAs, 14 and 15 the outputs'
+// MMAs of stream 0 and 1
+constexpr int kConvertWarp = 8, kCopyWarp = 12, kScoreWarp = 13, kOutputWarp = 14;
+constexpr int kMaxStages = 6;
 
-template <int D>
-struct TcSmem {
-  static constexpr int STAGE = 2 * kTile * D;      // key bytes, then value bytes
-  static constexpr int KTILE = kTile * D * 2;      // one fp16 tile
-  static constexpr int K_OFF = kStages * STAGE;
-  static constexpr int V_OFF = K_OFF + kBufs * KTILE;
-  static constexpr int BYTES = V_OFF + kBufs * KTILE;
+template <int D, bool WIDE, int R>
+struct TcPlan {
+  static constexpr bool SPLIT_ROWS = R == 256;      // the streams' rows differ (else their tokens do)
+  static constexpr int Q_SMEM = (WIDE ? 1 : 0) + (SPLIT_ROWS ? 1 : 0);  // Q tiles in shared memory
+  // shared memory
+  static constexpr int STAGE = 2 * kTile * D;       // pool bytes of a tile: keys, then values
+  static constexpr int TILE = kTile * D * 2;        // one fp16 tile of keys or values
+  static constexpr int Q_TILE = 128 * D * 2;
+  static constexpr int BUFS = Q_SMEM == 2 ? 3 : kMaxBufs;
+  static constexpr int FIXED = BUFS * 2 * TILE + Q_SMEM * Q_TILE;
+  static constexpr int FIT = (221184 - FIXED) / STAGE;  // 227 KB without what TcShared takes
+  static constexpr int STAGES = FIT < kMaxStages ? FIT : kMaxStages;
+  static_assert(STAGES >= 2, "room for the copies");
+  static constexpr int K_OFF = STAGES * STAGE, V_OFF = K_OFF + BUFS * TILE, Q_OFF = V_OFF + BUFS * TILE;
+  static constexpr int BYTES = Q_OFF + Q_SMEM * Q_TILE;
+  // tensor memory columns
+  static constexpr int P_COLS = (WIDE ? 2 : 1) * kTile / 2;
+  static constexpr int TM_O = 0, TM_S = 2 * D, TM_P = TM_S + 2 * kTile, TM_Q = TM_P + 2 * P_COLS;
+  static_assert((WIDE ? TM_Q : TM_Q + D / 2) <= 512, "tensor memory");
 };
 
 struct TcShared {
-  uint64_t full[kStages], empty[kStages];
-  uint64_t kready[kBufs], kfree[kBufs], vready[kBufs], vfree[kBufs];
-  uint64_t qready[2], sready[2], pready[2], oready[2], drain;
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t ready[kMaxBufs], free[kMaxBufs];
+  uint64_t qready[2], sready[2], sfree[2], pready[2], pdone[2], drain[3];
   unsigned long long plan[34];
   uint32_t tmem;
-  int dead, nan_met, last;
+  int dead, nan_met;
   float ml[2][128][2];
-  float merge[2 * 256 + 1];
+  // the arguments, for functions out of line (a reference to a kernel's parameters is read from global memory there)
+  TreeArgs args;
+  // each warp's place in the slice: in shared memory, not in registers that the roles' loops need
+  TreeSlice slice;
+  TreeWalk walk[kThreads / 32];
 };
 
 // Bits of the tokens tok .. tok + 63 that a row with these mask words sees.
@@ -83,41 +108,50 @@ __host__ __device__ constexpr int column_token(int c) {
 }
 
 template <int D, int FMT, bool WIDE, int R>
-__global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
-  using S = TcSmem<D>;
-  constexpr bool SPLIT_ROWS = R == 256;  // the streams' rows differ (else their tokens do)
-  constexpr int UPB = kTile / kBlock;    // pool blocks of a tile
-  constexpr uint32_t TM_O = 0, TM_Q = 2 * D, TM_S = 2 * D + D;  // columns: O, Q, S of stream 0; stream 1 follows each
-  constexpr uint32_t S_COLS = kTile, Q_COLS = D / 2;
+__global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_constant__ TreeArgs a) {
+  using S = TcPlan<D, WIDE, R>;
+  constexpr bool SPLIT_ROWS = S::SPLIT_ROWS;
+  constexpr int UPB = kTile / kBlock;  // pool blocks of a tile
+  constexpr unsigned kStages = S::STAGES, kBufs = S::BUFS;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ TcShared sh;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform for the compiler too
   const int gq = a.q_heads / a.kv_heads;
 
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 4);
+      mbar_init(&sh.empty[i], 2);
     }
-    for (int i = 0; i < kBufs; ++i) {
-      mbar_init(&sh.kready[i], 4);
-      mbar_init(&sh.vready[i], 4);
-      mbar_init(&sh.kfree[i], 1);
-      mbar_init(&sh.vfree[i], 1);
+    for (int i = 0; i < kMaxBufs; ++i) {
+      mbar_init(&sh.ready[i], 2);
+      mbar_init(&sh.free[i], SPLIT_ROWS ? 2 : 1);  // from each stream that reads the tile
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.qready[i], 4);
       mbar_init(&sh.sready[i], 1);
+      mbar_init(&sh.sfree[i], 4);
       mbar_init(&sh.pready[i], 4);
-      mbar_init(&sh.oready[i], 1);
+      mbar_init(&sh.pdone[i], 1);
     }
-    mbar_init(&sh.drain, 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&sh.drain[i], 1);
     sh.dead = sh.nan_met = 0;
+    sh.args = a;
     fence_mbar_init();
   }
-  const TreeSlice slice = tree_slice<R, kTile>(a, sh.plan, 2);
-  if (static_cast<int>(blockIdx.x) >= slice.blocks) return;
-  if (warp == kMmaWarp) {
+  if (tid == 0) tree_leave_none(a);
+  {
+    const TreeSlice s = tree_slice<R, kTile>(a, sh.plan, 2);
+    if (static_cast<int>(blockIdx.x) >= s.blocks) return;
+    if (tid == 0) sh.slice = s;
+    if (lane == 0) {
+      sh.walk[warp].at = s.begin;
+      sh.walk[warp].before = s.before;
+      sh.walk[warp].b = s.b;
+    }
+  }
+  if (warp == kScoreWarp) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
     tc_fence_before();
@@ -127,27 +161,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
   const uint32_t tmem = sh.tmem;
   volatile int* dead = &sh.dead;
 
-  long long at = slice.begin, before = slice.before;
-  int b = slice.b;
-  TreeSegment seg;
+  TreeWalk& walk = sh.walk[warp];
+  const TreeSegment& seg = walk.seg;
+  auto next_here = [&]() { return next_segment<R, kTile>(sh.args, sh.slice, walk); };
+  // the warp's next segment: one lane finds it, all read it
+  auto next = [&]() -> bool {
+    __syncwarp();
+    bool more = false;
+    if (elect_one()) more = next_here();
+    return __any_sync(0xffffffffu, more);
+  };
 
   if (warp == kCopyWarp) {
     // ---- copies: lane 2i + r takes block i of a tile, r = 0 keys, 1 values ----
     unsigned n = 0;  // tiles issued
     bool ok = true;
-    while (ok && next_segment<R, kTile>(a, slice, at, b, before, seg)) {
+    while (ok && next()) {
       const int nblk = (seg.r.len + seg.r.nodes + kBlock - 1) / kBlock;
       const int32_t* table = a.block_table + static_cast<long long>(seg.b) * a.max_blocks;
-      const uint8_t* pool = (lane & 1) ? a.v_pool : a.k_pool;
-      const int i = lane >> 1;
+      const uint8_t* pool = ((lane & 1) ? a.v_pool : a.k_pool) + static_cast<long long>(seg.h) * (kBlock * D);
+      const int i = lane >> 1, u0 = seg.u0, u1 = seg.u1;
       auto entry = [&](int t) -> int { return (i < UPB && t * UPB + i < nblk) ? table[t * UPB + i] : 0; };
-      int next = entry(seg.u0);
-      for (int t = seg.u0; t < seg.u1; ++t, ++n) {
-        const int blk = next;
-        if (t + 1 < seg.u1) next = entry(t + 1);
+      int ahead = entry(u0);
+      for (int t = u0; t < u1; ++t, ++n) {
+        const int blk = ahead;
+        if (t + 1 < u1) ahead = entry(t + 1);
         const int s = n % kStages;
-        if (n >= kStages) ok = role_wait(&sh.empty[s], (n / kStages - 1) & 1, dead, a.status);
-        ok = __all_sync(0xffffffffu, ok);
+        if (n >= kStages) ok = role_wait_warp(&sh.empty[s], (n / kStages - 1) & 1, dead, a.status);
         if (!ok) break;
         const int here = min(UPB, nblk - t * UPB);
         if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], here * 2 * kBlock * D);
@@ -155,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
         if (i < here) {
           const long long p = min(max(blk, 0), a.num_blocks - 1);
           bulk_g2s(smem + s * S::STAGE + (lane & 1) * (kTile * D) + i * (kBlock * D),
-                   pool + (p * a.kv_heads + seg.h) * (kBlock * D), kBlock * D, &sh.full[s]);
+                   pool + p * a.kv_heads * (kBlock * D), kBlock * D, &sh.full[s]);
         }
       }
     }
@@ -163,143 +203,154 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
       for (unsigned k = n > kStages ? n - kStages : 0; k < n; ++k)
         (void)mbar_wait_bounded(&sh.full[k % kStages], (k / kStages) & 1);
     }
-  } else if (warp == kMmaWarp) {
-    // ---- MMA: one thread ----
-    if (lane == 0) {
-      constexpr uint32_t ID_S = tc_idesc_f16(128, kTile), ID_O = tc_idesc_f16(128, D);
-      const uint32_t kbase = smem_addr(smem + S::K_OFF), vbase = smem_addr(smem + S::V_OFF);
-      unsigned n = 0;                    // tiles whose keys are in use or done
-      unsigned n_s[2] = {0, 0};          // tiles of each stream whose weights were used
-      unsigned segs = 0;
+  } else if (warp == kScoreWarp) {
+    // ---- scores: one thread; S_i = Q_i K(tile)^T once the scores before are read ----
+    if (elect_one()) {
+      constexpr uint32_t ID_S = tc_idesc_f16(128, kTile);
+      const uint32_t kbase = smem_addr(smem + S::K_OFF), qbase = smem_addr(smem + S::Q_OFF);
+      unsigned n = 0, n_s[2] = {0, 0}, segs = 0;  // tiles, tiles of each stream, segments
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         ok = ok && role_wait(bar, parity, dead, a.status);
         return ok;
       };
-      auto scores = [&](int i, unsigned k) {  // S_i = Q_i K(tile k)^T
-        const uint32_t kt = kbase + (k % kBufs) * S::KTILE;
+      auto scores = [&](int i, uint32_t kt, bool read) {
+        if (!read && !wait(&sh.sfree[i], (n_s[i] - 1) & 1)) return;
+        ++n_s[i];
+        tc_fence_after();
+        const bool q_smem = WIDE || (SPLIT_ROWS && i == 1);
+        const uint32_t qt = qbase + ((WIDE && SPLIT_ROWS) ? i * S::Q_TILE : 0);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc_mma_f16(tmem + TM_S + i * S_COLS, tmem + TM_Q + i * Q_COLS + 8 * ks,
-                     smem_desc_kmajor(kt + ks * (2 * kTile * 16), kTile * 16, 128), ID_S, ks > 0);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint64_t bd = smem_desc_kmajor(kt + ks * (2 * kTile * 16), kTile * 16, 128);
+          if (q_smem)
+            tc_mma_f16_ss(tmem + S::TM_S + i * kTile, smem_desc_kmajor(qt + ks * (2 * 128 * 16), 128 * 16, 128), bd, ID_S, ks > 0);
+          else
+            tc_mma_f16(tmem + S::TM_S + i * kTile, tmem + S::TM_Q + 8 * ks, bd, ID_S, ks > 0);
+        }
         tc_commit(&sh.sready[i]);
       };
-      auto outputs = [&](int i, unsigned k, bool first) {  // O_i += P_i V(tile k)
-        const uint32_t vt = vbase + (k % kBufs) * S::KTILE;
-#pragma unroll
-        for (int part = 0; part < (WIDE ? 2 : 1); ++part)
-#pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)
-            tc_mma_f16(tmem + TM_O + i * D, tmem + TM_S + i * S_COLS + part * (kTile / 2) + 8 * ks,
-                       smem_desc_kmajor(vt + ks * (2 * D * 16), D * 16, 128), ID_O, !(first && part == 0 && ks == 0));
-      };
-      while (ok && next_segment<R, kTile>(a, slice, at, b, before, seg)) {
-        const int tiles = seg.u1 - seg.u0;
+      while (ok && next_here()) {
         if (!wait(&sh.qready[0], segs & 1) || !wait(&sh.qready[1], segs & 1)) break;
         ++segs;
-        tc_fence_after();
-        if constexpr (SPLIT_ROWS) {
-          if (!wait(&sh.kready[n % kBufs], (n / kBufs) & 1)) break;
-          tc_fence_after();
-          scores(0, n);
-          scores(1, n);
-          tc_commit(&sh.kfree[n % kBufs]);
-          for (int t = 0; t < tiles && ok; ++t, ++n) {
-            const bool more = t + 1 < tiles;
-            if (more && !wait(&sh.kready[(n + 1) % kBufs], ((n + 1) / kBufs) & 1)) break;
-            if (!wait(&sh.vready[n % kBufs], (n / kBufs) & 1)) break;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (!wait(&sh.pready[i], n_s[i] & 1)) break;
-              ++n_s[i];
-              tc_fence_after();
-              outputs(i, n, t == 0);
-              if (i == 1) tc_commit(&sh.vfree[n % kBufs]);
-              if (more) {
-                scores(i, n + 1);  // after P_i V(n) on the tensor core, which reads the columns this writes
-                if (i == 1) tc_commit(&sh.kfree[(n + 1) % kBufs]);
-              } else {
-                tc_commit(&sh.oready[i]);
-              }
-            }
+        const int tiles = seg.u1 - seg.u0;
+        for (int t = 0; t < tiles; ++t, ++n) {
+          const unsigned k = n % kBufs;
+          // (asked together: each answer takes some 100 clocks)
+          auto read = [&](int i) { return n_s[i] == 0 || mbar_test(&sh.sfree[i], (n_s[i] - 1) & 1); };
+          const bool here = mbar_test(&sh.ready[k], (n / kBufs) & 1);
+          const bool read0 = (SPLIT_ROWS || !(t & 1)) && read(0), read1 = (SPLIT_ROWS || (t & 1)) && read(1);
+          if (!here && !wait(&sh.ready[k], (n / kBufs) & 1)) break;
+          const uint32_t kt = kbase + k * S::TILE;
+          if constexpr (SPLIT_ROWS) {
+            scores(0, kt, read0);
+            scores(1, kt, read1);
+          } else {
+            if (t & 1) scores(1, kt, read1);
+            else scores(0, kt, read0);
           }
-        } else {
-          for (int t = 0; t <= tiles && ok; ++t) {
-            if (t < tiles) {
-              const unsigned k = n + t;
-              if (!wait(&sh.kready[k % kBufs], (k / kBufs) & 1)) break;
-              tc_fence_after();
-              scores(t & 1, k);
-              tc_commit(&sh.kfree[k % kBufs]);
-            }
-            if (t > 0) {
-              const int i = (t - 1) & 1;
-              const unsigned k = n + t - 1;
-              if (!wait(&sh.vready[k % kBufs], (k / kBufs) & 1) || !wait(&sh.pready[i], n_s[i] & 1)) break;
-              ++n_s[i];
-              tc_fence_after();
-              outputs(i, k, t <= 2);
-              tc_commit(&sh.vfree[k % kBufs]);
-              if (t - 1 + 2 >= tiles) tc_commit(&sh.oready[i]);
-            }
-          }
-          n += tiles;
+          if (!ok) break;
         }
       }
-      if (!ok) {  // no MMA of this block is in flight when it frees its tensor memory
-        tc_commit(&sh.drain);
-        (void)mbar_wait_bounded(&sh.drain, 0);
+      if (!ok) {  // no MMA of this thread is in flight when the block frees its tensor memory
+        tc_commit(&sh.drain[0]);
+        (void)mbar_wait_bounded(&sh.drain[0], 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kOutputWarp) {
+    // ---- outputs of stream i: one thread; O_i += P_i V(tile) ----
+    const int i = warp - kOutputWarp;
+    if (elect_one()) {
+      constexpr uint32_t ID_O = tc_idesc_f16(128, D);
+      const uint32_t vbase = smem_addr(smem + S::V_OFF);
+      const uint32_t o = tmem + S::TM_O + i * D, pt = tmem + S::TM_P + i * S::P_COLS;
+      unsigned n = 0, n_p = 0;  // tiles, tiles of this stream
+      bool ok = true;
+      while (ok && next_here()) {
+        const int first = SPLIT_ROWS ? 0 : i, step = SPLIT_ROWS ? 1 : 2, tiles = seg.u1 - seg.u0;
+        for (int t = first; t < tiles; t += step, ++n_p) {
+          const unsigned k = (n + t) % kBufs;
+          // (weights are ready after the tile's scores, so its values are there too)
+          ok = role_wait(&sh.pready[i], n_p & 1, dead, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t vt = vbase + k * S::TILE;
+#pragma unroll
+          for (int part = 0; part < (WIDE ? 2 : 1); ++part)
+#pragma unroll
+            for (int ks = 0; ks < kTile / 16; ++ks)
+              tc_mma_f16(o, pt + part * (kTile / 2) + 8 * ks, smem_desc_kmajor(vt + ks * (2 * D * 16), D * 16, 128), ID_O,
+                         t != first || part != 0 || ks != 0);
+          tc_commit(&sh.pdone[i]);
+          tc_commit(&sh.free[k]);
+        }
+        n += tiles;
+      }
+      if (!ok) {
+        tc_commit(&sh.drain[1 + i]);
+        (void)mbar_wait_bounded(&sh.drain[1 + i], 0);
       }
     }
     __syncwarp();
   } else if (warp >= kConvertWarp) {
-    // ---- conversion: warp w takes block w of a tile ----
-    const int w = warp - kConvertWarp;
+    // ---- conversion: warps 2p and 2p + 1 take the tiles of parity p, two blocks each. (All four warps on
+    // one tile left the tensor core waiting: a tile's waits, fences and load latencies are a fixed cost of
+    // each warp, so two tiles are converted at a time.) ----
+    const int cw = warp - kConvertWarp, pair = cw >> 1, w0 = 2 * (cw & 1);
     unsigned n = 0;
     bool ok = true;
-    while (ok && next_segment<R, kTile>(a, slice, at, b, before, seg)) {
-      const int len = seg.r.len, total = len + seg.r.nodes;
-      for (int t = seg.u0; t < seg.u1; ++t, ++n) {
+    while (ok && next()) {
+      const int len = seg.r.len, total = len + seg.r.nodes, u0 = seg.u0, u1 = seg.u1;
+      for (int t = u0; t < u1; ++t, ++n) {
+        if (static_cast<int>(n & 1) != pair) continue;
         const int s = n % kStages, k = n % kBufs;
-        ok = role_wait(&sh.full[s], (n / kStages) & 1, dead, a.status);
-        if (ok && n >= kBufs) ok = role_wait(&sh.kfree[k], (n / kBufs - 1) & 1, dead, a.status);
-        ok = __all_sync(0xffffffffu, ok);
+        const bool room = n < kBufs || mbar_test(&sh.free[k], (n / kBufs - 1) & 1);
+        ok = role_wait_warp(&sh.full[s], (n / kStages) & 1, dead, a.status);
+        // unit (nt, kh, g, tig): 16 channels of token 8nt + g; a quarter of the warp takes 8 tokens of one
+        // core matrix, their tig rotated so that neither the reads nor the writes meet in a bank
+        const int g3 = lane & 3, nt = (lane >> 2) & 1, ktig = ((lane >> 3) + (g3 >> 1) + 2 * nt) & 3;
+        const uint8_t* ksrc = smem + s * S::STAGE + w0 * (kBlock * D) + (nt * (D / 64) * 32 + 4 * g3 + ktig) * 16;
+        uint4 x[2][D / 64][2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int kh = 0; kh < D / 64; ++kh)
+#pragma unroll
+            for (int gs = 0; gs < 2; ++gs)
+              x[w][kh][gs] = *reinterpret_cast<const uint4*>(ksrc + w * (kBlock * D) + kh * 512 + gs * 256);
+        // unit (c, g, tig): tokens 2tig, 2tig + 1, 8 + 2tig, 9 + 2tig of channels 8 (4c + j) + g
+        const int g = (lane >> 1) & 7, tig = 2 * ((lane >> 4) ^ ((g >> 1) & 1)) + (lane & 1);
+        const uint8_t* vsrc = smem + s * S::STAGE + kTile * D + w0 * (kBlock * D) + (4 * g + tig) * 16;
+        uint4 y[2][D / 32];
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) y[w][c] = *reinterpret_cast<const uint4*>(vsrc + w * (kBlock * D) + c * 512);
+        if (ok && !room) ok = role_wait_warp(&sh.free[k], (n / kBufs - 1) & 1, dead, a.status);
         if (!ok) break;
-        {
-          const uint8_t* src = smem + s * S::STAGE + w * (kBlock * D);
-          uint8_t* dst = smem + S::K_OFF + k * S::KTILE;
-          // unit (nt, kh, g, tig): 16 channels of token 8nt + g; a quarter of the warp takes 8 tokens of one
-          // core matrix, their tig rotated so that neither the reads nor the writes meet in a bank
-          const int q4 = lane >> 3, g3 = lane & 3, nt = (lane >> 2) & 1, tig = (q4 + (g3 >> 1) + 2 * nt) & 3;
-          const int v8 = 4 * (g3 >> 1) + 2 * nt + (g3 & 1);  // row of the core matrix
+        // row of the core matrix: 4 (g3 / 2) + 2nt + g3 % 2
+        uint8_t* kdst = smem + S::K_OFF + k * S::TILE + ktig * 2 * (kTile * 16) + 2 * w0 * 128 +
+                        (4 * (g3 >> 1) + 2 * nt + (g3 & 1)) * 16;
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
 #pragma unroll
           for (int kh = 0; kh < D / 64; ++kh)
 #pragma unroll
             for (int gs = 0; gs < 2; ++gs) {
-              const int g = g3 + 4 * gs;
-              const uint4 x = *reinterpret_cast<const uint4*>(src + ((nt * (D / 64) + kh) * 32 + 4 * g + tig) * 16);
-              uint8_t* d = dst + ((kh * 4 + tig) * 2) * (kTile * 16) + (2 * w + gs) * 128 + v8 * 16;
+              const uint4 u = x[w][kh][gs];
+              uint8_t* d = kdst + kh * 8 * (kTile * 16) + (2 * w + gs) * 128;
               *reinterpret_cast<uint4*>(d) =
-                  make_uint4(fp8_lo_pair<FMT>(x.x), fp8_hi_pair<FMT>(x.x), fp8_lo_pair<FMT>(x.y), fp8_hi_pair<FMT>(x.y));
+                  make_uint4(fp8_lo_pair<FMT>(u.x), fp8_hi_pair<FMT>(u.x), fp8_lo_pair<FMT>(u.y), fp8_hi_pair<FMT>(u.y));
               *reinterpret_cast<uint4*>(d + kTile * 16) =
-                  make_uint4(fp8_lo_pair<FMT>(x.z), fp8_hi_pair<FMT>(x.z), fp8_lo_pair<FMT>(x.w), fp8_hi_pair<FMT>(x.w));
+                  make_uint4(fp8_lo_pair<FMT>(u.z), fp8_hi_pair<FMT>(u.z), fp8_lo_pair<FMT>(u.w), fp8_hi_pair<FMT>(u.w));
             }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.kready[k]);
-        if (n >= kBufs) ok = role_wait(&sh.vfree[k], (n / kBufs - 1) & 1, dead, a.status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        {
-          const uint8_t* src = smem + s * S::STAGE + kTile * D + w * (kBlock * D);
-          uint8_t* dst = smem + S::V_OFF + k * S::KTILE;
-          // unit (c, g, tig): tokens 2tig, 2tig + 1, 8 + 2tig, 9 + 2tig of channels 8 (4c + j) + g
-          const int half = lane >> 4, g = (lane >> 1) & 7, tig = 2 * (half ^ ((g >> 1) & 1)) + (lane & 1);
-          const int tok0 = t * kTile + w * kBlock;
-          const bool edge = tok0 + kBlock > len;  // the tree's own tokens, and rows behind them
-          uint32_t keep = 0xFFFFFFFFu, tree_bytes = 0;
-          if (edge) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const int tok0 = t * kTile + (w0 + w) * kBlock;
+          uint32_t keep = 0xFFFFFFFFu;
+          if (tok0 + kBlock > len) {  // the tree's own tokens, and rows behind them
+            uint32_t tree_bytes = 0;
             keep = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -307,12 +358,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
               if (tok < total) keep |= 0xFFu << (8 * i);
               if (tok >= len) tree_bytes |= 0xFFu << (8 * i);
             }
-          }
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            const uint4 x = *reinterpret_cast<const uint4*>(src + (c * 32 + 4 * g + tig) * 16);
-            uint32_t word[4] = {x.x, x.y, x.z, x.w};
-            if (edge) {
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t* word = &y[w][c].x;
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const uint32_t bad = fp8_nonfinite<FMT>(word[j]) & tree_bytes & keep;
@@ -320,28 +368,30 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
                 word[j] &= keep & ~bad;
               }
             }
-            uint8_t* d = dst + (2 * w + (tig >> 1)) * (D * 16) + (4 * c) * 128 + g * 16 + (tig & 1) * 8;
+          }
+          uint8_t* vdst = smem + S::V_OFF + k * S::TILE + (2 * (w0 + w) + (tig >> 1)) * (D * 16) + g * 16 + (tig & 1) * 8;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            const uint32_t word[4] = {y[w][c].x, y[w][c].y, y[w][c].z, y[w][c].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint2*>(d + j * 128) = make_uint2(fp8_lo_pair<FMT>(word[j]), fp8_hi_pair<FMT>(word[j]));
+              *reinterpret_cast<uint2*>(vdst + (4 * c + j) * 128) = make_uint2(fp8_lo_pair<FMT>(word[j]), fp8_hi_pair<FMT>(word[j]));
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sh.vready[k]);
-          mbar_arrive(&sh.empty[s]);
-        }
+        mbar_arrive_if(&sh.ready[k], lane == 0);
+        mbar_arrive_if(&sh.empty[s], lane == 0);
       }
     }
   } else {
     // ---- softmax: stream `i`, a thread per query row ----
     const int i = warp >> 2, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t tm_s = tmem + lanes + TM_S + i * S_COLS;
-    unsigned n = 0, o_seen[2] = {0, 0};  // tiles of this stream; results of each stream waited for
+    const uint32_t tm_s = tmem + lanes + S::TM_S + i * kTile, tm_p = tmem + lanes + S::TM_P + i * S::P_COLS;
+    unsigned n = 0, n_both[2] = {0, 0};  // tiles of this stream; tiles of each stream at the segment's end
     bool ok = true;
-    while (next_segment<R, kTile>(a, slice, at, b, before, seg)) {
+    while (next()) {
       const int h = seg.h, len = seg.r.len, total = len + seg.r.nodes, row0 = seg.tile * R;
       const int rows = min(R, seg.r.nodes * gq - row0);       // of the tile
       const int my_rows = SPLIT_ROWS ? min(128, rows - 128 * i) : rows;  // of this stream (may be below 1)
@@ -356,99 +406,127 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
       const uint32_t flip = k_scale < 0.0f ? 0x80008000u : 0u;
       const uint64_t* mask = a.tree_mask + static_cast<long long>(seg.r.first + node) * a.mask_words;
 
-      if (ok) {  // the query row, its channels in the key units' order
+      if (ok) {  // the query row, its channels in the key units' order (R = 128: once for both streams)
         const __half* q = reinterpret_cast<const __half*>(a.q) + (seg.r.first + node) * a.q_stride +
                           static_cast<long long>(h * gq + (live ? (row0 + trow) % gq : 0)) * D;
+        if (SPLIT_ROWS || i == 0) {
 #pragma unroll
-        for (int kh = 0; kh < D / 64; ++kh) {
-          uint32_t w[32];
+          for (int kh = 0; kh < D / 64; ++kh) {
+            uint32_t w[32];
 #pragma unroll
-          for (int c4 = 0; c4 < 16; ++c4) {  // place 4 c4 of this half: channels 64kh + 16 (c4 % 4) + 4 (c4 / 4) .. +3
-            uint2 x = make_uint2(0u, 0u);
-            if (live) x = *reinterpret_cast<const uint2*>(q + 64 * kh + 16 * (c4 % 4) + 4 * (c4 / 4));
-            w[2 * c4] = x.x ^ flip;
-            w[2 * c4 + 1] = x.y ^ flip;
+            for (int c4 = 0; c4 < 16; ++c4) {  // place 4 c4 of this half: channels 64kh + 16 (c4 % 4) + 4 (c4 / 4) .. +3
+              uint2 x = make_uint2(0u, 0u);
+              if (live) x = *reinterpret_cast<const uint2*>(q + 64 * kh + 16 * (c4 % 4) + 4 * (c4 / 4));
+              w[2 * c4] = x.x ^ flip;
+              w[2 * c4 + 1] = x.y ^ flip;
+            }
+            if (WIDE || i == 1) {  // (uniform per warp)
+              uint8_t* d = smem + S::Q_OFF + ((WIDE && SPLIT_ROWS) ? i * S::Q_TILE : 0) + kh * 8 * (128 * 16) + row * 16;
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                *reinterpret_cast<uint4*>(d + c * (128 * 16)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+            } else {
+              tmem_st32(tmem + lanes + S::TM_Q + 32 * kh, w);
+            }
           }
-          tmem_st32(tmem + lanes + TM_Q + i * Q_COLS + 32 * kh, w);
+          if (WIDE || i == 1) fence_proxy_async_smem();
+          tmem_wait_st();
         }
-        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.qready[i]);
+        mbar_arrive_if(&sh.qready[i], lane == 0);
       }
 
       float m = -INFINITY, msub = -kBias, l = 0.0f;  // m in log2 units; weights are 2^(s * kmul - msub)
       const int step = SPLIT_ROWS ? 1 : 2;
-      for (int t = seg.u0 + (SPLIT_ROWS ? 0 : i); ok && t < seg.u1; t += step, ++n) {
-        ok = role_wait(&sh.sready[i], n & 1, dead, a.status);
-        ok = __all_sync(0xffffffffu, ok);
+      const int u0 = seg.u0, u1 = seg.u1;
+      for (int t = u0 + (SPLIT_ROWS ? 0 : i); ok && t < u1; t += step, ++n) {
+        ok = role_wait_warp(&sh.sready[i], n & 1, dead, a.status);
         if (!ok) break;
         tc_fence_after();
+        const bool pv_done = n > 0 && mbar_test(&sh.pdone[i], (n - 1) & 1);  // answers while the scores load
+        uint32_t sr[kTile];
         if (warp_live) {
-          uint32_t sr[kTile];
           tmem_ld32(tm_s, sr);
           tmem_ld32(tm_s + 32, sr + 32);
-          const int tok0 = t * kTile;
-          const bool edge = tok0 + kTile > len;
-          uint64_t vis = ~0ull;
-          if (edge) vis = tree_window(mask, a.mask_words, tok0, len, total);
-          tmem_wait_ld();
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        }
+        const int tok0 = t * kTile;
+        uint64_t vis = ~0ull;
+        const bool edge = tok0 + kTile > len;
+        if (edge && warp_live) vis = tree_window(mask, a.mask_words, tok0, len, total);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        mbar_arrive_if(&sh.sfree[i], lane == 0);
+        // the products of the tile before have read P and written O
+        if (n > 0 && !pv_done) ok = role_wait_warp(&sh.pdone[i], (n - 1) & 1, dead, a.status);
+        if (!ok) break;
+        if (warp_live) {
           if (edge) {
 #pragma unroll
             for (int c = 0; c < kTile; ++c)
               if (!((vis >> column_token(c)) & 1)) sr[c] = 0xFF800000u;
           }
-#pragma unroll
-          for (int c = 0; c < kTile; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(sr[c]));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kmul;
-          // grown beyond the slack (or from nothing): take the new maximum, bring what was summed to it
-          const bool grow = top > m + kSlack || (m == -INFINITY && top > m);
-          if (__any_sync(0xffffffffu, grow)) {
-            const float m_new = grow ? top : m;
-            const float alpha = grow ? fast_exp2(m - m_new) : 1.0f;
-            l *= alpha;
-            m = m_new;
-            msub = (m == -INFINITY ? 0.0f : m) - kBias;
-            if (t >= seg.u0 + step) {  // O holds something; the scores of this tile came after its last product
+          // Weights against the maximum so far; a tile needs no maximum of its own while their sum shows that none
+          // has left fp16's range. Where one has (and in a row without a maximum), the second pass follows a new one.
+          bool fresh = t < u0 + step;  // the stream's first tile: O is empty
+          float tile_sum = 0.0f;
 #pragma unroll 1
-              for (int c0 = 0; c0 < D; c0 += 16) {
-                uint32_t o[16];
-                tmem_ld16(tmem + lanes + TM_O + i * D + c0, o);
-                tmem_wait_ld();
+          for (int pass = fresh ? 1 : 0; pass < 2; ++pass) {
+            if (pass == 1) {
+              float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-                tmem_st16(tmem + lanes + TM_O + i * D + c0, o);
+              for (int c = 0; c < kTile; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(sr[c]));
+              const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kmul;
+              const bool grow = top > m && (m == -INFINITY || !(tile_sum <= kMostSum));
+              const float m_new = grow ? top : m;
+              const float alpha = grow ? fast_exp2(m - m_new) : 1.0f;
+              l *= alpha;
+              m = m_new;
+              msub = (m == -INFINITY ? 0.0f : m) - kBias;
+              if (!fresh) {
+                tc_fence_after();
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(tmem + lanes + S::TM_O + i * D + c0, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                  tmem_st16(tmem + lanes + S::TM_O + i * D + c0, o);
+                }
               }
             }
-          }
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          // (all scores are in registers: the weights may go over their columns)
+            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            const float2 mul2 = make_float2(kmul, kmul), sub2 = make_float2(-msub, -msub);
 #pragma unroll
-          for (int c0 = 0; c0 < kTile; c0 += 32) {
-            uint32_t hi[16], lo[WIDE ? 16 : 1];
+            for (int c0 = 0; c0 < kTile; c0 += 32) {
+              uint32_t hi[16], lo[WIDE ? 16 : 1];
 #pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              const float p0 = fast_exp2(fmaf(__uint_as_float(sr[c0 + c]), kmul, -msub));
-              const float p1 = fast_exp2(fmaf(__uint_as_float(sr[c0 + c + 1]), kmul, -msub));
-              sum[c & 2] += p0;
-              sum[(c & 2) + 1] += p1;
-              const __half2 p = __floats2half2_rn(p0, p1);
-              hi[c / 2] = h2_bits(p);
-              if constexpr (WIDE) {
-                const float2 f = __half22float2(p);
-                lo[c / 2] = pack_rn_f16x2(p0 - f.x, p1 - f.y);
+              for (int c = 0; c < 32; c += 2) {
+                float2 p = __ffma2_rn(make_float2(__uint_as_float(sr[c0 + c]), __uint_as_float(sr[c0 + c + 1])), mul2, sub2);
+                p.x = fast_exp2(p.x);
+                p.y = fast_exp2(p.y);
+                sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], p);
+                const __half2 hp = __floats2half2_rn(p.x, p.y);
+                hi[c / 2] = h2_bits(hp);
+                if constexpr (WIDE) {
+                  const float2 f = __half22float2(hp);
+                  lo[c / 2] = pack_rn_f16x2(p.x - f.x, p.y - f.y);
+                }
               }
+              tmem_st16(tm_p + c0 / 2, hi);
+              if constexpr (WIDE) tmem_st16(tm_p + kTile / 2 + c0 / 2, lo);
             }
-            tmem_st16(tm_s + c0 / 2, hi);
-            if constexpr (WIDE) tmem_st16(tm_s + kTile / 2 + c0 / 2, lo);
+            tile_sum = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            if (!__any_sync(0xffffffffu, m == -INFINITY || !(tile_sum <= kMostSum))) break;
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          l += tile_sum;
           tmem_wait_st();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.pready[i]);
+        mbar_arrive_if(&sh.pready[i], lane == 0);
       }
 
       // ---- the segment's result ----
@@ -457,14 +535,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
         sh.ml[i][row][0] = m;
         sh.ml[i][row][1] = l;
       }
-      // (with rows split a stream reads its own outputs only)
-      if (!SPLIT_ROWS || i == 0) {
-        ok = ok && role_wait(&sh.oready[0], o_seen[0] & 1, dead, a.status);
-        ++o_seen[0];
-      }
-      if (have1 && (!SPLIT_ROWS || i == 1)) {
-        ok = ok && role_wait(&sh.oready[1], o_seen[1] & 1, dead, a.status);
-        ++o_seen[1];
+      // the last products of the streams whose outputs this thread reads
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int tiles = seg.u1 - seg.u0, its = SPLIT_ROWS ? tiles : (tiles + 1 - e) / 2;
+        n_both[e] += its;
+        if (its > 0 && (!SPLIT_ROWS || e == i)) ok = ok && role_wait_warp(&sh.pdone[e], (n_both[e] - 1) & 1, dead, a.status);
       }
       ok = barrier_and(1, 256, ok);
       const bool whole = seg.parts == 1;
@@ -489,9 +565,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
 #pragma unroll 1
           for (int c0 = c_begin; c0 < c_begin + COLS; c0 += 16) {
             uint32_t o[16], o1[SPLIT_ROWS ? 1 : 16];
-            tmem_ld16(tmem + lanes + TM_O + (SPLIT_ROWS ? i * D : 0) + c0, o);
+            tmem_ld16(tmem + lanes + S::TM_O + (SPLIT_ROWS ? i * D : 0) + c0, o);
             if constexpr (!SPLIT_ROWS) {
-              if (have1) tmem_ld16(tmem + lanes + TM_O + D + c0, o1);
+              if (have1) tmem_ld16(tmem + lanes + S::TM_O + D + c0, o1);
             }
             tmem_wait_ld();
             if (!live) continue;
@@ -513,32 +589,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
                 *reinterpret_cast<float4*>(a.part_o + prow * D + c0 + c) = x;
             }
           }
-          if (whole && live && nan_met) tree_put_nan<D, FMT>(a, seg, gq, row0 + trow, c_begin, c_begin + COLS);
+          if (whole && live && nan_met) 
+            tree_put_nan<D, FMT>(sh.args, seg.b, h, seg.r.first, seg.r.nodes, len, row0 + trow, c_begin, c_begin + COLS);
           if (!whole && live && (SPLIT_ROWS || i == 0))
             *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(M, L);
         }
         tc_fence_before();
       }
-      if (!whole) {
-        if (tid == 0) a.part_flag[seg.slot] = sh.nan_met;
-        __threadfence();
-        named_barrier(1, 256);
-        if (tid == 0) {
-          const bool last = atomicAdd(a.counters + seg.first_block, 1u) == static_cast<uint32_t>(seg.parts - 1);
-          if (last) a.counters[seg.first_block] = 0u;
-          sh.last = last;
-        }
-        named_barrier(1, 256);
-        if (sh.last && ok) {
-          __threadfence();
-          tree_merge<R, D, FMT>(a, seg, slice, gq, rows, v_scale, sh.merge, tid, 256, [] { named_barrier(1, 256); });
-        }
-        named_barrier(1, 256);  // sh.last and sh.merge are free again
+      if (!whole && tid == 0) {
+        a.part_flag[seg.slot] = sh.nan_met;
+        if (seg.u0 == 0) tree_leave_join(sh.args, seg, ok ? rows : 0, row0);
       }
     }
   }
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -546,15 +611,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(TreeArgs a) {
 
 template <int D, int FMT, bool WIDE, int R>
 cudaError_t launch_tc(const TreeArgs& a, cudaStream_t s) {
-  constexpr int smem = TcSmem<D>::BYTES;
+  constexpr int smem = TcPlan<D, WIDE, R>::BYTES;
+  static_assert(smem + sizeof(TcShared) <= 232448, "shared memory of a thread block");
   auto kern = tree_tc_kernel<D, FMT, WIDE, R>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SharedMemoryOnce once;
+  cudaError_t e = once.set(kern, smem);
   if (e != cudaSuccess) return e;
   constexpr int kMost = kTreePartRows / (2 * R);  // blocks whose partial results fit the workspace
   static_assert(kMost <= kTreeMaxBlocks, "their counters too");
-  const int sms = device_sm_count();
-  kern<<<sms < kMost ? sms : kMost, kThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  const int sms = device_sm_count(), grid = sms < kMost ? sms : kMost;
+  kern<<<grid, kThreads, smem, s>>>(a);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_tree_join(a, grid, R, s);
 }
 
 template <int R>
