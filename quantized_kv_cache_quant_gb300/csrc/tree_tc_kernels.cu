@@ -643,7 +643,11 @@ cudaError_t dispatch_tc(const TreeArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t s) {
-  return a.max_tree * (a.q_heads / a.kv_heads) <= 128 ? dispatch_tc<128>(a, s) : dispatch_tc<256>(a, s);
+  // 256 rows a tile read and convert the keys once for twice the rows, but a request with fewer rows pays for both
+  // streams: it takes an average (host's knowledge: the rows of all requests) above one stream's rows.
+  const int gq = a.q_heads / a.kv_heads;
+  const bool wide_tile = static_cast<long long>(a.n_tokens) * gq > 128ll * a.batch && a.max_tree * gq > 128;
+  return wide_tile ? dispatch_tc<256>(a, s) : dispatch_tc<128>(a, s);
 }
 
 }  // namespace kvq

@@ -43,40 +43,63 @@ for _name, (_args, _res) in _SIG.items():
     _fn.restype = _res
 
 
-def _arg(name: str, t, dtype, shape, device) -> int:
-    """The address of a contiguous tensor of this type, shape (None: any size) and device."""
+# A call's checks cost more host time than the launch itself when each one builds shapes and devices, so they
+# compare plain numbers and leave the wording of a refusal to _refuse.
+_I32, _I64, _F16 = torch.int32, torch.int64, torch.float16
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _refuse(name: str, t, dtype, n, dev) -> None:
     if t.dtype is not dtype:
         raise TypeError(f"{name}: {dtype} expected, not {t.dtype}")
-    s = t.shape
-    if len(s) != len(shape) or any(w is not None and n != w for n, w in zip(s, shape)):
-        raise ValueError(f"{name}: shape {tuple(shape)} expected (None: any), not {tuple(s)}")
+    if t.numel() != n:
+        raise ValueError(f"{name}: {n} elements expected, not {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous tensor expected")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, not on {device}")
+    raise ValueError(f"{name}: on {t.device}, not on cuda:{dev}")
+
+
+def _arg(name: str, t, dtype, n: int, dev: int) -> int:
+    """The address of a contiguous tensor of n elements of this type on device dev."""
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+        _refuse(name, t, dtype, n, dev)
     return t.data_ptr()
 
 
-def _rows(name: str, t, heads: int, dim: int, device):
-    """(address, row stride) of fp16 rows [N, heads, dim] whose rows are contiguous and may lie apart."""
-    if t.dtype is not torch.float16:
-        raise TypeError(f"{name}: torch.float16 expected, not {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name}: shape (N, {heads}, {dim}) expected, not {tuple(t.shape)}")
+def _rows(name: str, t, n, heads: int, dim: int, dev: int):
+    """(address, row stride) of fp16 rows [n, heads, dim] whose rows are contiguous and may lie apart."""
+    if t.dtype is not _F16:
+        raise TypeError(f"{name}: {_F16} expected, not {t.dtype}")
+    if t.shape != (n, heads, dim):
+        raise ValueError(f"{name}: shape {(n, heads, dim)} expected, not {tuple(t.shape)}")
     row, head, one = t.stride()
     if one != 1 or (heads > 1 and head != dim):
         raise ValueError(f"{name}: contiguous [heads, dim] rows expected")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, not on {device}")
-    return t.data_ptr(), row if t.shape[0] > 1 else max(row, heads * dim)
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, not on cuda:{dev}")
+    return t.data_ptr(), row if n > 1 else max(row, heads * dim)
 
 
-def _here(t) -> torch.device:
+def _here(t) -> int:
     """The tensor's device, which has to be the current one: the kernels launch there."""
-    d = t.device
-    if d.type != "cuda" or d.index != torch.cuda.current_device():
-        raise ValueError(f"tensors have to be on the current CUDA device, not on {d}")
-    return d
+    dev = t.get_device()
+    if dev < 0 or dev != _current_device():
+        raise ValueError(f"tensors have to be on the current CUDA device, not on {t.device}")
+    return dev
+
+
+def _on(stream, dev: int):
+    if stream is None and _current_stream is not None:
+        return _current_stream(dev)
+    return _stream(stream)
+
+
+def _table(t):
+    """(batch, max_blocks) of a block table."""
+    if t.dim() != 2:
+        raise ValueError(f"block_table: two dimensions expected, not {tuple(t.shape)}")
+    return t.shape
 
 
 def kv_blocks_resize(block_table, n_held, target_tokens, block_tokens: int, free_blocks, free_count, granted=None,
@@ -87,14 +110,15 @@ def kv_blocks_resize(block_table, n_held, target_tokens, block_tokens: int, free
     free_blocks int32 [num_blocks] (a stack) with free_count int32 [1], granted
     int32 [B] (written 1 or 0) or None."""
     d = _here(block_table)
-    i32 = torch.int32
-    b, width = block_table.shape
-    _check(_lib.kv_blocks_resize(
-        _arg("block_table", block_table, i32, (b, width), d), b, width, _arg("n_held", n_held, i32, (b,), d),
-        _arg("target_tokens", target_tokens, i32, (b,), d), block_tokens,
-        _arg("free_blocks", free_blocks, i32, (None,), d), _arg("free_count", free_count, i32, (1,), d),
-        free_blocks.shape[0], None if granted is None else _arg("granted", granted, i32, (b,), d), _stream(stream)),
-        "kv_blocks_resize")
+    b, width = _table(block_table)
+    blocks = free_blocks.numel()
+    code = _lib.kv_blocks_resize(
+        _arg("block_table", block_table, _I32, b * width, d), b, width, _arg("n_held", n_held, _I32, b, d),
+        _arg("target_tokens", target_tokens, _I32, b, d), block_tokens, _arg("free_blocks", free_blocks, _I32, blocks, d),
+        _arg("free_count", free_count, _I32, 1, d), blocks,
+        None if granted is None else _arg("granted", granted, _I32, b, d), _on(stream, d))
+    if code:
+        _check(code, "kv_blocks_resize")
 
 
 def kv_slot_map(block_table, seq_lens, new_lens, block_tokens: int, num_blocks: int, offsets, slots, seq_ids=None,
@@ -103,28 +127,27 @@ def kv_slot_map(block_table, seq_lens, new_lens, block_tokens: int, num_blocks: 
     offsets int32 [B + 1], slots int64 [N] and, where given, seq_ids and
     positions int32 [N]; rows behind the last request become -1."""
     d = _here(block_table)
-    i32 = torch.int32
-    b, width = block_table.shape
-    n = slots.shape[0]
-    _check(_lib.kv_slot_map(
-        _arg("block_table", block_table, i32, (b, width), d), b, width, _arg("seq_lens", seq_lens, i32, (b,), d),
-        _arg("new_lens", new_lens, i32, (b,), d), block_tokens, num_blocks, n,
-        _arg("offsets", offsets, i32, (b + 1,), d), _arg("slots", slots, torch.int64, (n,), d),
-        None if seq_ids is None else _arg("seq_ids", seq_ids, i32, (n,), d),
-        None if positions is None else _arg("positions", positions, i32, (n,), d), _stream(stream)), "kv_slot_map")
+    b, width = _table(block_table)
+    n = slots.numel()
+    code = _lib.kv_slot_map(
+        _arg("block_table", block_table, _I32, b * width, d), b, width, _arg("seq_lens", seq_lens, _I32, b, d),
+        _arg("new_lens", new_lens, _I32, b, d), block_tokens, num_blocks, n, _arg("offsets", offsets, _I32, b + 1, d),
+        _arg("slots", slots, _I64, n, d), None if seq_ids is None else _arg("seq_ids", seq_ids, _I32, n, d),
+        None if positions is None else _arg("positions", positions, _I32, n, d), _on(stream, d))
+    if code:
+        _check(code, "kv_slot_map")
 
 
 def fp8_kv_append(k_pool, v_pool, k_new, v_new, slots, stream=None) -> None:
     """Quantize tokens k_new, v_new fp16 [N, H, D] (rows may lie apart) with the
     pools' scales into the rows that slots int64 [N] names (-1: skipped)."""
     d = _here(k_new)
-    kp, ks = _rows("k_new", k_new, k_pool.kv_heads, k_pool.head_dim, d)
-    vp, vs = _rows("v_new", v_new, k_pool.kv_heads, k_pool.head_dim, d)
-    n = k_new.shape[0]
-    if v_new.shape[0] != n:
-        raise ValueError(f"v_new: {n} rows expected, not {v_new.shape[0]}")
-    _check(_lib.fp8_kv_append(k_pool, v_pool, kp, ks, vp, vs, _arg("slots", slots, torch.int64, (n,), d), n,
-                              _stream(stream)), "fp8_kv_append")
+    n, h, dim = slots.numel(), k_pool.kv_heads, k_pool.head_dim
+    kp, ks = _rows("k_new", k_new, n, h, dim, d)
+    vp, vs = _rows("v_new", v_new, n, h, dim, d)
+    code = _lib.fp8_kv_append(k_pool, v_pool, kp, ks, vp, vs, _arg("slots", slots, _I64, n, d), n, _on(stream, d))
+    if code:
+        _check(code, "fp8_kv_append")
 
 
 def fp8_kv_accept(k_pool, v_pool, block_table, seq_lens, path, n_accepted, new_lens, stream=None) -> None:
@@ -132,13 +155,16 @@ def fp8_kv_accept(k_pool, v_pool, block_table, seq_lens, path, n_accepted, new_l
     n_accepted[b] of a row count) to the end of each sequence and write
     new_lens = seq_lens + n_accepted (new_lens may be seq_lens)."""
     d = _here(block_table)
-    i32 = torch.int32
-    b, width = block_table.shape
-    _check(_lib.fp8_kv_accept(
-        k_pool, v_pool, _arg("block_table", block_table, i32, (b, width), d), b, width,
-        _arg("seq_lens", seq_lens, i32, (b,), d), _arg("path", path, i32, (b, None), d), path.shape[1],
-        _arg("n_accepted", n_accepted, i32, (b,), d), _arg("new_lens", new_lens, i32, (b,), d), _stream(stream)),
-        "fp8_kv_accept")
+    b, width = _table(block_table)
+    if path.dim() != 2 or path.shape[0] != b:
+        raise ValueError(f"path: shape ({b}, P) expected, not {tuple(path.shape)}")
+    p = path.shape[1]
+    code = _lib.fp8_kv_accept(
+        k_pool, v_pool, _arg("block_table", block_table, _I32, b * width, d), b, width,
+        _arg("seq_lens", seq_lens, _I32, b, d), _arg("path", path, _I32, b * p, d), p,
+        _arg("n_accepted", n_accepted, _I32, b, d), _arg("new_lens", new_lens, _I32, b, d), _on(stream, d))
+    if code:
+        _check(code, "fp8_kv_accept")
 
 
 def fp8_tree_workspace_bytes(batch: int, kv_heads: int, q_heads: int, head_dim: int, max_tree: int) -> int:
@@ -154,17 +180,22 @@ def fp8_tree_attention(q, k_pool, v_pool, block_table, seq_lens, tree_offsets, t
     [N, Hq, D]; tree_offsets int32 [B + 1]; ws uint8, zeroed once, at least
     fp8_tree_workspace_bytes."""
     d = _here(q)
-    i32 = torch.int32
     n, hq, dim = q.shape
-    qp, qs = _rows("q", q, hq, k_pool.head_dim, d)
-    b, width = block_table.shape
-    wide = out.dtype is torch.float32
-    _check(_lib.fp8_tree_attention(
-        qp, qs, n, k_pool, v_pool, _arg("block_table", block_table, i32, (b, width), d),
-        _arg("seq_lens", seq_lens, i32, (b,), d), _arg("tree_offsets", tree_offsets, i32, (b + 1,), d),
-        _arg("tree_mask", tree_mask, torch.int64, (n, None), d), tree_mask.shape[1], b, hq, width, max_tree, max_seq_len,
-        _arg("out", out, torch.float32 if wide else torch.float16, (n, hq, dim), d), int(wide), softmax_scale,
-        _arg("ws", ws, torch.uint8, (None,), d), ws.shape[0], _stream(stream)), "fp8_tree_attention")
+    qp, qs = _rows("q", q, n, hq, k_pool.head_dim, d)
+    b, width = _table(block_table)
+    if tree_mask.dim() != 2 or tree_mask.shape[0] != n:
+        raise ValueError(f"tree_mask: shape ({n}, words) expected, not {tuple(tree_mask.shape)}")
+    if out.shape != q.shape:
+        raise ValueError(f"out: shape {tuple(q.shape)} expected, not {tuple(out.shape)}")
+    words, wide, size = tree_mask.shape[1], out.dtype is torch.float32, ws.numel()
+    code = _lib.fp8_tree_attention(
+        qp, qs, n, k_pool, v_pool, _arg("block_table", block_table, _I32, b * width, d),
+        _arg("seq_lens", seq_lens, _I32, b, d), _arg("tree_offsets", tree_offsets, _I32, b + 1, d),
+        _arg("tree_mask", tree_mask, _I64, n * words, d), words, b, hq, width, max_tree, max_seq_len,
+        _arg("out", out, torch.float32 if wide else _F16, n * hq * dim, d), int(wide), softmax_scale,
+        _arg("ws", ws, torch.uint8, size, d), size, _on(stream, d))
+    if code:
+        _check(code, "fp8_tree_attention")
 
 
 class BlockTables:
