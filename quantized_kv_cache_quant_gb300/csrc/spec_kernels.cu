@@ -1,6 +1,7 @@
 // Serving-step kernels of the paged caches for sm_103a: block tables and slot
 // maps from request lengths, the append of new tokens into the FP8 pools by
 // slot, and the move of an accepted path (kvq_spec.h).
+#include <climits>
 #include <cooperative_groups.h>
 
 #include "kvq_device.cuh"
@@ -115,19 +116,47 @@ __global__ void __launch_bounds__(1024) blocks_resize_kernel(BlocksResizeArgs a)
   const int grown = grown_s;
 
   const int threads = blockDim.x * cluster.num_blocks(), me = cluster.block_rank() * blockDim.x + threadIdx.x;
-  for (int i = me; i < released; i += threads) {
-    const int b = owner_of(a.batch, i, [&](int m) { return drop_s[m]; });
-    int32_t* entry = a.block_table + static_cast<long long>(b) * a.max_blocks + want_s[b] + (i - drop_s[b]);
-    const int place = top - 1 - i;
-    if (place >= 0) a.free_blocks[place] = *entry;
-    *entry = -1;
+  // A warp takes 128 neighbouring entries, a lane four of them 32 apart: their reads are in flight together.
+  const int first = (me & ~31) * 4 + (me & 31);
+  for (int i0 = first; i0 < released; i0 += 4 * threads) {
+    int b = owner_of(a.batch, i0, [&](int m) { return drop_s[m]; });
+    int32_t* entry[4];
+    int32_t block[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      entry[e] = nullptr;
+      if (i0 + 32 * e < released) {
+        while (b + 1 < a.batch && i0 + 32 * e >= drop_s[b + 1]) ++b;
+        entry[e] = a.block_table + static_cast<long long>(b) * a.max_blocks + want_s[b] + (i0 + 32 * e - drop_s[b]);
+        block[e] = *entry[e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (entry[e] == nullptr) continue;
+      const int place = top - 1 - (i0 + 32 * e);
+      if (place >= 0) a.free_blocks[place] = block[e];
+      *entry[e] = -1;
+    }
   }
   cluster.sync();
-  for (int i = me; i < grown; i += threads) {
+  for (int i0 = first; i0 < grown; i0 += 4 * threads) {
     // growth is granted in order until it is refused for good: what the granted requests asked for is their place
-    const int b = owner_of(a.batch, i, [&](int m) { return min(ask_s[m], grown); });
-    a.block_table[static_cast<long long>(b) * a.max_blocks + held_s[b] + (i - ask_s[b])] =
-        __ldcg(a.free_blocks + (top - 1 - i));
+    int b = owner_of(a.batch, i0, [&](int m) { return min(ask_s[m], grown); });
+    int32_t* entry[4];
+    int32_t block[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      entry[e] = nullptr;
+      if (i0 + 32 * e < grown) {
+        while (b + 1 < a.batch && i0 + 32 * e >= ask_s[b + 1]) ++b;
+        entry[e] = a.block_table + static_cast<long long>(b) * a.max_blocks + held_s[b] + (i0 + 32 * e - ask_s[b]);
+        block[e] = __ldcg(a.free_blocks + (top - 1 - (i0 + 32 * e)));
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (entry[e] != nullptr) *entry[e] = block[e];
   }
   // every block has read the old counts before the barrier
   if (cluster.block_rank() == 0) {
@@ -166,38 +195,58 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(SlotMapArgs a) {
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b <= a.batch; b += kMapThreads) a.offsets[b] = off_s[b];
 
-  for (int i0 = 4 * (blockIdx.x * kMapThreads + threadIdx.x); i0 < a.n_rows; i0 += 4 * gridDim.x * kMapThreads) {
+  const int lane = threadIdx.x & 31;
+  // (64 bits: the last step may pass 2^31)
+  for (long long first = 4ll * (blockIdx.x * kMapThreads + (threadIdx.x & ~31)); first < a.n_rows;
+       first += 4ll * gridDim.x * kMapThreads) {
+    const int i0 = static_cast<int>(min(first + 4 * lane, static_cast<long long>(a.n_rows)));
     long long slot[4];
     int seq[4], pos[4];
     int b = i0 < n ? owner_of(a.batch, i0, [&](int m) { return off_s[m]; }) : 0;
-    int held_at = -1, block = -1;
+    // positions that leave 31 bits lie outside every table
+    int next = i0 < n ? off_s[b + 1] : 0, j = 0, block = -1;
+    long long p = 0;
+    int row = 0;  // p's row in its block
+    bool fresh = true;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int i = i0 + e;
       slot[e] = seq[e] = pos[e] = -1;
       if (i < n) {
-        while (i >= off_s[b + 1]) {
-          ++b;
-          held_at = -1;
+        while (i >= next) {
+          next = off_s[++b + 1];
+          fresh = true;
         }
-        const long long p = static_cast<long long>(a.seq_lens[b]) + (i - off_s[b]);
+        if (fresh) {  // the one division of most threads
+          p = static_cast<long long>(a.seq_lens[b]) + (i - off_s[b]);
+          j = p >= 0 && p <= INT_MAX ? static_cast<int>(p) / a.block_tokens : a.max_blocks;
+          row = static_cast<int>(p - static_cast<long long>(j) * a.block_tokens);
+        } else {
+          ++p;
+          if (++row == a.block_tokens) {
+            row = 0;
+            ++j;
+            fresh = true;
+          }
+        }
+        if (fresh) block = j < a.max_blocks && p <= INT_MAX ? a.block_table[static_cast<long long>(b) * a.max_blocks + j] : -1;
+        fresh = false;
         seq[e] = b;
         pos[e] = static_cast<int>(p);
-        const long long j = p / a.block_tokens;
-        if (p >= 0 && j < a.max_blocks) {
-          if (j != held_at) {
-            held_at = static_cast<int>(j);
-            block = a.block_table[static_cast<long long>(b) * a.max_blocks + j];
-          }
-          if (block >= 0 && block < a.num_blocks)
-            slot[e] = static_cast<long long>(block) * a.block_tokens + (p - j * a.block_tokens);
-        }
+        if (block >= 0 && block < a.num_blocks) slot[e] = static_cast<long long>(block) * a.block_tokens + row;
       }
     }
-    if (i0 + 3 < a.n_rows) {
-      longlong2* s2 = reinterpret_cast<longlong2*>(a.slots + i0);
-      s2[0] = make_longlong2(slot[0], slot[1]);
-      s2[1] = make_longlong2(slot[2], slot[3]);
+    if (first + 127 < a.n_rows) {
+      // slots change lanes so that each store covers 512 neighbouring bytes (a thread's own 32 would be written as
+      // two halves of its sector: 2.2 million rows in 11.9 us, so in 10.9)
+      longlong2* s2 = reinterpret_cast<longlong2*>(a.slots + first);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int from = 16 * half + (lane >> 1);
+        const long long lo0 = __shfl_sync(0xffffffffu, slot[0], from), lo1 = __shfl_sync(0xffffffffu, slot[1], from);
+        const long long hi0 = __shfl_sync(0xffffffffu, slot[2], from), hi1 = __shfl_sync(0xffffffffu, slot[3], from);
+        s2[32 * half + lane] = (lane & 1) ? make_longlong2(hi0, hi1) : make_longlong2(lo0, lo1);
+      }
       if (a.seq_ids) *reinterpret_cast<int4*>(a.seq_ids + i0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
       if (a.positions) *reinterpret_cast<int4*>(a.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
     } else {
@@ -338,17 +387,23 @@ __global__ void __launch_bounds__(32 * kAppendWarps) fp8_append_kernel(Fp8Append
 }
 
 // ---------------------------------------------------------------------------
-// Accept. One thread block per request; a thread owns one column (a 16-byte
-// key unit or 4 value bytes of one head) of every token row. A path ascends,
-// so row i's place seq_len + i is at or before its source and before every
-// later source: a thread that moves its column row by row in order never reads
-// what it has overwritten, and no two threads share a byte.
+// Accept. One thread block per request. A path ascends, so row i's place seq_len
+// + i is at or before its source and before every later source: moving rows in
+// order never reads what has been overwritten.
+//   keys  : a thread owns one column (a 16-byte unit of one head) of every row
+//   values: a unit holds 4 tokens of 4 channels, so a row alone is 4 single
+//           bytes a unit; a warp takes one 512-byte chunk (32 channels of a head,
+//           16 tokens) of a place block at a time, each lane gathers its unit's
+//           bytes from the units of their sources (of the same channels, so the
+//           same warp's) and writes the unit whole. Byte by byte this took 18 us
+//           for 256 requests x 8 rows: 2.1 million writes of parts of sectors.
 // ---------------------------------------------------------------------------
 constexpr int kAcceptBatch = 8;
 
 template <int D>
 __global__ void __launch_bounds__(512) fp8_accept_kernel(Fp8AcceptArgs a) {
-  __shared__ int src_blk[kTreeMax], dst_blk[kTreeMax], rows[kTreeMax];  // rows: source row | place row << 8
+  // of row i: source block (-1: stays), place block, source row | place row << 8
+  __shared__ int src_blk[kTreeMax], dst_blk[kTreeMax], rows[kTreeMax];
   const int b = blockIdx.x;
   const int len = a.seq_lens[b];
   const int n = min(max(a.n_accepted[b], 0), a.path_len);
@@ -369,46 +424,64 @@ __global__ void __launch_bounds__(512) fp8_accept_kernel(Fp8AcceptArgs a) {
   }
   __syncthreads();
   if (threadIdx.x == 0) a.new_lens[b] = len + n;  // (this block alone reads seq_lens[b])
-  constexpr int KU = D / 16, VU = D / 4;
-  const int k_cols = a.kv_heads * KU, cols = a.kv_heads * (KU + VU);
-  for (int col = threadIdx.x; col < cols; col += blockDim.x) {
-    const bool key = col < k_cols;
-    const int h = key ? col / KU : (col - k_cols) / VU, u = key ? col % KU : (col - k_cols) % VU;
-    auto at = [&](int blk, int t) -> long long {
-      const int in_block = key ? ((t / 8 * (D / 64) + u / 4) * 32 + 4 * (t % 8) + u % 4) * 16
-                               : (u / 8 * 32 + 4 * (u % 8) + t % 8 / 2) * 16 + t / 8 * 2 + t % 2;
-      return (static_cast<long long>(blk) * a.kv_heads + h) * (kBlock * D) + in_block;
-    };
-    for (int i0 = 0; i0 < n; i0 += kAcceptBatch) {
-      uint4 v[kAcceptBatch];
+  if (len < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  constexpr int KU = D / 16, CH = D / 32;
+  const int k_tasks = (a.kv_heads * KU + 31) / 32, tasks = k_tasks + a.kv_heads * CH;
+  for (int task = warp; task < tasks; task += warps) {
+    if (task < k_tasks) {
+      const int col = task * 32 + lane, h = col / KU, u = col % KU;
+      if (h >= a.kv_heads) continue;
+      auto unit = [&](int blk, int t) {
+        return reinterpret_cast<uint4*>(a.k_pool + (static_cast<long long>(blk) * a.kv_heads + h) * (kBlock * D) +
+                                        ((t / 8 * (D / 64) + u / 4) * 32 + 4 * (t % 8) + u % 4) * 16);
+      };
+      for (int i0 = 0; i0 < n; i0 += kAcceptBatch) {
+        uint4 v[kAcceptBatch];
 #pragma unroll
-      for (int e = 0; e < kAcceptBatch; ++e) {
-        const int i = i0 + e;
-        if (i < n && src_blk[i] >= 0) {
-          const long long s = at(src_blk[i], rows[i] & 255);
-          if (key) {
-            v[e] = *reinterpret_cast<const uint4*>(a.k_pool + s);
-          } else {
-            const uint8_t* p = a.v_pool + s;
-            v[e].x = p[0] | (p[4] << 8) | (p[8] << 16) | (static_cast<uint32_t>(p[12]) << 24);
-          }
-        }
+        for (int e = 0; e < kAcceptBatch; ++e)
+          if (i0 + e < n && src_blk[i0 + e] >= 0) v[e] = *unit(src_blk[i0 + e], rows[i0 + e] & 255);
+#pragma unroll
+        for (int e = 0; e < kAcceptBatch; ++e)
+          if (i0 + e < n && src_blk[i0 + e] >= 0) *unit(dst_blk[i0 + e], rows[i0 + e] >> 8) = v[e];
       }
+    } else {
+      const int h = (task - k_tasks) / CH, c = (task - k_tasks) % CH, tig = lane & 3;
+      auto unit = [&](int blk, int in_chunk) {
+        return reinterpret_cast<uint4*>(a.v_pool + (static_cast<long long>(blk) * a.kv_heads + h) * (kBlock * D) +
+                                        (c * 32 + in_chunk) * 16);
+      };
+      // place blocks in order: what a later one's rows come from lies behind every place of an earlier one
+      for (int p0 = len / kBlock * kBlock; p0 < len + n; p0 += kBlock) {
+        uint4 src[4];
+        int shift[4], place = -1;
 #pragma unroll
-      for (int e = 0; e < kAcceptBatch; ++e) {
-        const int i = i0 + e;
-        if (i < n && src_blk[i] >= 0) {
-          const long long d = at(dst_blk[i], rows[i] >> 8);
-          if (key) {
-            *reinterpret_cast<uint4*>(a.k_pool + d) = v[e];
-          } else {
-            uint8_t* p = a.v_pool + d;
-            p[0] = static_cast<uint8_t>(v[e].x);
-            p[4] = static_cast<uint8_t>(v[e].x >> 8);
-            p[8] = static_cast<uint8_t>(v[e].x >> 16);
-            p[12] = static_cast<uint8_t>(v[e].x >> 24);
+        for (int e = 0; e < 4; ++e) {  // the unit's tokens: byte e of each word is token 8 (e / 2) + 2 tig + e % 2
+          const int i = p0 + 8 * (e >> 1) + 2 * tig + (e & 1) - len;
+          shift[e] = -1;
+          if (i >= 0 && i < n && src_blk[i] >= 0) {
+            const int from = rows[i] & 255;
+            shift[e] = 8 * (from / 8 * 2 + from % 2);
+            src[e] = *unit(src_blk[i], (lane & ~3) + from % 8 / 2);
+            place = dst_blk[i];
           }
         }
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (place >= 0) w = *unit(place, lane);
+        __syncwarp();  // every lane has read before one writes
+        if (place >= 0) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (shift[e] < 0) continue;
+            const uint32_t sel = 0x3210u ^ ((e ^ 4u) << (4 * e));  // byte e from the second word's byte 0
+            w.x = __byte_perm(w.x, src[e].x >> shift[e], sel);
+            w.y = __byte_perm(w.y, src[e].y >> shift[e], sel);
+            w.z = __byte_perm(w.z, src[e].z >> shift[e], sel);
+            w.w = __byte_perm(w.w, src[e].w >> shift[e], sel);
+          }
+          *unit(place, lane) = w;
+        }
+        __syncwarp();
       }
     }
   }
@@ -425,7 +498,8 @@ cudaError_t launch_blocks_resize(const BlocksResizeArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = small ? 1 : 8;
+  // tables of more than 16K entries: 16 blocks (7.4 us for 135K changed entries; 8, the portable most, take 10.5)
+  attr.val.clusterDim.x = small ? 1 : 16;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.gridDim = dim3(attr.val.clusterDim.x);
   cfg.blockDim = dim3(small ? 256 : 1024);
@@ -433,6 +507,27 @@ cudaError_t launch_blocks_resize(const BlocksResizeArgs& a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  if (!small) {
+    static std::atomic<int> fits[SharedMemoryOnce::kDevices] = {};  // 16 blocks: 1 they do, -1 they do not
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int f = dev < SharedMemoryOnce::kDevices ? fits[dev].load(std::memory_order_relaxed) : 0;
+    if (f == 0) {
+      e = cudaFuncSetAttribute(blocks_resize_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      cudaLaunchConfig_t most = cfg;
+      most.dynamicSmemBytes = 4 * kSpecMaxBatch * sizeof(int);
+      int clusters = 0;
+      f = cudaOccupancyMaxActiveClusters(&clusters, blocks_resize_kernel, &most) == cudaSuccess && clusters > 0 ? 1 : -1;
+      if (f < 0) (void)cudaGetLastError();
+      if (dev < SharedMemoryOnce::kDevices) fits[dev].store(f, std::memory_order_relaxed);
+    }
+    if (f < 0) {
+      attr.val.clusterDim.x = 8;
+      cfg.gridDim = dim3(8);
+    }
+  }
   e = cudaLaunchKernelEx(&cfg, blocks_resize_kernel, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -465,8 +560,9 @@ cudaError_t launch_fp8_append(const Fp8AppendArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_fp8_accept(const Fp8AcceptArgs& a, cudaStream_t s) {
-  const long long cols = static_cast<long long>(a.kv_heads) * (a.head_dim / 16 + a.head_dim / 4);
-  const int threads = static_cast<int>(cols < 512 ? (cols + 31) / 32 * 32 : 512);
+  const long long tasks = (static_cast<long long>(a.kv_heads) * (a.head_dim / 16) + 31) / 32 +
+                          static_cast<long long>(a.kv_heads) * (a.head_dim / 32);
+  const int threads = static_cast<int>(32 * (tasks < 16 ? tasks : 16));
   if (a.head_dim == 128)
     fp8_accept_kernel<128><<<a.batch, threads, 0, s>>>(a);
   else
