@@ -486,6 +486,16 @@ __global__ void __launch_bounds__(128) fp8_decode_kernel(Fp8DecodeArgs a) {
       vw[4 * c + 2] = x.z;
       vw[4 * c + 3] = x.w;
     }
+    if (tok_base + kBlock > len) {
+      // Rows behind the sequence weigh 0, but they may hold anything (fp8_kv_append leaves them as they are), a NaN
+      // among it: take them as 0.
+      uint32_t keep = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (tok_base + 8 * (i >> 1) + 2 * tig + (i & 1) < len) keep |= 0xFFu << (8 * i);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) vw[nt] &= keep;
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
       mma16816(o_acc[nt], A0, A1, A2, A3, fp8_lo_pair<FMT>(vw[nt]), fp8_hi_pair<FMT>(vw[nt]));

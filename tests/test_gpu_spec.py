@@ -515,6 +515,41 @@ def test_tree_one_node_matches_decode():
     assert np.abs(got - host(out)).max() <= 2e-5       # both a few 1e-6 from the 64-bit result on unit-size values
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_decode_after_append_does_not_read_stale_rows(dim, fmt):
+    """A cache filled by appends alone, in blocks that held NaN before: the rows behind each sequence stay as they were,
+    and the single-token decode does not see them either."""
+    import torch
+    kvq, spec = _mods()
+    rng = np.random.default_rng(33)
+    b, h, hq, lens = 3, 2, 8, [1, 19, 45]
+    p = Pools(rng, 12, h, dim, fmt, False, fill=0x7F)
+    table = rng.permutation(12)[:9].reshape(3, 3).astype(np.int32)
+    new = torch.empty(sum(lens), dtype=torch.int64, device="cuda")
+    off = torch.empty(b + 1, dtype=torch.int32, device="cuda")
+    spec.kv_slot_map(dev(table), i32([0] * b), i32(lens), 16, 12, off, new)
+    x = rng.standard_normal((2, sum(lens), h, dim)).astype(np.float16)
+    spec.fp8_kv_append(*p.descs, dev(x[0]), dev(x[1]), new)
+    q = rng.standard_normal((b, hq, dim)).astype(np.float16)
+    out = torch.empty((b, hq, dim), dtype=torch.float32, device="cuda")
+    n = kvq.fp8_decode_workspace_bytes(b, hq, dim)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    for q_fp8 in (False, True):
+        kvq.fp8_decode_attention(dev(q), *p.descs, dev(table), i32(lens), b, hq, 3, 48, out, True, 0.0, ws, n, q_fp8=q_fp8)
+        got = host(out)
+        qq = fp8.query_hat(*fp8.quantize_query(q)) if q_fp8 else q.astype(np.float64)
+        at = 0
+        for bi, m in enumerate(lens):
+            kk, vv = (fp8.decode(fp8.quantize(x[r, at:at + m].transpose(1, 0, 2)[None], p.scale[r][0], fmt)[0], fmt) *
+                      np.float64(p.scale[r][0]) for r in range(2))
+            at += m
+            for g in range(hq):
+                s = kk[g // 4] @ qq[bi, g] / np.sqrt(dim)
+                w = np.exp(s - s.max())
+                assert np.abs(got[bi, g] - w @ vv[g // 4] / w.sum()).max() <= 2e-3
+
+
 def test_tree_same_call_twice_gives_the_same_bits():
     import torch
     kvq, spec = _mods()
