@@ -57,11 +57,15 @@ struct TcPlan {
   static constexpr int STAGE = 2 * kTile * D;       // pool bytes of a tile: keys, then values
   static constexpr int TILE = kTile * D * 2;        // one fp16 tile of keys or values
   static constexpr int Q_TILE = 128 * D * 2;
-  static constexpr int BUFS = Q_SMEM == 2 ? 3 : kMaxBufs;
+  // Both rings have an even number of places: the converting pairs take tiles of alternate parity, and so a place
+  // always belongs to one pair, which sees each phase of its barriers. (In an odd ring a pair meets a place every second
+  // time round, and its wait for a phase's parity is over while the phase before still runs.)
+  static constexpr int BUFS = Q_SMEM == 2 ? 2 : kMaxBufs;  // (2 in place of 4: 690 / 536 / 340 us for 492 / 448 / 244)
   static constexpr int FIXED = BUFS * 2 * TILE + Q_SMEM * Q_TILE;
   static constexpr int FIT = (221184 - FIXED) / STAGE;  // 227 KB without what TcShared takes
-  static constexpr int STAGES = FIT < kMaxStages ? FIT : kMaxStages;
+  static constexpr int STAGES = (FIT < kMaxStages ? FIT : kMaxStages) & ~1;
   static_assert(STAGES >= 2, "room for the copies");
+  static_assert(STAGES % 2 == 0 && BUFS % 2 == 0, "a place of a ring belongs to one converting pair");
   static constexpr int K_OFF = STAGES * STAGE, V_OFF = K_OFF + BUFS * TILE, Q_OFF = V_OFF + BUFS * TILE;
   static constexpr int BYTES = Q_OFF + Q_SMEM * Q_TILE;
   // tensor memory columns
@@ -199,10 +203,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         }
       }
     }
-    if (!ok || *dead) {  // no copy of this block is in flight when it ends
-      for (unsigned k = n > kStages ? n - kStages : 0; k < n; ++k)
-        (void)mbar_wait_bounded(&sh.full[k % kStages], (k / kStages) & 1);
-    }
+    // no copy of this block is in flight when it ends, whichever role gave up
+    for (unsigned k = n > kStages ? n - kStages : 0; k < n; ++k)
+      (void)mbar_wait_bounded(&sh.full[k % kStages], (k / kStages) & 1);
   } else if (warp == kScoreWarp) {
     // ---- scores: one thread; S_i = Q_i K(tile)^T once the scores before are read ----
     if (elect_one()) {
@@ -252,10 +255,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
           if (!ok) break;
         }
       }
-      if (!ok) {  // no MMA of this thread is in flight when the block frees its tensor memory
-        tc_commit(&sh.drain[0]);
-        (void)mbar_wait_bounded(&sh.drain[0], 0);
-      }
+      // no MMA of this thread is in flight when the block frees its tensor memory, whichever role gave up
+      tc_commit(&sh.drain[0]);
+      (void)mbar_wait_bounded(&sh.drain[0], 0);
     }
     __syncwarp();
   } else if (warp >= kOutputWarp) {
@@ -287,10 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         }
         n += tiles;
       }
-      if (!ok) {
-        tc_commit(&sh.drain[1 + i]);
-        (void)mbar_wait_bounded(&sh.drain[1 + i], 0);
-      }
+      tc_commit(&sh.drain[1 + i]);
+      (void)mbar_wait_bounded(&sh.drain[1 + i], 0);
     }
     __syncwarp();
   } else if (warp >= kConvertWarp) {
