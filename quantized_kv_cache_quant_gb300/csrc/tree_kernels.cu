@@ -68,9 +68,7 @@ __global__ void __launch_bounds__(128) tree_rows16_kernel(const __grid_constant_
   }
   __syncthreads();
   TreeWalk walk;
-  walk.at = slice.begin;
-  walk.before = slice.before;
-  walk.b = slice.b;
+  walk.start(slice);
   const TreeSegment& seg = walk.seg;
   unsigned it = 0;         // blocks this warp has taken through its ring
   bool dead = false;       // a wait ran out: no more copies

@@ -135,18 +135,28 @@ struct TreeWalk {
   long long at, before;
   int b;
   TreeSegment seg;
+
+  __device__ __forceinline__ void start(const TreeSlice& s) {
+    at = s.begin;
+    before = s.before;
+    b = s.b;
+    seg.b = -1;
+  }
 };
 
 // Walks a slice's segments: w.at is the unit to go on from, w.b and w.before
-// its request. Out of line: the roles of a thread block share one copy (their
-// hot loops and five inlined copies together did not fit the instruction cache).
+// its request, w.seg.r that request once w.seg.b names it. Out of line: the
+// roles of a thread block share one copy (their hot loops and five inlined
+// copies together did not fit the instruction cache). Between two segments every
+// role waits for this, so it reads a request once, not once a pair, and divides
+// in 64 bits only for pairs that blocks share.
 template <int R, int UNIT>
 __device__ __noinline__ bool next_segment(const TreeArgs& a, const TreeSlice& s, TreeWalk& w) {
   long long at = w.at, before = w.before;
   int b = w.b;
   TreeSegment& g = w.seg;
   if (at >= s.end) return false;
-  g.r = tree_request<R, UNIT>(a, b);
+  if (g.b != b) g.r = tree_request<R, UNIT>(a, b);
   long long n = static_cast<long long>(g.r.units) * g.r.tiles * a.kv_heads;
   while (at >= before + n) {  // requests without nodes have no units
     before += n;
@@ -154,7 +164,8 @@ __device__ __noinline__ bool next_segment(const TreeArgs& a, const TreeSlice& s,
     g.r = tree_request<R, UNIT>(a, b);
     n = static_cast<long long>(g.r.units) * g.r.tiles * a.kv_heads;
   }
-  const int pair = static_cast<int>((at - before) / g.r.units);
+  const unsigned long long in = static_cast<unsigned long long>(at - before);
+  const int pair = in >> 32 ? static_cast<int>(in / g.r.units) : static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(g.r.units));
   g.b = b;
   g.h = pair / g.r.tiles;
   g.tile = pair % g.r.tiles;
@@ -162,7 +173,8 @@ __device__ __noinline__ bool next_segment(const TreeArgs& a, const TreeSlice& s,
   g.u0 = static_cast<int>(at - g.pair_begin);
   g.u1 = static_cast<int>(min(s.end - g.pair_begin, static_cast<long long>(g.r.units)));
   g.slot = 2 * static_cast<int>(blockIdx.x) + (at == s.begin ? 0 : 1);
-  g.parts = s.block_of(g.pair_begin + g.r.units - 1) - s.block_of(g.pair_begin) + 1;
+  g.parts = 1;
+  if (g.u0 != 0 || g.u1 != g.r.units) g.parts = s.block_of(g.pair_begin + g.r.units - 1) - s.block_of(g.pair_begin) + 1;
   w.at = g.pair_begin + g.u1;
   w.before = before;
   w.b = b;

@@ -149,11 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     const TreeSlice s = tree_slice<R, kTile>(a, sh.plan, 2);
     if (static_cast<int>(blockIdx.x) >= s.blocks) return;
     if (tid == 0) sh.slice = s;
-    if (lane == 0) {
-      sh.walk[warp].at = s.begin;
-      sh.walk[warp].before = s.before;
-      sh.walk[warp].b = s.b;
-    }
+    if (lane == 0) sh.walk[warp].start(s);
   }
   if (warp == kScoreWarp) {
     tmem_alloc(&sh.tmem, 512);
@@ -398,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       const int trow = SPLIT_ROWS ? row + 128 * i : row;      // row of the tile
       const bool live = row < my_rows;
       const bool warp_live = (row & ~31) < my_rows;
-      const int node = live ? (row0 + trow) / gq : 0;
+      const int node = live ? (row0 + trow) / gq : 0, head = live ? row0 + trow - node * gq : 0;
       const float k_scale = a.k_scale[a.per_head ? h : 0], v_scale = a.v_scale[a.per_head ? h : 0];
       // a negative scale turns the query's signs, so that larger scores stay larger
       float kmul = fabsf(k_scale) * a.scale_log2;
@@ -406,21 +402,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       const uint32_t flip = k_scale < 0.0f ? 0x80008000u : 0u;
       const uint64_t* mask = a.tree_mask + static_cast<long long>(seg.r.first + node) * a.mask_words;
 
-      if (ok) {  // the query row, its channels in the key units' order (R = 128: once for both streams)
+      if (ok) {  // the query row, its channels in the key units' order (R = 128: each stream brings half of them)
         const __half* q = reinterpret_cast<const __half*>(a.q) + (seg.r.first + node) * a.q_stride +
-                          static_cast<long long>(h * gq + (live ? (row0 + trow) % gq : 0)) * D;
-        if (SPLIT_ROWS || i == 0) {
-#pragma unroll
-          for (int kh = 0; kh < D / 64; ++kh) {
+                          static_cast<long long>(h * gq + head) * D;
+        constexpr bool HALVES = !SPLIT_ROWS && D == 128;
+        if (SPLIT_ROWS || HALVES || i == 0) {
+#pragma unroll 1
+          for (int kh = HALVES ? i : 0; kh < (HALVES ? i + 1 : D / 64); ++kh) {
             uint32_t w[32];
 #pragma unroll
-            for (int c4 = 0; c4 < 16; ++c4) {  // place 4 c4 of this half: channels 64kh + 16 (c4 % 4) + 4 (c4 / 4) .. +3
-              uint2 x = make_uint2(0u, 0u);
-              if (live) x = *reinterpret_cast<const uint2*>(q + 64 * kh + 16 * (c4 % 4) + 4 * (c4 / 4));
-              w[2 * c4] = x.x ^ flip;
-              w[2 * c4 + 1] = x.y ^ flip;
+            for (int c8 = 0; c8 < 8; ++c8) {  // channels 64kh + 8 c8 .. +7: places 16 (c8 % 2) + 4 (c8 / 2), and 16 behind them
+              uint4 x = make_uint4(0u, 0u, 0u, 0u);
+              if (live) x = *reinterpret_cast<const uint4*>(q + 64 * kh + 8 * c8);
+              const int at = 2 * (8 * (c8 % 2) + c8 / 2);
+              w[at] = x.x ^ flip;
+              w[at + 1] = x.y ^ flip;
+              w[at + 8] = x.z ^ flip;
+              w[at + 9] = x.w ^ flip;
             }
-            if (WIDE || i == 1) {  // (uniform per warp)
+            if (WIDE || (SPLIT_ROWS && i == 1)) {  // (uniform per warp)
               uint8_t* d = smem + S::Q_OFF + ((WIDE && SPLIT_ROWS) ? i * S::Q_TILE : 0) + kh * 8 * (128 * 16) + row * 16;
 #pragma unroll
               for (int c = 0; c < 8; ++c)
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
               tmem_st32(tmem + lanes + S::TM_Q + 32 * kh, w);
             }
           }
-          if (WIDE || i == 1) fence_proxy_async_smem();
+          if (WIDE || (SPLIT_ROWS && i == 1)) fence_proxy_async_smem();
           tmem_wait_st();
         }
         tc_fence_before();
@@ -561,6 +561,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         }
         const float f = whole ? (L == 0.0f ? 0.0f : v_scale / L) : 1.0f;
         const long long prow = static_cast<long long>(seg.slot) * R + trow;
+        const long long orow = static_cast<long long>(seg.r.first + node) * a.q_heads + h * gq + head;
+        const bool halves = whole && !WIDE;  // fp16 output, else fp32 output or a partial result
+        float* const dst = (whole ? reinterpret_cast<float*>(a.out) + orow * D : a.part_o + prow * D);
         if (warp_live) {
 #pragma unroll 1
           for (int c0 = c_begin; c0 < c_begin + COLS; c0 += 16) {
@@ -570,28 +573,30 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
               if (have1) tmem_ld16(tmem + lanes + S::TM_O + D + c0, o1);
             }
             tmem_wait_ld();
-            if (!live) continue;
 #pragma unroll
-            for (int c = 0; c < 16; c += 4) {
-              float v[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                v[e] = __uint_as_float(o[c + e]) * f0;
-                if constexpr (!SPLIT_ROWS) {
-                  if (have1) v[e] = fmaf(__uint_as_float(o1[c + e]), f1, v[e]);
-                }
-                v[e] *= f;
+            for (int c = 0; c < 16; ++c) {
+              float v = __uint_as_float(o[c]) * f0;
+              if constexpr (!SPLIT_ROWS) {
+                if (have1) v = fmaf(__uint_as_float(o1[c]), f1, v);
               }
-              const float4 x = make_float4(v[0], v[1], v[2], v[3]);
-              if (whole)
-                tree_store4<D>(a, seg, gq, row0 + trow, (c0 + c) / 4, x);
-              else
-                *reinterpret_cast<float4*>(a.part_o + prow * D + c0 + c) = x;
+              o[c] = __float_as_uint(v * f);
+            }
+            if (!live) continue;
+            if (halves) {
+              uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<__half*>(a.out) + orow * D + c0);
+#pragma unroll
+              for (int c = 0; c < 16; c += 8) {
+                auto two = [&](int e) { return pack_rn_f16x2(__uint_as_float(o[c + e]), __uint_as_float(o[c + e + 1])); };
+                d[c / 8] = make_uint4(two(0), two(2), two(4), two(6));
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 16; c += 4) reinterpret_cast<uint4*>(dst + c0)[c / 4] = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
             }
           }
-          if (whole && live && nan_met) 
+          if (whole && live && nan_met)
             tree_put_nan<D, FMT>(sh.args, seg.b, h, seg.r.first, seg.r.nodes, len, row0 + trow, c_begin, c_begin + COLS);
-          if (!whole && live && (SPLIT_ROWS || i == 0))
+        if (!whole && live && (SPLIT_ROWS || i == 0))
             *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(M, L);
         }
         tc_fence_before();
