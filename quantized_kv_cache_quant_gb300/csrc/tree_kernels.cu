@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(128) tree_rows16_kernel(const __grid_constant_
   using S = TreeSmem<D>;
   constexpr int KS = D / 16, NT = D / 8, CH = D / 32;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ unsigned long long plan_s[34];
+  __shared__ unsigned long long plan_s[36];
   __shared__ int nan_s;
   // the arguments and the slice, for functions out of line (a reference to a kernel's parameters is read from global
   // memory there)
@@ -59,8 +59,10 @@ __global__ void __launch_bounds__(128) tree_rows16_kernel(const __grid_constant_
     fence_mbar_init();
   }
   if (tid == 0) tree_leave_none(a);
-  const TreeSlice slice = tree_slice<kRows, kUnit>(a, plan_s, 2);
-  if (static_cast<int>(blockIdx.x) >= slice.blocks) return;
+  // (one request of 2500 tokens: slices of 4 units 15.5 us, of 2 18.1; of 400 tokens: 13.5 and 12.4)
+  const TreeSlice slice = tree_slice<kRows, kUnit>(
+      a, plan_s, [](long long pair) { return pair >= 32 ? 4 : 2; }, [](long long u) { return u >= 4 ? 4 : 2; });
+  if (slice.begin >= slice.end) return;
 
   if (tid == 0) {
     args_s = a;
@@ -418,7 +420,12 @@ cudaError_t launch_tree_join(const TreeArgs& a, int blocks, int tile_rows, cudaS
 }
 
 cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s) {
-  if (a.max_tree * (a.q_heads / a.kv_heads) > kRows) return launch_tree_tc(a, s);
+  // Up to 16 rows a kv head, and little work altogether: few tiles of 16 rows over at most 2560 tokens, where the wider
+  // kernel's longer change of segments decides (8 heads, one request: trees of 5 at 1000 tokens 14.0 us here and 15.8
+  // there, of 32 17.6 and 23.2, at 2500 tokens 23.0 and 24.0, at 5000 30.1 and 29.1; 16 requests at 1000 26 and 22).
+  const int rows = a.max_tree * (a.q_heads / a.kv_heads);
+  const long long tiles = static_cast<long long>(a.batch) * a.kv_heads * ((rows + kRows - 1) / kRows);
+  if (rows > kRows && (tiles > 64 || a.max_seq_len > 2560)) return launch_tree_tc(a, s);
   static_assert(2 * kTreeMaxBlocks * kRows <= kTreePartRows, "partial results fit the workspace");
   switch (a.head_dim * 100 + a.fmt * 10 + (a.out_fp32 ? 1 : 0)) {
     case 12800: return launch_rows16<128, 0, false>(a, s);

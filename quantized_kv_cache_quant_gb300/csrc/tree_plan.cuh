@@ -6,12 +6,16 @@
 // "pair"; its work is ceil((len + T) / unit) units of tokens. The units of all
 // pairs follow one another (b, then h, then tile: tiles that read the same
 // keys run next to one another and meet in L2) and are cut into equal slices,
-// one per thread block, whatever the requests' lengths. Lengths live on the
-// device, so every thread block finds its slice itself with one scan over the
-// requests. A block that holds only part of a pair leaves a partial result,
-// its first segment's in slot 2c, its last one's in 2c + 1; the last block of
-// the pair to finish joins them, always in the same order. A block begins at
-// most one pair that it does not end, so the pair's counter is that block's.
+// one per thread block, whatever the requests' lengths; a cut that would leave
+// fewer than `snap` units of a pair on one of its sides moves to the pair's
+// nearer end, since a piece costs a partial result and a change of segments
+// whatever its length. Lengths live on the device, so every thread block finds
+// its slice itself with one scan over the requests. A block that holds only part
+// of a pair leaves a partial result, its first segment's in slot 2c, a later
+// one's in 2c + 1, and a second kernel joins them, always in the same order. A
+// block begins at most one pair that it does not end: that pair is the one it
+// describes to the second kernel, and the pair's other parts are the following
+// blocks' first segments.
 #pragma once
 
 #include "kvq_device.cuh"
@@ -41,19 +45,34 @@ __device__ __forceinline__ TreeRequest tree_request(const TreeArgs& a, int b) {
 struct TreeSlice {
   long long total;   // units of all pairs
   int blocks;        // slices that share them
-  long long begin, end;
+  int snap;
+  long long begin, end;  // (an empty slice: begin >= end)
   int b;             // request of the first unit
   long long before;  // units of the requests before b
 
-  __device__ __forceinline__ long long start_of(int c) const { return static_cast<long long>(c) * total / blocks; }
-  __device__ __forceinline__ int block_of(long long u) const { return static_cast<int>(((u + 1) * blocks - 1) / total); }
+  __device__ __forceinline__ long long cut(int c) const { return static_cast<long long>(c) * total / blocks; }
+  // blocks that share the pair of units [begin, begin + units)
+  __device__ __forceinline__ int parts_of(long long pair_begin, int units) const {
+    // cut(c) >= u for c >= ceil(u * blocks / total)
+    const long long lo = pair_begin + snap, hi = pair_begin + units - snap;
+    if (lo > hi) return 1;
+    auto first = [&](long long u) { return (u * blocks + total - 1) / total; };
+    return 1 + static_cast<int>(first(hi + 1) - first(lo));
+  }
 };
 
-// The slice of thread block blockIdx.x. sm: 32 + 2 words of 8 bytes of shared
+// u / v for 0 <= u, 0 < v
+__device__ __forceinline__ int tree_div(long long u, int v) {
+  const unsigned long long x = static_cast<unsigned long long>(u);
+  return x >> 32 ? static_cast<int>(x / v) : static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(v));
+}
+
+// The slice of thread block blockIdx.x. sm: 32 + 4 words of 8 bytes of shared
 // memory that nothing else uses until the next __syncthreads after the call.
-// min_units: slices get at least about so many units.
-template <int R, int UNIT>
-__device__ __forceinline__ TreeSlice tree_slice(const TreeArgs& a, unsigned long long* sm, int min_units) {
+// shortest(u): the units that slices get at least, where a pair has about u;
+// snap(u): the snap, 1 or more, of slices of u units.
+template <int R, int UNIT, class Shortest, class Snap>
+__device__ __forceinline__ TreeSlice tree_slice(const TreeArgs& a, unsigned long long* sm, Shortest shortest, Snap snap_of) {
   TreeSlice s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   auto units_of = [&](int b) -> unsigned long long {
@@ -90,17 +109,25 @@ __device__ __forceinline__ TreeSlice tree_slice(const TreeArgs& a, unsigned long
     total += sum;
   }
   s.total = static_cast<long long>(total);
-  s.blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), (s.total + min_units - 1) / min_units));
+  // (the pairs that requests of equal trees would have)
+  const int rows = (a.n_tokens + a.batch - 1) / a.batch * (a.q_heads / a.kv_heads);
+  const int per = shortest(s.total / (static_cast<long long>(a.batch) * a.kv_heads * ((rows + R - 1) / R)));
+  s.blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), (s.total + per - 1) / per));
+  const int snap = s.blocks > 0 ? snap_of(s.total / s.blocks) : 1;
+  s.snap = snap;
   s.begin = s.end = s.before = 0;
   s.b = 0;
   if (static_cast<int>(blockIdx.x) >= s.blocks) return s;
-  s.begin = s.start_of(blockIdx.x);
-  s.end = s.start_of(blockIdx.x + 1);
-  const unsigned long long u = static_cast<unsigned long long>(s.begin);
+  const unsigned long long u0 = static_cast<unsigned long long>(s.cut(blockIdx.x));
+  const unsigned long long u1 = static_cast<unsigned long long>(s.cut(blockIdx.x + 1));  // == total for the last one
   auto claim = [&](int b, unsigned long long at, unsigned long long n) {
-    if (at <= u && u < at + n) {
+    if (at <= u0 && u0 < at + n) {
       sm[32] = static_cast<unsigned long long>(b);
       sm[33] = at;
+    }
+    if (at <= u1 && u1 < at + n) {
+      sm[34] = static_cast<unsigned long long>(b);
+      sm[35] = at;
     }
   };
   claim(threadIdx.x, mine_at, mine);
@@ -115,8 +142,18 @@ __device__ __forceinline__ TreeSlice tree_slice(const TreeArgs& a, unsigned long
     }
   }
   __syncthreads();
+  // the cut at unit u of request b, whose units begin at `before`
+  auto snapped = [&](long long u, int b, long long before) -> long long {
+    const TreeRequest r = tree_request<R, UNIT>(a, b);
+    const long long pair_begin = before + static_cast<long long>(tree_div(u - before, r.units)) * r.units;
+    const int in = static_cast<int>(u - pair_begin);
+    if (in >= snap && r.units - in >= snap) return u;
+    return 2 * in <= r.units ? pair_begin : pair_begin + r.units;
+  };
   s.b = static_cast<int>(sm[32]);
   s.before = static_cast<long long>(sm[33]);
+  s.begin = snapped(u0, s.b, s.before);
+  s.end = static_cast<int>(blockIdx.x) + 1 == s.blocks ? s.total : snapped(u1, static_cast<int>(sm[34]), static_cast<long long>(sm[35]));
   __syncthreads();
   return s;
 }
@@ -164,8 +201,7 @@ __device__ __noinline__ bool next_segment(const TreeArgs& a, const TreeSlice& s,
     g.r = tree_request<R, UNIT>(a, b);
     n = static_cast<long long>(g.r.units) * g.r.tiles * a.kv_heads;
   }
-  const unsigned long long in = static_cast<unsigned long long>(at - before);
-  const int pair = in >> 32 ? static_cast<int>(in / g.r.units) : static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(g.r.units));
+  const int pair = tree_div(at - before, g.r.units);
   g.b = b;
   g.h = pair / g.r.tiles;
   g.tile = pair % g.r.tiles;
@@ -173,8 +209,7 @@ __device__ __noinline__ bool next_segment(const TreeArgs& a, const TreeSlice& s,
   g.u0 = static_cast<int>(at - g.pair_begin);
   g.u1 = static_cast<int>(min(s.end - g.pair_begin, static_cast<long long>(g.r.units)));
   g.slot = 2 * static_cast<int>(blockIdx.x) + (at == s.begin ? 0 : 1);
-  g.parts = 1;
-  if (g.u0 != 0 || g.u1 != g.r.units) g.parts = s.block_of(g.pair_begin + g.r.units - 1) - s.block_of(g.pair_begin) + 1;
+  g.parts = g.u0 == 0 && g.u1 == g.r.units ? 1 : s.parts_of(g.pair_begin, g.r.units);
   w.at = g.pair_begin + g.u1;
   w.before = before;
   w.b = b;

@@ -78,7 +78,7 @@ struct TcShared {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t ready[kMaxBufs], free[kMaxBufs];
   uint64_t qready[2], sready[2], sfree[2], pready[2], pdone[2], drain[3];
-  unsigned long long plan[34];
+  unsigned long long plan[36];
   uint32_t tmem;
   int dead, nan_met;
   float ml[2][128][2];
@@ -146,8 +146,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   }
   if (tid == 0) tree_leave_none(a);
   {
-    const TreeSlice s = tree_slice<R, kTile>(a, sh.plan, 2);
-    if (static_cast<int>(blockIdx.x) >= s.blocks) return;
+    // Slices of 2 to 4 tiles at least: a pair of 2 tiles (one request of 100 tokens) takes 11 us alone in its block and
+    // 16 with another one, a request of 2500 tokens 20 us in slices of 2 and 17 in slices of 4. Cuts keep 4 to 8 tiles
+    // from a pair's ends: 16 requests of 1000 tokens and 64 rows 31 us with cuts anywhere, 23 with 8.
+    const TreeSlice s = tree_slice<R, kTile>(
+        a, sh.plan, [](long long pair) { return static_cast<int>(min(max(pair, 2ll), 4ll)); },
+        [](long long u) { return static_cast<int>(min(max(u, 4ll), 8ll)); });
+    if (s.begin >= s.end) return;
     if (tid == 0) sh.slice = s;
     if (lane == 0) sh.walk[warp].start(s);
   }
@@ -649,9 +654,12 @@ cudaError_t dispatch_tc(const TreeArgs& a, cudaStream_t s) {
 
 cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t s) {
   // 256 rows a tile read and convert the keys once for twice the rows, but a request with fewer rows pays for both
-  // streams: it takes an average (host's knowledge: the rows of all requests) above one stream's rows.
+  // streams: it takes an average (host's knowledge: the rows of all requests) above one stream's rows. And it takes more
+  // tiles of 128 rows than SMs (one request, 252 rows, 1000 tokens: 23 us with 128, 29 with 256; four requests, 512 rows,
+  // 2500 tokens: 49 and 51; 16 requests: 131 and 116).
   const int gq = a.q_heads / a.kv_heads;
-  const bool wide_tile = static_cast<long long>(a.n_tokens) * gq > 128ll * a.batch && a.max_tree * gq > 128;
+  const long long rows = static_cast<long long>(a.n_tokens) * gq, row_tiles = (rows + 127) / 128;
+  const bool wide_tile = rows > 128ll * a.batch && a.max_tree * gq > 128 && row_tiles * a.kv_heads > device_sm_count();
   return wide_tile ? dispatch_tc<256>(a, s) : dispatch_tc<128>(a, s);
 }
 

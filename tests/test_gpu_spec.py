@@ -288,6 +288,18 @@ def tree_bound(mag, spread, dots, ref, wide, dim):
     return out
 
 
+# max_seq_len of every call, where it is more than the lengths need: calls with short tables and few rows take one kernel,
+# the same ones with long tables another
+LONGEST = [0]
+
+
+@pytest.fixture
+def long_tables():
+    LONGEST[0] = 4096
+    yield
+    LONGEST[0] = 0
+
+
 def run_tree(spec, p, table, seq, trees, sees, q, wide, max_tree=None, extra_rows=0, strided=False, ws=None, scale=0.0):
     import torch
     n, hq, d = q.shape
@@ -307,8 +319,10 @@ def run_tree(spec, p, table, seq, trees, sees, q, wide, max_tree=None, extra_row
     out = torch.full((n + extra_rows, hq, d), -77.0, dtype=torch.float32 if wide else torch.float16, device="cuda")
     if ws is None:
         ws = spec.tree_workspace(len(seq), p.descs[0].kv_heads, hq, d, max_tree)
+    if table.shape[1] * 16 < LONGEST[0]:
+        table = np.pad(table, ((0, 0), (0, LONGEST[0] // 16 - table.shape[1])), constant_values=-1)
     width = table.shape[1]
-    most = int(max(s + t for s, t in zip(seq, trees)))
+    most = max(int(max(s + t for s, t in zip(seq, trees))), LONGEST[0])
     spec.fp8_tree_attention(dq, *p.descs, dev(table), i32(seq), dev(off), mask, max_tree, max(1, min(most, width * 16)), out,
                             scale, ws)
     got = host(out).astype(np.float64)
@@ -562,6 +576,128 @@ def test_tree_same_call_twice_gives_the_same_bits():
     for _ in range(3):
         b, _ = run_tree(spec, p, table, [4400], [16], sees, q, True, ws=ws)
         assert np.array_equal(a, b)
+
+
+TREE_SHAPES = [(2, 4, [17], [5]), (2, 8, [100, 3, 0, 250], [1, 4, 7, 2]), (1, 4, [129, 64, 15], [9, 8, 16]),
+               (2, 2, [300, 0, 1, 16, 31], [33, 20, 0, 1, 40]), (1, 8, [511, 40], [63, 17]), (1, 1, [70], [130])]
+
+
+@pytest.mark.parametrize("test,args", [(test_tree_matches_oracle, s + f + (w,)) for s in TREE_SHAPES for w in (False, True)
+                                       for f in ((128, "e4m3", False), (64, "e5m2", True))]
+                         + [(test_tree_odd_head_groups, (g,)) for g in (3, 7, 64)]
+                         + [(test_tree_context_lengths, (n,)) for n in (1, 15, 16, 63, 64, 65, 129, 1023)]
+                         + [(test_tree_nan_in_masked_nodes_stays_there, (d, 8)) for d in (64, 128)]
+                         + [(t, ()) for t in (test_tree_rows_that_see_nothing_are_zero, test_tree_query_nan_stays_in_its_row,
+                                              test_tree_strided_queries_and_padded_rows, test_tree_many_requests,
+                                              test_tree_softmax_scale_and_large_scores, test_tree_rising_scores,
+                                              test_tree_of_256_nodes, test_tree_same_call_twice_gives_the_same_bits)])
+def test_tree_with_long_tables(long_tables, test, args):
+    test(*args)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("dim,fmt", [(128, "e4m3"), (64, "e5m2")])
+@pytest.mark.parametrize("seq,trees", [
+    ([700, 0, 65, 130, 1], [90, 80, 64, 70, 100]),     # the longest passes every ring of tiles more than twice
+    ([40] * 12, [20, 33, 40, 64, 17, 31, 50, 63, 21, 40, 35, 64]),  # more pairs than blocks
+])
+def test_tree_of_many_rows(seq, trees, dim, fmt, wide):
+    """Trees with more rows than one stream of the tensor cores' kernel, in enough requests that it takes its wide tiles."""
+    check_tree(np.random.default_rng(dim + len(seq)), 8, 8, dim, seq, trees, fmt, True, wide)
+
+
+@pytest.mark.parametrize("dim,wide", [(128, False), (128, True), (64, False)])
+def test_tree_many_rows_see_nan_nodes_only_where_the_mask_says(dim, wide):
+    kvq, spec = _mods()
+    rng = np.random.default_rng(26)
+    seq, trees = [30, 5, 90, 0], [80, 81, 82, 79]
+    sees, at = random_sees(rng, trees), np.cumsum([0] + trees)
+    table = np.full((4, 12), -1, np.int32)
+    perm, used = rng.permutation(40), 0
+    for b in range(4):
+        m = -(-(seq[b] + trees[b]) // 16)
+        table[b, :m], used = perm[used:used + m], used + m
+    p = Pools(rng, 40, 8, dim, "e4m3", False)
+    sees[:, 2] = sees[:, 70] = False
+    for b in range(4):
+        sees[at[b] + 2, 2] = sees[at[b] + 70, 70] = True
+        for node, nat in ((2, p.nat[0]), (70, p.nat[1])):
+            pos = seq[b] + node
+            nat[table[b, pos // 16], :, pos % 16, :] = 0xFF
+    p.upload()
+    n = int(at[-1])
+    q = rng.standard_normal((n, 64, dim)).astype(np.float16)
+    got, off = run_tree(spec, p, table, seq, trees, sees, q, wide)
+    ref, mag, spread, dots = ospec.tree_attention(q, p.nat[0], p.nat[1], p.scale[0], p.scale[1], "e4m3", table, seq, off, sees,
+                                                  np.float32(1.0) / np.sqrt(np.float32(dim)))
+    dirty = [at[b] + i for b in range(4) for i in (2, 70)]
+    clean = [i for i in range(n) if i not in dirty]
+    assert np.isnan(got[dirty]).all() and np.isnan(ref[dirty]).all()
+    assert np.all(np.abs(got - ref)[clean] <= tree_bound(mag, spread, dots, ref, wide, dim)[clean])
+
+
+@pytest.mark.parametrize("heads,gq,nodes", [(2, 8, 8), (8, 8, 200)])
+def test_tree_bad_tables_and_lengths_of_wide_trees_stay_inside(heads, gq, nodes):
+    import torch
+    kvq, spec = _mods()
+    rng = np.random.default_rng(27)
+    p = Pools(rng, 3, heads, 128, "e4m3", False)
+    n = 3 * nodes
+    q = dev(rng.standard_normal((n, heads * gq, 128)).astype(np.float16))
+    mask = torch.full((n, -(-nodes // 64)), -1, dtype=torch.int64, device="cuda")
+    ws = spec.tree_workspace(3, heads, heads * gq, 128, nodes)
+    out = torch.zeros((n, heads * gq, 128), dtype=torch.float16, device="cuda")
+    table = torch.full((3, 256), -1, dtype=torch.int32, device="cuda")
+    table[1:, 1] = 99
+    for off in ([0, nodes, 2, 50 * n], [-4, 2, n + 3, n + 3], [0, nodes, 2 * nodes, n]):
+        for lens in ([100000, -5, 31], [0, 0, 0], [4095, 4096, 2 ** 31 - 1]):
+            spec.fp8_tree_attention(q, *p.descs, table, i32(lens), i32(off), mask, nodes, 4096, out, 0.0, ws)
+    torch.cuda.synchronize()
+    assert int(ws[:4].view(torch.int32).item()) == 0
+
+
+@pytest.mark.parametrize("nodes", [2, 30, 70])
+def test_tree_calls_on_two_streams_and_in_two_graphs(nodes):
+    """Two calls at a time with a workspace each, eager and captured, give what one call alone gives."""
+    import torch
+    kvq, spec = _mods()
+    rng = np.random.default_rng(28 + nodes)
+    p = Pools(rng, 2100, 4, 128, "e4m3", False)
+    table = rng.permutation(2100)[:2064].reshape(4, 516).astype(np.int32)
+    sees = random_sees(rng, [nodes] * 4)
+    mask = spec.pack_tree_mask(dev(np.pad(sees, ((0, 0), (0, -nodes % 64))))).contiguous()
+    q = [dev(rng.standard_normal((4 * nodes, 32, 128)).astype(np.float16)) for _ in range(2)]
+    lens, off, dt = i32([8000, 100, 5000, 777]), i32([0, nodes, 2 * nodes, 3 * nodes, 4 * nodes]), dev(table)
+    out = [torch.zeros_like(x) for x in q]
+    ws = [spec.tree_workspace(4, 4, 32, 128, nodes) for _ in range(2)]
+
+    def call(i):
+        spec.fp8_tree_attention(q[i], *p.descs, dt, lens, off, mask, nodes, 8256, out[i], 0.0, ws[i])
+
+    want = []
+    for i in range(2):
+        call(i)
+        torch.cuda.synchronize()
+        want.append(out[i].clone())
+        out[i].zero_()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    graphs = []
+    for i in range(2):
+        streams[i].wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=streams[i]):
+            call(i)
+        graphs.append(g)
+    for replayed in (False, True):
+        for _ in range(4):
+            for i in range(2):
+                with torch.cuda.stream(streams[i]):
+                    graphs[i].replay() if replayed else call(i)
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(out[i], want[i])
+            out[i].zero_()
+        torch.cuda.synchronize()
 
 
 # ---------------------------------------------------------------- together
