@@ -423,10 +423,12 @@ __global__ void __launch_bounds__(512) fp8_accept_kernel(Fp8AcceptArgs a) {
     rows[i] = r;
   }
   __syncthreads();
-  if (threadIdx.x == 0) a.new_lens[b] = len + n;  // (this block alone reads seq_lens[b])
+  // (this block alone reads seq_lens[b]; a length near 2^31 wraps)
+  if (threadIdx.x == 0) a.new_lens[b] = static_cast<int>(static_cast<unsigned>(len) + n);
   if (len < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   constexpr int KU = D / 16, CH = D / 32;
+  const long long end = min(static_cast<long long>(len) + n, static_cast<long long>(a.max_blocks) * kBlock);
   const int k_tasks = (a.kv_heads * KU + 31) / 32, tasks = k_tasks + a.kv_heads * CH;
   for (int task = warp; task < tasks; task += warps) {
     if (task < k_tasks) {
@@ -452,12 +454,12 @@ __global__ void __launch_bounds__(512) fp8_accept_kernel(Fp8AcceptArgs a) {
                                         (c * 32 + in_chunk) * 16);
       };
       // place blocks in order: what a later one's rows come from lies behind every place of an earlier one
-      for (int p0 = len / kBlock * kBlock; p0 < len + n; p0 += kBlock) {
+      for (long long p0 = len / kBlock * kBlock; p0 < end; p0 += kBlock) {
         uint4 src[4];
         int shift[4], place = -1;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {  // the unit's tokens: byte e of each word is token 8 (e / 2) + 2 tig + e % 2
-          const int i = p0 + 8 * (e >> 1) + 2 * tig + (e & 1) - len;
+          const int i = static_cast<int>(p0 - len) + 8 * (e >> 1) + 2 * tig + (e & 1);
           shift[e] = -1;
           if (i >= 0 && i < n && src_blk[i] >= 0) {
             const int from = rows[i] & 255;

@@ -239,6 +239,21 @@ def test_accept_moves_rows(heads, dim, batch, tree, plen):
     assert np.array_equal(host(lens), seq + acc)
 
 
+def test_accept_of_lengths_beyond_every_table():
+    """Lengths up to 2^31 - 1 behind the table: nothing moves, and the call's work does not follow them."""
+    import torch
+    kvq, spec = _mods()
+    rng = np.random.default_rng(7)
+    p = Pools(rng, 4, 2, 64, "e4m3", False)
+    p.upload()
+    path = np.tile(np.arange(1, 201, dtype=np.int32), (3, 1))
+    lens = np.array([2 ** 31 - 1, 2 ** 31 - 150, 65], np.int32)
+    new = torch.zeros(3, dtype=torch.int32, device="cuda")
+    spec.fp8_kv_accept(*p.descs, i32([[0, 1, 2, 3]] * 3), dev(lens), dev(path), i32([200] * 3), new)
+    assert host(new).tolist() == [int(np.int32((int(n) + 200 + 2 ** 31) % 2 ** 32 - 2 ** 31)) for n in lens]
+    p.check()
+
+
 def test_accept_skips_what_is_outside():
     kvq, spec = _mods()
     rng = np.random.default_rng(5)
@@ -593,6 +608,11 @@ TREE_SHAPES = [(2, 4, [17], [5]), (2, 8, [100, 3, 0, 250], [1, 4, 7, 2]), (1, 4,
                                               test_tree_of_256_nodes, test_tree_same_call_twice_gives_the_same_bits)])
 def test_tree_with_long_tables(long_tables, test, args):
     test(*args)
+
+
+def test_tree_more_requests_than_threads_of_a_block(long_tables):
+    rng = np.random.default_rng(29)
+    check_tree(rng, 1, 4, 64, rng.integers(0, 40, 700).tolist(), rng.integers(0, 7, 700).tolist())
 
 
 @pytest.mark.parametrize("wide", [False, True])
