@@ -117,41 +117,44 @@ __global__ void __launch_bounds__(1024) blocks_resize_kernel(BlocksResizeArgs a)
 
   const int threads = blockDim.x * cluster.num_blocks(), me = cluster.block_rank() * blockDim.x + threadIdx.x;
   // A warp takes 128 neighbouring entries, a lane four of them 32 apart: their reads are in flight together.
-  const int first = (me & ~31) * 4 + (me & 31);
-  for (int i0 = first; i0 < released; i0 += 4 * threads) {
-    int b = owner_of(a.batch, i0, [&](int m) { return drop_s[m]; });
+  // (entries count up to 2^31 - 1: unsigned, so that the last step passes that number without wrapping)
+  const unsigned first = (me & ~31) * 4 + (me & 31), n_drop = released, n_grow = grown;
+  for (unsigned i0 = first; i0 < n_drop; i0 += 4 * threads) {
+    int b = owner_of(a.batch, static_cast<int>(i0), [&](int m) { return drop_s[m]; });
     int32_t* entry[4];
     int32_t block[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       entry[e] = nullptr;
-      if (i0 + 32 * e < released) {
-        while (b + 1 < a.batch && i0 + 32 * e >= drop_s[b + 1]) ++b;
-        entry[e] = a.block_table + static_cast<long long>(b) * a.max_blocks + want_s[b] + (i0 + 32 * e - drop_s[b]);
+      const unsigned i = i0 + 32 * e;
+      if (i < n_drop) {
+        while (b + 1 < a.batch && static_cast<int>(i) >= drop_s[b + 1]) ++b;
+        entry[e] = a.block_table + static_cast<long long>(b) * a.max_blocks + want_s[b] + (static_cast<int>(i) - drop_s[b]);
         block[e] = *entry[e];
       }
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (entry[e] == nullptr) continue;
-      const int place = top - 1 - (i0 + 32 * e);
+      const int place = top - 1 - static_cast<int>(i0 + 32 * e);
       if (place >= 0) a.free_blocks[place] = block[e];
       *entry[e] = -1;
     }
   }
   cluster.sync();
-  for (int i0 = first; i0 < grown; i0 += 4 * threads) {
+  for (unsigned i0 = first; i0 < n_grow; i0 += 4 * threads) {
     // growth is granted in order until it is refused for good: what the granted requests asked for is their place
-    int b = owner_of(a.batch, i0, [&](int m) { return min(ask_s[m], grown); });
+    int b = owner_of(a.batch, static_cast<int>(i0), [&](int m) { return min(ask_s[m], grown); });
     int32_t* entry[4];
     int32_t block[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       entry[e] = nullptr;
-      if (i0 + 32 * e < grown) {
-        while (b + 1 < a.batch && i0 + 32 * e >= ask_s[b + 1]) ++b;
-        entry[e] = a.block_table + static_cast<long long>(b) * a.max_blocks + held_s[b] + (i0 + 32 * e - ask_s[b]);
-        block[e] = __ldcg(a.free_blocks + (top - 1 - (i0 + 32 * e)));
+      const unsigned i = i0 + 32 * e;
+      if (i < n_grow) {
+        while (b + 1 < a.batch && static_cast<int>(i) >= ask_s[b + 1]) ++b;
+        entry[e] = a.block_table + static_cast<long long>(b) * a.max_blocks + held_s[b] + (static_cast<int>(i) - ask_s[b]);
+        block[e] = __ldcg(a.free_blocks + (top - 1 - static_cast<int>(i)));
       }
     }
 #pragma unroll
@@ -210,9 +213,9 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(SlotMapArgs a) {
     bool fresh = true;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int i = i0 + e;
       slot[e] = seq[e] = pos[e] = -1;
-      if (i < n) {
+      if (e < n - i0) {
+        const int i = i0 + e;
         while (i >= next) {
           next = off_s[++b + 1];
           fresh = true;
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(SlotMapArgs a) {
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (i0 + e >= a.n_rows) break;
+        if (e >= a.n_rows - i0) break;
         a.slots[i0 + e] = slot[e];
         if (a.seq_ids) a.seq_ids[i0 + e] = seq[e];
         if (a.positions) a.positions[i0 + e] = pos[e];

@@ -110,7 +110,7 @@ __device__ __forceinline__ TreeSlice tree_slice(const TreeArgs& a, unsigned long
   }
   s.total = static_cast<long long>(total);
   // (the pairs that requests of equal trees would have)
-  const int rows = (a.n_tokens + a.batch - 1) / a.batch * (a.q_heads / a.kv_heads);
+  const int rows = min((a.n_tokens - 1) / a.batch + 1, a.max_tree) * (a.q_heads / a.kv_heads);
   const int per = shortest(s.total / (static_cast<long long>(a.batch) * a.kv_heads * ((rows + R - 1) / R)));
   s.blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), (s.total + per - 1) / per));
   const int snap = s.blocks > 0 ? snap_of(s.total / s.blocks) : 1;

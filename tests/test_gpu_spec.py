@@ -78,6 +78,25 @@ def test_grow_and_shrink_restore_the_stack():
     assert (host(t.table) == -1).all()
 
 
+def test_resize_of_the_largest_table():
+    """2^31 - 1 entries: all released, then granted again."""
+    import torch
+    _, spec = _mods()
+    n = 2 ** 31 - 1
+    table = torch.arange(n, dtype=torch.int32, device="cuda").view(1, n)
+    free = torch.zeros(n, dtype=torch.int32, device="cuda")
+    held, count = i32([n]), i32([0])
+    spec.kv_blocks_resize(table, held, i32([0]), 1, free, count)
+    assert (int(held), int(count)) == (0, n)
+    assert int(table.max()) == -1 and int(table.min()) == -1
+    for at in (0, 1, 65535, n // 2, n - 65536, n - 1):
+        assert int(free[at]) == n - 1 - at             # the first one released is on top
+    spec.kv_blocks_resize(table, held, i32([n]), 1, free, count)
+    assert (int(held), int(count)) == (n, 0)
+    want = torch.arange(n, dtype=torch.int32, device="cuda")
+    assert torch.equal(table[0], want)
+
+
 def test_resize_with_a_state_that_does_not_add_up_stays_inside():
     """More blocks held and free than the pool has: the stack never runs past its end."""
     kvq, spec = _mods()
