@@ -116,8 +116,9 @@ KVQ_API kvq_status fp8_kv_accept(const fp8_pool* k, const fp8_pool* v, const int
 /* ------------------------------------------------------------------------ */
 
 /* Workspace of fp8_tree_attention: a status word at offset 0 (as
- * kv_decode_workspace_bytes), counters that return to zero after every call,
- * and partial results. Zero it once after allocating it. One workspace serves
+ * kv_decode_workspace_bytes), and what the call's two kernels hand over: partial
+ * results and which of them belong together. Zero it once after allocating it
+ * (the status word collects errors until it is cleared). One workspace serves
  * one stream: calls that overlap on the device (two captured graphs among
  * them) must not share it. 0 for shapes the call refuses. */
 KVQ_API size_t fp8_tree_workspace_bytes(int32_t batch, int32_t kv_heads, int32_t q_heads, int32_t head_dim,

@@ -61,6 +61,8 @@ __device__ __forceinline__ int owner_of(int n, int i, F start) {
 // blocks that this call released.
 //   A = blocks free after the releases; released entry r goes to stack place
 //   A-1-r, granted entry i comes from place A-1-i.
+// Bound by latency: 3.1 us for 8 requests with nothing to change, 8 us for 135
+// thousand changed entries (scan, scattered table rows, the barrier).
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(1024) blocks_resize_kernel(BlocksResizeArgs a) {
   extern __shared__ int sm[];
@@ -174,7 +176,9 @@ __global__ void __launch_bounds__(1024) blocks_resize_kernel(BlocksResizeArgs a)
 
 // ---------------------------------------------------------------------------
 // Slot map: every thread block scans the requests' new lengths itself (no
-// second launch), then takes its share of the rows, four to a thread.
+// second launch), then takes its share of the rows, four to a thread. 16 bytes
+// are written a row: 2.16 million rows in 10.7 us, 3.2 TB/s (the output stays in
+// L2); a few rows in 4.2 us, the scan and two dependent reads.
 // ---------------------------------------------------------------------------
 constexpr int kMapThreads = 256;
 
@@ -271,7 +275,9 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(SlotMapArgs a) {
 // where the run covers them (a key unit is 16 channels of one token, a value
 // unit 4 tokens of 4 channels). A value row alone is single bytes, each in a
 // 32-byte sector of its own, so writing whole runs at once is what keeps long
-// appends at the memory's rate.
+// appends at the memory's rate. 65536 tokens (8 heads, D = 128, rows of a fused
+// projection) in 73.8 us, 80 % of the measured copy rate; 2112 tokens in runs of
+// 33 in 6.1 us; 8 tokens in 3.6 us, one chain of dependent reads.
 // ---------------------------------------------------------------------------
 constexpr int kAppendWarps = 4;
 
@@ -400,6 +406,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps) fp8_append_kernel(Fp8Append
 //           bytes from the units of their sources (of the same channels, so the
 //           same warp's) and writes the unit whole. Byte by byte this took 18 us
 //           for 256 requests x 8 rows: 2.1 million writes of parts of sectors.
+// One request: 4.5 us, a chain of dependent reads (length, path, table, rows).
+// 256 requests x 12 rows: 14.5 us; a value row touches all 64 sectors of its
+// block and head, 16 times its bytes, and that is what is moved.
 // ---------------------------------------------------------------------------
 constexpr int kAcceptBatch = 8;
 

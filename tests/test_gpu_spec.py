@@ -739,6 +739,27 @@ def test_tree_calls_on_two_streams_and_in_two_graphs(nodes):
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("dim,nodes", [(128, 30), (128, 70), (128, 200), (64, 70)])
+def test_tree_many_calls_give_the_same_bits(dim, nodes, wide):
+    """A tile that is overwritten while it is read shows now and then only."""
+    import torch
+    kvq, spec = _mods()
+    rng = np.random.default_rng(30 + nodes)
+    p = Pools(rng, 2100, 4, dim, "e4m3", False)
+    table = dev(rng.permutation(2100)[:2064].reshape(4, 516).astype(np.int32))
+    sees = random_sees(rng, [nodes] * 4)
+    mask = spec.pack_tree_mask(dev(np.pad(sees, ((0, 0), (0, -nodes % 64))))).contiguous()
+    q = dev(rng.standard_normal((4 * nodes, 32, dim)).astype(np.float16))
+    lens, off = i32([8000, 100, 5000, 777]), i32([nodes * i for i in range(5)])
+    ws = spec.tree_workspace(4, 4, 32, dim, nodes)
+    out = [torch.empty(q.shape, dtype=torch.float32 if wide else torch.float16, device="cuda") for _ in range(60)]
+    for o in out:
+        spec.fp8_tree_attention(q, *p.descs, table, lens, off, mask, nodes, 8256, o, 0.0, ws)
+    differ = sum(not torch.equal(o, out[0]) for o in out)
+    assert differ == 0, f"{differ} of 60 differ"
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("fmt,dim,captured", [("e4m3", 128, False), ("e5m2", 64, False), ("e4m3", 128, True)])
