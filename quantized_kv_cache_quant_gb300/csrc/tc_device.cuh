@@ -190,13 +190,6 @@ __device__ __forceinline__ bool role_wait_warp(uint64_t* bar, uint32_t parity, v
   }
 }
 
-// Maximum of three.
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
