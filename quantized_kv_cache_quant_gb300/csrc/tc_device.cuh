@@ -138,7 +138,8 @@ __device__ __forceinline__ void mbar_arrive_if(uint64_t* bar, bool on) {
 }
 
 // Whether phase `parity` has completed, without waiting (mbar_try_wait may
-// suspend the thread until it has).
+// suspend the thread until it has). The answer is the thread's own: two lanes of
+// a warp may differ, so a branch around role_wait_warp goes by the warp's vote.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(

@@ -341,7 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         for (int w = 0; w < 2; ++w)
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) y[w][c] = *reinterpret_cast<const uint4*>(vsrc + w * (kBlock * D) + c * 512);
-        if (ok && !room) ok = role_wait_warp(&sh.free[k], (n / kBufs - 1) & 1, dead, a.status);
+        // (the warp's answer, not the lane's: the barrier may complete between two lanes' tests)
+        if (ok && !__all_sync(0xffffffffu, room)) ok = role_wait_warp(&sh.free[k], (n / kBufs - 1) & 1, dead, a.status);
         if (!ok) break;
         // row of the core matrix: 4 (g3 / 2) + 2nt + g3 % 2
         uint8_t* kdst = smem + S::K_OFF + k * S::TILE + ktig * 2 * (kTile * 16) + 2 * w0 * 128 +
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         __syncwarp();
         mbar_arrive_if(&sh.sfree[i], lane == 0);
         // the products of the tile before have read P and written O
-        if (n > 0 && !pv_done) ok = role_wait_warp(&sh.pdone[i], (n - 1) & 1, dead, a.status);
+        if (n > 0 && !__all_sync(0xffffffffu, pv_done)) ok = role_wait_warp(&sh.pdone[i], (n - 1) & 1, dead, a.status);
         if (!ok) break;
         if (warp_live) {
           if (edge) {

@@ -1,0 +1,24 @@
+"""Orderings that the tree-attention kernels have to state in their source: no run can be relied on to show them missing."""
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "quantized_kv_cache_quant_gb300", "csrc")
+
+
+def source(name):
+    """A source file without its comments."""
+    text = open(os.path.join(CSRC, name), encoding="utf-8").read()
+    return re.sub(r"//[^\n]*", "", re.sub(r"/\*.*?\*/", "", text, flags=re.S))
+
+
+def test_a_lanes_own_answer_on_a_barrier_never_branches_around_a_warps_wait():
+    """role_wait_warp votes with all 32 lanes. A barrier may complete between two lanes' mbar_test, so a branch on such an
+    answer has to be on the warp's vote of it, or some lanes stay in the vote for ever."""
+    text = source("tree_tc_kernels.cu")
+    own = set(re.findall(r"const bool (\w+) = [^;]*\bmbar_test\(", text))
+    assert own
+    guarded = [c for c in re.findall(r"\bif \(([^;{}]*)\) ok = role_wait_warp\(", text)]
+    assert len(guarded) >= 3
+    for condition in guarded:
+        left = re.sub(r"__all_sync\(0xffffffffu, \w+\)", "", condition)
+        assert not own & set(re.findall(r"\w+", left)), condition
