@@ -552,7 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
 
       // ---- the segment's result ----
       const bool have1 = SPLIT_ROWS || seg.u1 - seg.u0 > 1;  // stream 1 had tiles
-      if constexpr (!SPLIT_ROWS) {
+      // A stream writes ml only where it had tiles: their scores waited for the queries of both streams, which each brings
+      // once it has read the segment before. Without tiles nothing would order its write behind the other stream's reads.
+      if (!SPLIT_ROWS && (i == 0 || have1)) {
         sh.ml[i][row][0] = m;
         sh.ml[i][row][1] = l;
       }
@@ -573,7 +575,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         const int c_begin = SPLIT_ROWS ? 0 : i * COLS;
         float M = m, L = l, f0 = 1.0f, f1 = 0.0f;
         if constexpr (!SPLIT_ROWS) {
-          const float m0 = sh.ml[0][row][0], l0 = sh.ml[0][row][1], m1 = sh.ml[1][row][0], l1 = sh.ml[1][row][1];
+          const float m0 = sh.ml[0][row][0], l0 = sh.ml[0][row][1];
+          const float m1 = have1 ? sh.ml[1][row][0] : -INFINITY, l1 = have1 ? sh.ml[1][row][1] : 0.0f;
           M = fmaxf(m0, m1);
           // (a stream without a maximum has the sum 0, or NaN, which stays)
           f0 = M == -INFINITY ? 1.0f : fast_exp2(m0 - M);
