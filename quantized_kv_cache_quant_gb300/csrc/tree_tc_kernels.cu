@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     __syncwarp();
     bool more = false;
     if (elect_one()) more = next_here();
+    __syncwarp();  // (a vote alone does not order memory)
     return __any_sync(0xffffffffu, more);
   };
 

@@ -22,3 +22,10 @@ def test_a_lanes_own_answer_on_a_barrier_never_branches_around_a_warps_wait():
     for condition in guarded:
         left = re.sub(r"__all_sync\(0xffffffffu, \w+\)", "", condition)
         assert not own & set(re.findall(r"\w+", left)), condition
+
+
+def test_a_segment_that_one_lane_found_is_ordered_before_its_warps_reads():
+    """One lane writes the warp's walk in shared memory and all lanes read it: a vote does not order memory."""
+    body = re.search(r"auto next = \[&\]\(\) -> bool \{(.*?)\n  \};", source("tree_tc_kernels.cu"), re.S).group(1)
+    written = body.index("next_here()")
+    assert "__syncwarp()" in body[:written] and "__syncwarp()" in body[written:]
