@@ -507,6 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
               m = m_new;
               msub = (m == -INFINITY ? 0.0f : m) - kBias;
               if (!fresh) {
+                tmem_wait_st();  // the first pass's weights, which this one overwrites
                 tc_fence_after();
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 16) {

@@ -29,3 +29,11 @@ def test_a_segment_that_one_lane_found_is_ordered_before_its_warps_reads():
     body = re.search(r"auto next = \[&\]\(\) -> bool \{(.*?)\n  \};", source("tree_tc_kernels.cu"), re.S).group(1)
     written = body.index("next_here()")
     assert "__syncwarp()" in body[:written] and "__syncwarp()" in body[written:]
+
+
+def test_the_second_pass_over_a_tile_stores_its_weights_after_the_firsts():
+    """Stores to tensor memory are asynchronous: a second one to the same columns has to wait for the first, which in
+    this path may hold infinities."""
+    text = source("tree_tc_kernels.cu")
+    again = re.search(r"if \(!fresh\) \{(.*?)#pragma unroll", text, re.S).group(1)
+    assert "tmem_wait_st()" in again
