@@ -442,6 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
               w[at + 8] = x.z ^ flip;
               w[at + 9] = x.w ^ flip;
             }
+            __syncwarp();  // lanes without a row loaded nothing
             if (WIDE || (SPLIT_ROWS && i == 1)) {  // (uniform per warp)
               uint8_t* d = smem + S::Q_OFF + ((WIDE && SPLIT_ROWS) ? i * S::Q_TILE : 0) + kh * 8 * (128 * 16) + row * 16;
 #pragma unroll
@@ -594,6 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
 #pragma unroll 1
           for (int c0 = c_begin; c0 < c_begin + COLS; c0 += 16) {
             uint32_t o[16], o1[SPLIT_ROWS ? 1 : 16];
+            __syncwarp();  // lanes without a row have come round early
             tmem_ld16(tmem + lanes + S::TM_O + (SPLIT_ROWS ? i * D : 0) + c0, o);
             if constexpr (!SPLIT_ROWS) {
               if (have1) tmem_ld16(tmem + lanes + S::TM_O + D + c0, o1);

@@ -37,3 +37,13 @@ def test_the_second_pass_over_a_tile_stores_its_weights_after_the_firsts():
     text = source("tree_tc_kernels.cu")
     again = re.search(r"if \(!fresh\) \{(.*?)#pragma unroll", text, re.S).group(1)
     assert "tmem_wait_st()" in again
+
+
+def test_lanes_without_a_row_meet_their_warp_before_it_moves_tensor_memory():
+    """tcgen05.ld and .st are the whole warp's: what only the lanes with a query row do stands between a __syncwarp and
+    the one before."""
+    text = source("tree_tc_kernels.cu")
+    out = re.search(r"for \(int c0 = c_begin;.*?\{(.*?)tmem_ld16", text, re.S).group(1)
+    assert "__syncwarp()" in out
+    query = re.search(r"if \(live\) x = (.*?)tmem_st32", text, re.S).group(1)
+    assert "__syncwarp()" in query
