@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(128) tree_rows16_kernel(const __grid_constant_
   while (next_segment<kRows, kUnit>(args_s, slice_s, walk)) {
     const int h = seg.h, len = seg.r.len, total = len + seg.r.nodes, row0 = seg.tile * kRows;
     const int rows = min(kRows, seg.r.nodes * gq - row0);
-    const int nblk = (total + kBlock - 1) / kBlock;
+    const int nblk = tree_units(total, kBlock);
     const int j_begin = seg.u0 * 4, j_end = min(seg.u1 * 4, nblk);
     const int n_mine = (!dead && j_end - j_begin > warp) ? (j_end - j_begin - warp + 3) / 4 : 0;
     const int32_t* table = a.block_table + static_cast<long long>(seg.b) * a.max_blocks;
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(128) tree_rows16_kernel(const __grid_constant_
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[e][i] = sacc[i >> 1][2 * e + (i & 1)] * kmul;
-      if (tok_base + kBlock > len) {  // the tree's own tokens, and rows behind them
+      if (tree_beyond(tok_base, kBlock, len)) {  // the tree's own tokens, and rows behind them
         uint32_t keep = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

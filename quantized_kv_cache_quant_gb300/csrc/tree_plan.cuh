@@ -18,11 +18,25 @@
 // blocks' first segments.
 #pragma once
 
+#include <climits>
+
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
 #include "spec_internal.h"
 
 namespace kvq {
+
+// Lengths go up to the longest table, 16 below 2^31: neither of these leaves 31 bits there.
+constexpr int kTreeLongest = INT_MAX / 16 * 16;
+// Units of n tokens (n > 0).
+__host__ __device__ constexpr int tree_units(int n, int unit) { return (n - 1) / unit + 1; }
+// Whether the n tokens from tok on reach beyond the first len.
+__host__ __device__ constexpr bool tree_beyond(int tok, int n, int len) { return tok > len - n; }
+static_assert(tree_units(1, 64) == 1 && tree_units(64, 64) == 1 && tree_units(65, 64) == 2);
+static_assert(tree_units(kTreeLongest, 64) == 1 << 25 && tree_units(kTreeLongest, 16) == INT_MAX / 16);
+static_assert(!tree_beyond(0, 16, 16) && tree_beyond(1, 16, 16) && tree_beyond(0, 64, 0));
+static_assert(tree_beyond(((1 << 25) - 1) * 64, 64, kTreeLongest) && !tree_beyond(((1 << 25) - 2) * 64, 64, kTreeLongest));
+static_assert(!tree_beyond(kTreeLongest - 16, 16, kTreeLongest) && tree_beyond(kTreeLongest - 16, 16, kTreeLongest - 1));
 
 struct TreeRequest {
   int first, nodes, len;  // first row, rows, tokens before them
@@ -38,7 +52,7 @@ __device__ __forceinline__ TreeRequest tree_request(const TreeArgs& a, int b) {
   r.nodes = static_cast<int>(min(max(rows, 0ll), static_cast<long long>(min(min(a.max_tree, cap), a.n_tokens - r.first))));
   r.len = min(max(a.seq_lens[b], 0), cap - r.nodes);
   r.tiles = (r.nodes * gq + R - 1) / R;
-  r.units = r.nodes > 0 ? (r.len + r.nodes + UNIT - 1) / UNIT : 0;
+  r.units = r.nodes > 0 ? tree_units(r.len + r.nodes, UNIT) : 0;
   return r;
 }
 

@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     unsigned n = 0;  // tiles issued
     bool ok = true;
     while (ok && next()) {
-      const int nblk = (seg.r.len + seg.r.nodes + kBlock - 1) / kBlock;
+      const int nblk = tree_units(seg.r.len + seg.r.nodes, kBlock);
       const int32_t* table = a.block_table + static_cast<long long>(seg.b) * a.max_blocks;
       const uint8_t* pool = ((lane & 1) ? a.v_pool : a.k_pool) + static_cast<long long>(seg.h) * (kBlock * D);
       const int i = lane >> 1, u0 = seg.u0, u1 = seg.u1;
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         for (int w = 0; w < 2; ++w) {
           const int tok0 = t * kTile + (w0 + w) * kBlock;
           uint32_t keep = 0xFFFFFFFFu;
-          if (tok0 + kBlock > len) {  // the tree's own tokens, and rows behind them
+          if (tree_beyond(tok0, kBlock, len)) {  // the tree's own tokens, and rows behind them
             uint32_t tree_bytes = 0;
             keep = 0;
 #pragma unroll
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         }
         const int tok0 = t * kTile;
         uint64_t vis = ~0ull;
-        const bool edge = tok0 + kTile > len;
+        const bool edge = tree_beyond(tok0, kTile, len);
         if (edge && warp_live) vis = tree_window(mask, a.mask_words, tok0, len, total);
         tmem_wait_ld();
         tc_fence_before();
