@@ -70,9 +70,11 @@ KVQ_API kvq_status kv_blocks_resize(int32_t* block_table, int32_t batch, int32_t
  *   slots     : device int64 [n_rows]; row offsets[b] + i is position
  *               p = seq_lens[b] + i: block_table[b, p / block_tokens] *
  *               block_tokens + p % block_tokens, or -1 where p lies outside the
- *               table's row or its entry outside [0, num_blocks)
+ *               table's row or 31 bits, or its entry outside [0, num_blocks)
  *   seq_ids   : device int32 [n_rows], b; may be NULL
- *   positions : device int32 [n_rows], p; may be NULL
+ *   positions : device int32 [n_rows], p (-1 where it leaves 31 bits): the
+ *               token's place in the cache. For the nodes of a tree that is
+ *               not their depth, which a rotary embedding goes by. May be NULL
  * Rows behind the last request get -1 in all three, which the append skips: a
  * padded batch needs no other care. */
 KVQ_API kvq_status kv_slot_map(const int32_t* block_table, int32_t batch, int32_t max_blocks, const int32_t* seq_lens,

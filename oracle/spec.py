@@ -45,10 +45,11 @@ def slot_map(table, seq_lens, new_lens, block_tokens, num_blocks, rows):
         for p in range(int(n0), int(n0) + max(0, int(n))):
             if len(slots) == rows:
                 break
-            blk = int(table[b, p // block_tokens]) if p // block_tokens < width else -1
+            inside = 0 <= p < min(width * block_tokens, 2**31)
+            blk = int(table[b, p // block_tokens]) if inside else -1
             slots.append(blk * block_tokens + p % block_tokens if 0 <= blk < num_blocks else -1)
             seqs.append(b)
-            poss.append(p)
+            poss.append(p if p < 2**31 else -1)
         offsets.append(len(slots))
     pad = [-1] * (rows - len(slots))
     return (np.array(offsets, np.int32), np.array(slots + pad, np.int64), np.array(seqs + pad, np.int32),

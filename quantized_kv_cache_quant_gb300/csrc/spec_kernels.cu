@@ -210,7 +210,6 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(SlotMapArgs a) {
     long long slot[4];
     int seq[4], pos[4];
     int b = i0 < n ? owner_of(a.batch, i0, [&](int m) { return off_s[m]; }) : 0;
-    // positions that leave 31 bits lie outside every table
     int next = i0 < n ? off_s[b + 1] : 0, j = 0, block = -1;
     long long p = 0;
     int row = 0;  // p's row in its block
@@ -224,22 +223,18 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(SlotMapArgs a) {
           next = off_s[++b + 1];
           fresh = true;
         }
-        if (fresh) {  // the one division of most threads
-          p = static_cast<long long>(a.seq_lens[b]) + (i - off_s[b]);
-          j = p >= 0 && p <= INT_MAX ? static_cast<int>(p) / a.block_tokens : a.max_blocks;
-          row = static_cast<int>(p - static_cast<long long>(j) * a.block_tokens);
-        } else {
-          ++p;
-          if (++row == a.block_tokens) {
-            row = 0;
-            ++j;
-            fresh = true;
-          }
+        p = fresh ? static_cast<long long>(a.seq_lens[b]) + (i - off_s[b]) : p + 1;
+        if (p < 0 || p > INT_MAX) {  // outside every table
+          block = -1;
+        } else if (fresh || p == 0 || ++row == a.block_tokens) {
+          // the one division of most threads; behind a position outside, 0 begins the table, behind a block the next one
+          j = fresh ? static_cast<int>(p) / a.block_tokens : p == 0 ? 0 : j + 1;
+          row = fresh ? static_cast<int>(p) - j * a.block_tokens : 0;
+          block = j < a.max_blocks ? a.block_table[static_cast<long long>(b) * a.max_blocks + j] : -1;
         }
-        if (fresh) block = j < a.max_blocks && p <= INT_MAX ? a.block_table[static_cast<long long>(b) * a.max_blocks + j] : -1;
         fresh = false;
         seq[e] = b;
-        pos[e] = static_cast<int>(p);
+        pos[e] = p <= INT_MAX ? static_cast<int>(p) : -1;
         if (block >= 0 && block < a.num_blocks) slot[e] = static_cast<long long>(block) * a.block_tokens + row;
       }
     }
