@@ -147,9 +147,12 @@ KVQ_API size_t fp8_tree_workspace_bytes(int32_t batch, int32_t kv_heads, int32_t
  * max_seq_len bounds seq_lens[b] + the nodes of b; max_seq_len <= max_blocks *
  * 16. Lengths, offsets and table entries are clamped on the device: a bad one
  * gives wrong numbers, never an access outside the buffers.
- * With fp16 output the softmax weights are rounded to fp16 for the value
- * product (2^-11 relative, as the output itself); with fp32 output they are
- * carried in two fp16 parts. Scores, sums and outputs accumulate in fp32.
+ * The softmax weights go into the value product in two fp16 parts (2^-22
+ * relative), as fp8_decode_attention's, for fp32 output, for max_tree *
+ * (q_heads / kv_heads) <= 16, and for little work altogether (max_seq_len <=
+ * 2560, few tiles of 16 rows). Larger calls with fp16 output round them to one
+ * (2^-11 relative, as the output itself): two would take them 1.5 to 1.8 times
+ * as long. Scores, sums and outputs accumulate in fp32.
  * KVQ_ERR_UNSUPPORTED for max_tree > KVQ_TREE_MAX, batch > KVQ_SPEC_MAX_BATCH
  * or q_heads / kv_heads > KVQ_TREE_MAX_GQA; KVQ_ERR_ARG for mask_words * 64 <
  * max_tree. */

@@ -12,14 +12,15 @@ constexpr int kBlock = 16;  // tokens of an FP8 pool block
 // through its own ring of bulk copies, with its own running maximum, sum and
 // outputs, joined at the end of the segment.
 //   q.k^T: A = q (channels permuted as the keys' order), B = the keys as fp16
-//   p.V  : A = p rounded to fp16 (WIDE: and what the rounding left, on a
-//          second product), B = the values as fp16
+//   p.V  : A = p rounded to fp16 and, on a second product, what the rounding
+//          left (2^-22 of p, as the decode of one token), B = the values as fp16
 // p carries a factor 2^kBias so that weights down to 2^-24 of the largest stay
 // normal fp16 numbers.
 // Bound by the memory: 32 requests x 32768 tokens, 8 heads, D = 128, 16 rows in
-// 335 us, 6.3 TB/s, 93 % of the measured copy rate; three blocks an SM (168
-// registers) keep four copies of 4 KB a warp in flight. A tile of 32 rows on this
-// layout spilled and took 331 us for the 128K chains that tcgen05 does in 240.
+// 370 us on random pages, 5.8 TB/s, 85 % of the measured copy rate (383 us with
+// cold caches, 375 with p in one part); three blocks an SM (168 registers) keep
+// four copies of 4 KB a warp in flight. A tile of 32 rows on this layout spilled
+// and took a third longer than tcgen05 for chains of 4 over 128K tokens.
 // ---------------------------------------------------------------------------
 constexpr int kRows = 16;
 constexpr int kUnit = 64;    // tokens of a unit: one block a warp
@@ -36,7 +37,7 @@ struct TreeSmem {
   static constexpr int BYTES = BAR_BYTES + AREA;
 };
 
-template <int D, int FMT, bool WIDE>
+template <int D, int FMT>
 __global__ void __launch_bounds__(128) tree_rows16_kernel(const __grid_constant__ TreeArgs a) {
   using S = TreeSmem<D>;
   constexpr int KS = D / 16, NT = D / 8, CH = D / 32;
@@ -220,17 +221,15 @@ __global__ void __launch_bounds__(128) tree_rows16_kernel(const __grid_constant_
         const __half2 h0 = __floats2half2_rn(p[0], p[1]), h1 = __floats2half2_rn(p[2], p[3]);
         A[e] = h2_bits(h0);
         A[2 + e] = h2_bits(h1);
-        if constexpr (WIDE) {
-          const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-          L[e] = pack_rn_f16x2(p[0] - f0.x, p[1] - f0.y);
-          L[2 + e] = pack_rn_f16x2(p[2] - f1.x, p[3] - f1.y);
-        }
+        const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+        L[e] = pack_rn_f16x2(p[0] - f0.x, p[1] - f0.y);
+        L[2 + e] = pack_rn_f16x2(p[2] - f1.x, p[3] - f1.y);
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const uint32_t b0 = fp8_lo_pair<FMT>(vw[nt]), b1 = fp8_hi_pair<FMT>(vw[nt]);
         mma16816(o_acc[nt], A[0], A[1], A[2], A[3], b0, b1);
-        if constexpr (WIDE) mma16816(o_acc[nt], L[0], L[1], L[2], L[3], b0, b1);
+        mma16816(o_acc[nt], L[0], L[1], L[2], L[3], b0, b1);
       }
       __syncwarp();
       if (lane == 0 && j + kStages < n_mine) {
@@ -304,10 +303,10 @@ __global__ void __launch_bounds__(128) tree_rows16_kernel(const __grid_constant_
   }
 }
 
-template <int D, int FMT, bool WIDE>
+template <int D, int FMT>
 cudaError_t launch_rows16(const TreeArgs& a, cudaStream_t s) {
   constexpr int smem = TreeSmem<D>::BYTES;
-  auto kern = tree_rows16_kernel<D, FMT, WIDE>;
+  auto kern = tree_rows16_kernel<D, FMT>;
   static SharedMemoryOnce once;
   int per_sm = 0;
   cudaError_t e = once.set(kern, smem, 128, &per_sm);
@@ -427,21 +426,17 @@ cudaError_t launch_tree_join(const TreeArgs& a, int blocks, int tile_rows, cudaS
 
 cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s) {
   // Up to 16 rows a kv head, and little work altogether: few tiles of 16 rows over at most 2560 tokens, where the wider
-  // kernel's longer change of segments decides (8 heads, one request: trees of 5 at 1000 tokens 14.0 us here and 15.8
-  // there, of 32 17.6 and 23.2, at 2500 tokens 23.0 and 24.0, at 5000 30.1 and 29.1; 16 requests at 1000 26 and 22).
+  // kernel's longer change of segments decides (8 heads, one request: trees of 5 at 1000 tokens 14.0 us here and 15.7
+  // there, of 32 17.8 and 24.4, at 2500 tokens 24.5 and 24.7, at 5000 32.1 and 29.9; 16 requests at 1000 27 and 23).
   const int rows = a.max_tree * (a.q_heads / a.kv_heads);
   const long long tiles = static_cast<long long>(a.batch) * a.kv_heads * ((rows + kRows - 1) / kRows);
   if (rows > kRows && (tiles > 64 || a.max_seq_len > 2560)) return launch_tree_tc(a, s);
   static_assert(2 * kTreeMaxBlocks * kRows <= kTreePartRows, "partial results fit the workspace");
-  switch (a.head_dim * 100 + a.fmt * 10 + (a.out_fp32 ? 1 : 0)) {
-    case 12800: return launch_rows16<128, 0, false>(a, s);
-    case 12801: return launch_rows16<128, 0, true>(a, s);
-    case 12810: return launch_rows16<128, 1, false>(a, s);
-    case 12811: return launch_rows16<128, 1, true>(a, s);
-    case 6400: return launch_rows16<64, 0, false>(a, s);
-    case 6401: return launch_rows16<64, 0, true>(a, s);
-    case 6410: return launch_rows16<64, 1, false>(a, s);
-    case 6411: return launch_rows16<64, 1, true>(a, s);
+  switch (a.head_dim * 10 + a.fmt) {
+    case 1280: return launch_rows16<128, 0>(a, s);
+    case 1281: return launch_rows16<128, 1>(a, s);
+    case 640: return launch_rows16<64, 0>(a, s);
+    case 641: return launch_rows16<64, 1>(a, s);
     default: return cudaErrorInvalidValue;
   }
 }
