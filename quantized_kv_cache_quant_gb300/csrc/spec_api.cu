@@ -10,6 +10,9 @@
 
 namespace {
 
+static_assert(kvq::kSpecMaxBatch == KVQ_SPEC_MAX_BATCH, "the kernels' arrays hold what the checks let through");
+static_assert(kvq::kTreeMax == KVQ_TREE_MAX, "the same");
+
 bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

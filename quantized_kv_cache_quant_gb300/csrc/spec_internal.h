@@ -10,7 +10,6 @@ namespace kvq {
 
 constexpr int kSpecMaxBatch = 4096;  // KVQ_SPEC_MAX_BATCH
 constexpr int kTreeMax = 256;        // KVQ_TREE_MAX
-constexpr int kTreeMaxGqa = 64;      // KVQ_TREE_MAX_GQA
 
 // A kernel's shared-memory limit, raised once per device (and its resident
 // blocks per SM asked once): both calls cost more than a small launch. Two

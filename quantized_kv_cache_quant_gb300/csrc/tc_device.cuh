@@ -191,11 +191,7 @@ __device__ __forceinline__ bool role_wait_warp(uint64_t* bar, uint32_t parity, v
   }
 }
 
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-// named_barrier that returns whether `ok` was true in all its threads.
+// Barrier `id` of `threads` threads; whether `ok` was true in all of them.
 __device__ __forceinline__ bool barrier_and(int id, int threads, bool ok) {
   uint32_t all;
   asm volatile(

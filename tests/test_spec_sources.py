@@ -47,3 +47,20 @@ def test_lanes_without_a_row_meet_their_warp_before_it_moves_tensor_memory():
     assert "__syncwarp()" in out
     query = re.search(r"if \(live\) x = (.*?)tmem_st32", text, re.S).group(1)
     assert "__syncwarp()" in query
+
+
+def test_what_the_headers_of_these_calls_define_is_used():
+    files = {n: source(n) for n in os.listdir(CSRC) if n.endswith((".cu", ".cuh", ".h"))}
+    everything = "\n".join(files.values())
+    for name in ("tc_device.cuh", "tree_plan.cuh", "spec_internal.h"):
+        defined = re.findall(r"__forceinline__ [\w:<>]+ (\w+)\(", files[name]) + re.findall(r"constexpr \w+ (k[A-Z]\w*) =", files[name])
+        assert defined
+        for d in defined:
+            assert len(re.findall(rf"\b{d}\b", everything)) > 1, f"{name}: {d}"
+
+
+def test_limits_of_the_kernels_are_the_headers():
+    """The kernels' shared arrays go by constants of their own, the host's checks by the public header's."""
+    text = source("spec_api.cu")
+    for own, public in (("kSpecMaxBatch", "KVQ_SPEC_MAX_BATCH"), ("kTreeMax", "KVQ_TREE_MAX")):
+        assert re.search(rf"static_assert\([^;]*kvq::{own} == {public}\b", text), own
