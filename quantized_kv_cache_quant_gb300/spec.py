@@ -78,7 +78,7 @@ def _rows(name: str, t, n, heads: int, dim: int, dev: int):
         raise ValueError(f"{name}: contiguous [heads, dim] rows expected")
     if t.get_device() != dev:
         raise ValueError(f"{name}: on {t.device}, not on cuda:{dev}")
-    return t.data_ptr(), row if n > 1 else max(row, heads * dim)
+    return t.data_ptr(), row if n > 1 else heads * dim
 
 
 def _here(t) -> int:
