@@ -19,6 +19,8 @@
  * they can be slices of a fused projection's output.
  *
  * A slot is the place of one token in the pools: block * block_tokens + row.
+ * A call without tokens, rows or requests is refused: a step that adds nothing
+ * makes none.
  * Calls that work on one pool, table or workspace run on one stream, or are
  * ordered by the caller.
  */
@@ -107,8 +109,9 @@ KVQ_API kvq_status fp8_kv_append(const fp8_pool* k, const fp8_pool* v, const uin
  *                nodes are numbered parents first), each in [0, KVQ_TREE_MAX)
  *   n_accepted : device int32 [batch], in [0, path_len]
  *   new_lens   : device int32 [batch]; may be seq_lens itself
- * Rows that stay in place are not written. Entries outside the table or the
- * pool are skipped. */
+ * Rows that stay in place keep their bytes (values are stored whole 16-byte
+ * units at a time, with the bytes of up to three tokens beside a moved one as
+ * they were). Entries outside the table or the pool are skipped. */
 KVQ_API kvq_status fp8_kv_accept(const fp8_pool* k, const fp8_pool* v, const int32_t* block_table, int32_t batch,
                                  int32_t max_blocks, const int32_t* seq_lens, const int32_t* path, int32_t path_len,
                                  const int32_t* n_accepted, int32_t* new_lens, void* stream);
@@ -122,7 +125,9 @@ KVQ_API kvq_status fp8_kv_accept(const fp8_pool* k, const fp8_pool* v, const int
  * results and which of them belong together. Zero it once after allocating it
  * (the status word collects errors until it is cleared). One workspace serves
  * one stream: calls that overlap on the device (two captured graphs among
- * them) must not share it. 0 for shapes the call refuses. */
+ * them) must not share it. The size goes by head_dim alone (43 MB at 128, 22 MB
+ * at 64: what the blocks of one launch can leave); 0 for shapes the call
+ * refuses. */
 KVQ_API size_t fp8_tree_workspace_bytes(int32_t batch, int32_t kv_heads, int32_t q_heads, int32_t head_dim,
                                         int32_t max_tree);
 

@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(1024) blocks_resize_kernel(BlocksResizeArgs a)
 // Slot map: every thread block scans the requests' new lengths itself (no
 // second launch), then takes its share of the rows, four to a thread. 16 bytes
 // are written a row: 2.16 million rows in 10.7 us, 3.2 TB/s (the output stays in
-// L2); a few rows in 4.2 us, the scan and two dependent reads.
+// L2); a few rows in 3.7 us, the scan and two dependent reads.
 // ---------------------------------------------------------------------------
 constexpr int kMapThreads = 256;
 
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) fp8_append_kernel(Fp8Append
 //           same warp's) and writes the unit whole. Byte by byte this took 18 us
 //           for 256 requests x 8 rows: 2.1 million writes of parts of sectors.
 // One request: 4.5 us, a chain of dependent reads (length, path, table, rows).
-// 256 requests x 12 rows: 14.5 us; a value row touches all 64 sectors of its
+// 256 requests x 12 rows: 14.2 us; a value row touches all 64 sectors of its
 // block and head, 16 times its bytes, and that is what is moved.
 // ---------------------------------------------------------------------------
 constexpr int kAcceptBatch = 8;

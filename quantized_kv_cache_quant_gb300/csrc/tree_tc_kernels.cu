@@ -11,8 +11,8 @@
 //   S = Q K^T : A = Q (fp16, exact) in tensor memory, or in shared memory where
 //               tensor memory has no room, B = the keys as fp16 in shared
 //               memory, accumulators 128 x 64 fp32 in tensor memory
-//   O += P V  : A = P in tensor memory (fp16; WIDE: and the rounding's
-//               remainder), B = the values as fp16
+//   O += P V  : A = P in tensor memory (fp16; WIDE, for fp32 output: and the
+//               rounding's remainder), B = the values as fp16
 // Tensor memory's 512 columns (D = 128): O 2 x 128, S 2 x 64, P 2 x 32 and Q 64,
 // or with WIDE P 2 x 64 and no Q. P beside S, not over it, is what lets a
 // stream's next scores run under its softmax: with P over S a tile took 1220
@@ -33,16 +33,18 @@
 // e is token 8r + 2t + e), so that both conversions read 16-byte units and
 // write 16- and 8-byte pieces, all without bank conflicts.
 //
-// What bounds it. R = 128: 1050 clocks a tile, where the memory needs 745, the
-// products 512 and the softmax 690. A place of the fp16 ring lives 4200 clocks
-// from the conversion (1250) over the scores (900) and the softmax (1380) to the
-// product (700), and four places are what shared memory holds. R = 256: the two
-// streams' softmax, 1430 of 1900 clocks each (exponentials and the packing to
-// fp16 share a pipe); the products need 1024. Measured, 8 kv heads, D = 128, E4M3:
-//   32 requests x 32768 tokens, trees of 16, 64 rows   472 us  4.5 TB/s
-//   4 requests x 131072 tokens, chains of 4, 32 rows   240 us  4.4 TB/s
-//   16 requests x 16384 tokens, 63 nodes, 504 rows     445 us  1210 TFLOP/s
-//   16 requests x 400 tokens, trees of 16               16 us
+// What bounds it: the chain within a stream. P has one buffer, so a stream's
+// weights of a tile wait for the product of its tile before: 1380 clocks of
+// softmax and 700 of product and commit with R = 128, 2080 a tile of the stream
+// and, with two streams on alternate tiles, 1040 a tile, whatever D; the memory
+// needs 745, the products 512. (Six places in the fp16 ring in place of four, at
+// D = 64, changed nothing.) R = 256: 1430 and 500, 1930 a tile; the products need
+// 1024. Weights in two parts (WIDE) take 1.5 to 1.8 times as long. Measured on
+// random pages, cold caches, 8 kv heads, E4M3 at D = 128, E5M2 per head at D = 64:
+//   32 requests x 32768 tokens, trees of 16, 64 rows   512 us  4.2 TB/s (WIDE 875)
+//   4 requests x 131072 tokens, chains of 4, 32 rows   259 us  4.1 TB/s (WIDE 424)
+//   16 requests x 16384 tokens, 63 nodes, 504 rows     505 us  1075 TFLOP/s (WIDE 885)
+//   32 requests x 512 to 16384 tokens, 1 to 40 nodes, D = 64   195 us (WIDE 287)
 // Between segments: about 8000 clocks from the last scores of one to the first
 // of the next (outputs 4000, queries 2000, the next segment 1500).
 #include "tc_device.cuh"
@@ -73,7 +75,8 @@ struct TcPlan {
   // Both rings have an even number of places: the converting pairs take tiles of alternate parity, and so a place
   // always belongs to one pair, which sees each phase of its barriers. (In an odd ring a pair meets a place every second
   // time round, and its wait for a phase's parity is over while the phase before still runs.)
-  static constexpr int BUFS = Q_SMEM == 2 ? 2 : kMaxBufs;  // (2 in place of 4: 690 / 536 / 340 us for 492 / 448 / 244)
+  // (2 places in place of 4 where 4 fit: 690, 536 and 340 us for 492, 448 and 244 of an earlier state)
+  static constexpr int BUFS = Q_SMEM == 2 ? 2 : kMaxBufs;
   static constexpr int FIXED = BUFS * 2 * TILE + Q_SMEM * Q_TILE;
   static constexpr int FIT = (221184 - FIXED) / STAGE;  // 227 KB without what TcShared takes
   static constexpr int STAGES = (FIT < kMaxStages ? FIT : kMaxStages) & ~1;
