@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     if (lane == 0) sh.walk[warp].start(s);
   }
   if (warp == kScoreWarp) {
+    __syncwarp();
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
     tc_fence_before();

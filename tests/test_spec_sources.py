@@ -64,3 +64,9 @@ def test_limits_of_the_kernels_are_the_headers():
     text = source("spec_api.cu")
     for own, public in (("kSpecMaxBatch", "KVQ_SPEC_MAX_BATCH"), ("kTreeMax", "KVQ_TREE_MAX")):
         assert re.search(rf"static_assert\([^;]*kvq::{own} == {public}\b", text), own
+
+
+def test_the_allocating_warp_is_whole_when_it_allocates():
+    """tcgen05.alloc is the whole warp's, and one lane has just written the warp's walk."""
+    before = source("tree_tc_kernels.cu").split("tmem_alloc(", 1)[0]
+    assert "__syncwarp()" in before[before.rindex("walk[warp].start(s)"):]
