@@ -1,0 +1,179 @@
+// C-ABI host layer of the beam-search calls (kvq_beam.h): argument checks and
+// launches.
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "beam_internal.h"
+#include "kvq_beam.h"
+#include "kvq_device.cuh"
+#include "pool_checks.h"
+#include "spec_internal.h"
+
+namespace {
+
+using namespace kvq::checks;
+
+static_assert(kvq::kBeamMaxWidth == KVQ_BEAM_MAX_WIDTH, "the kernels' arrays hold what the checks let through");
+static_assert(kvq::kBeamMaxOut == KVQ_BEAM_MAX_OUT, "the same");
+static_assert(kvq::kCopyMaxBuffers == KVQ_COPY_MAX_BUFFERS, "the same");
+
+// Workspace of the block calls: [what compaction knows | 256 B][words of freed blocks][words of free blocks][ranks before
+// each word][per request].
+size_t padded(size_t n) { return (n + 255) / 256 * 256; }
+size_t words_bytes(int32_t num_blocks) { return padded((static_cast<size_t>(num_blocks) + 31) / 32 * sizeof(uint32_t)); }
+
+kvq_status check_workspace(const void* ws, size_t ws_bytes, int32_t groups, int32_t num_blocks) {
+  if (ws == nullptr) return KVQ_ERR_WORKSPACE;
+  if (!aligned(ws)) return KVQ_ERR_ALIGN;
+  const size_t need = kv_blocks_workspace_bytes(groups, num_blocks);
+  if (need == 0) return KVQ_ERR_UNSUPPORTED;
+  return ws_bytes < need ? KVQ_ERR_WORKSPACE : KVQ_OK;
+}
+
+}  // namespace
+
+kvq_status beam_select(const void* logits, int32_t logits_type, int64_t row_stride, const float* scores,
+                       const uint8_t* finished, int32_t end_token, int32_t groups, int32_t width, int32_t vocab,
+                       int32_t n_out, float* out_scores, int32_t* out_parents, int32_t* out_tokens, void* stream) {
+  if (!logits || !scores || !out_scores || !out_parents || !out_tokens) return KVQ_ERR_NULL;
+  if (logits_type != KVQ_LOGITS_FP16 && logits_type != KVQ_LOGITS_FP32 && logits_type != KVQ_LOGITS_BF16) return KVQ_ERR_ARG;
+  if (groups <= 0 || width <= 0 || vocab <= 0 || n_out <= 0 || n_out > vocab || row_stride < vocab) return KVQ_ERR_ARG;
+  if (finished != nullptr && (end_token < 0 || end_token >= vocab)) return KVQ_ERR_ARG;
+  if (width > KVQ_BEAM_MAX_WIDTH || n_out > KVQ_BEAM_MAX_OUT || vocab > (1 << 30) || groups > (1 << 24))
+    return KVQ_ERR_UNSUPPORTED;
+  const uintptr_t size = logits_type == KVQ_LOGITS_FP32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(logits) % size != 0) return KVQ_ERR_ALIGN;
+  if (!aligned(scores) || !aligned(finished) || !aligned(out_scores) || !aligned(out_parents) || !aligned(out_tokens))
+    return KVQ_ERR_ALIGN;
+  kvq::BeamSelectArgs a{};
+  a.logits = logits;
+  a.row_stride = row_stride;
+  a.scores = scores;
+  a.finished = finished;
+  a.out_scores = out_scores;
+  a.out_parents = out_parents;
+  a.out_tokens = out_tokens;
+  a.type = logits_type;
+  a.end_token = end_token;
+  a.groups = groups;
+  a.width = width;
+  a.vocab = vocab;
+  a.n_out = n_out;
+  return from_cuda(kvq::launch_beam_select(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t kv_blocks_workspace_bytes(int32_t groups, int32_t num_blocks) {
+  if (groups <= 0 || groups > KVQ_SPEC_MAX_BATCH || num_blocks <= 0 || num_blocks > INT_MAX - 31) return 0;
+  return kvq::kWsHeader + 3 * words_bytes(num_blocks) + padded(static_cast<size_t>(groups) * sizeof(int32_t));
+}
+
+kvq_status kv_blocks_fork(int32_t* block_table, int32_t batch, int32_t max_blocks, int32_t* n_held, int32_t* seq_lens,
+                          const int32_t* parents, int32_t width, int32_t block_tokens, int32_t* shares,
+                          int32_t* free_blocks, int32_t* free_count, int32_t num_blocks, int32_t* copy_src,
+                          int32_t* copy_dst, int32_t* copy_count, int32_t* granted, int32_t* shared_blocks, void* ws,
+                          size_t ws_bytes, void* stream) {
+  if (!block_table || !n_held || !seq_lens || !parents || !shares || !free_blocks || !free_count || !copy_src ||
+      !copy_dst || !copy_count)
+    return KVQ_ERR_NULL;
+  if (batch <= 0 || max_blocks <= 0 || width <= 0 || block_tokens <= 0 || num_blocks <= 0) return KVQ_ERR_ARG;
+  if (batch > KVQ_SPEC_MAX_BATCH || width > KVQ_BEAM_MAX_WIDTH || static_cast<long long>(batch) * max_blocks > INT_MAX)
+    return KVQ_ERR_UNSUPPORTED;
+  if (batch % width != 0) return KVQ_ERR_SHAPE;
+  if (!aligned(block_table) || !aligned(n_held) || !aligned(seq_lens) || !aligned(parents) || !aligned(shares) ||
+      !aligned(free_blocks) || !aligned(free_count) || !aligned(copy_src) || !aligned(copy_dst) || !aligned(copy_count) ||
+      !aligned(granted) || !aligned(shared_blocks))
+    return KVQ_ERR_ALIGN;
+  const kvq_status st = check_workspace(ws, ws_bytes, batch / width, num_blocks);
+  if (st != KVQ_OK) return st;
+  kvq::BlocksForkArgs a{};
+  a.block_table = block_table;
+  a.n_held = n_held;
+  a.seq_lens = seq_lens;
+  a.parents = parents;
+  a.shares = shares;
+  a.free_blocks = free_blocks;
+  a.free_count = free_count;
+  a.copy_src = copy_src;
+  a.copy_dst = copy_dst;
+  a.copy_count = copy_count;
+  a.granted = granted;
+  a.shared_blocks = shared_blocks;
+  uint8_t* const base = static_cast<uint8_t*>(ws) + kvq::kWsHeader;
+  a.bits = reinterpret_cast<uint32_t*>(base);
+  a.alike = reinterpret_cast<int32_t*>(base + 3 * words_bytes(num_blocks));
+  a.batch = batch;
+  a.max_blocks = max_blocks;
+  a.width = width;
+  a.block_tokens = block_tokens;
+  a.num_blocks = num_blocks;
+  return from_cuda(kvq::launch_blocks_fork(a, static_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kv_blocks_copy(const kvq_block_buffer* buffers, int32_t n_buffers, int32_t num_blocks, const int32_t* src,
+                          const int32_t* dst, int32_t n_pairs, const int32_t* count, void* stream) {
+  if (!buffers || !src || !dst) return KVQ_ERR_NULL;
+  if (n_buffers <= 0 || num_blocks <= 0 || n_pairs <= 0) return KVQ_ERR_ARG;
+  if (n_buffers > KVQ_COPY_MAX_BUFFERS) return KVQ_ERR_UNSUPPORTED;
+  if (!aligned(src) || !aligned(dst) || !aligned(count)) return KVQ_ERR_ALIGN;
+  kvq::BlocksCopyArgs a{};
+  long long pieces = 0;
+  for (int i = 0; i < n_buffers; ++i) {
+    if (buffers[i].base == nullptr) return KVQ_ERR_NULL;
+    if (buffers[i].block_bytes <= 0 || buffers[i].block_bytes % 16 != 0) return KVQ_ERR_ARG;
+    if (buffers[i].block_bytes > LLONG_MAX / num_blocks) return KVQ_ERR_UNSUPPORTED;
+    if (!aligned(buffers[i].base)) return KVQ_ERR_ALIGN;
+    a.base[i] = static_cast<uint8_t*>(buffers[i].base);
+    a.block_bytes[i] = buffers[i].block_bytes;
+    a.first_piece[i] = static_cast<int32_t>(pieces);
+    pieces += (buffers[i].block_bytes + kvq::kCopyPiece - 1) / kvq::kCopyPiece;
+    if (pieces > INT_MAX) return KVQ_ERR_UNSUPPORTED;
+  }
+  a.first_piece[n_buffers] = static_cast<int32_t>(pieces);
+  a.src = src;
+  a.dst = dst;
+  a.count = count;
+  a.n_buffers = n_buffers;
+  a.n_pairs = n_pairs;
+  a.num_blocks = num_blocks;
+  return from_cuda(kvq::launch_blocks_copy(a, static_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kv_blocks_compact(int32_t* block_table, int32_t batch, int32_t max_blocks, const int32_t* n_held,
+                             int32_t keep_blocks, int32_t* shares, int32_t* free_blocks, int32_t* free_count,
+                             int32_t num_blocks, int32_t* moved_to, int32_t* copy_src, int32_t* copy_dst,
+                             int32_t max_copies, int32_t* copy_count, int32_t* done, void* ws, size_t ws_bytes,
+                             void* stream) {
+  if (!block_table || !n_held || !shares || !free_blocks || !free_count || !moved_to || !copy_src || !copy_dst ||
+      !copy_count || !done)
+    return KVQ_ERR_NULL;
+  if (batch <= 0 || max_blocks <= 0 || num_blocks <= 0 || max_copies <= 0 || keep_blocks < 0 || keep_blocks > num_blocks)
+    return KVQ_ERR_ARG;
+  if (batch > KVQ_SPEC_MAX_BATCH || static_cast<long long>(batch) * max_blocks > INT_MAX) return KVQ_ERR_UNSUPPORTED;
+  if (!aligned(block_table) || !aligned(n_held) || !aligned(shares) || !aligned(free_blocks) || !aligned(free_count) ||
+      !aligned(moved_to) || !aligned(copy_src) || !aligned(copy_dst) || !aligned(copy_count) || !aligned(done))
+    return KVQ_ERR_ALIGN;
+  const kvq_status st = check_workspace(ws, ws_bytes, 1, num_blocks);
+  if (st != KVQ_OK) return st;
+  kvq::BlocksCompactArgs a{};
+  a.block_table = block_table;
+  a.n_held = n_held;
+  a.shares = shares;
+  a.free_blocks = free_blocks;
+  a.free_count = free_count;
+  a.moved_to = moved_to;
+  a.copy_src = copy_src;
+  a.copy_dst = copy_dst;
+  a.copy_count = copy_count;
+  a.done = done;
+  uint8_t* const base = static_cast<uint8_t*>(ws);
+  a.state = reinterpret_cast<kvq::CompactState*>(base);
+  a.bits = reinterpret_cast<uint32_t*>(base + kvq::kWsHeader + words_bytes(num_blocks));
+  a.before = reinterpret_cast<int32_t*>(base + kvq::kWsHeader + 2 * words_bytes(num_blocks));
+  a.batch = batch;
+  a.max_blocks = max_blocks;
+  a.keep = keep_blocks;
+  a.num_blocks = num_blocks;
+  a.max_copies = max_copies;
+  return from_cuda(kvq::launch_blocks_compact(a, static_cast<cudaStream_t>(stream)));
+}

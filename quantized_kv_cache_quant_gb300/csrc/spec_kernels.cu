@@ -4,6 +4,7 @@
 #include <climits>
 #include <cooperative_groups.h>
 
+#include "block_scan.cuh"
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
 #include "spec_internal.h"
@@ -14,31 +15,6 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kBlock = 16;  // tokens of an FP8 pool block
-
-// Exclusive prefix sum of v over the thread block (a multiple of 32 threads),
-// the sum of all in `total`. ws: 32 words of shared memory, free to reuse
-// after the next __syncthreads.
-__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long* ws,
-                                                         unsigned long long& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  unsigned long long inc = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long u = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += u;
-  }
-  if (lane == 31) ws[warp] = inc;
-  __syncthreads();
-  unsigned long long w = lane < warps ? ws[lane] : 0ull;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long u = __shfl_up_sync(0xffffffffu, w, o);
-    if (lane >= o) w += u;
-  }
-  total = __shfl_sync(0xffffffffu, w, 31);
-  const unsigned long long before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
-  return inc - v + (warp > 0 ? before : 0ull);
-}
 
 // The last index b in [0, n) with start(b) <= i, start ascending and start(0) <= i.
 template <class F>
