@@ -153,6 +153,50 @@ KVQ_API kvq_status kv_blocks_compact(int32_t* block_table, int32_t batch, int32_
                                      int32_t max_copies, int32_t* copy_count, int32_t* done, void* ws, size_t ws_bytes,
                                      void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Attention                                                                 */
+/* ------------------------------------------------------------------------ */
+
+/* Workspace of fp8_group_attention: a status word at offset 0 (as
+ * kv_decode_workspace_bytes) and the partial results that the call's kernels
+ * hand over: at head_dim 128 between 17 and 59 MB, and 520 bytes for every query head of
+ * every sequence, up to five times. Zero it once after allocating it (the status
+ * word collects errors until it is cleared). One workspace serves one stream:
+ * calls that overlap on the device (two captured graphs among them) must not
+ * share it. 0 for shapes the call refuses. */
+KVQ_API size_t fp8_group_workspace_bytes(int32_t batch, int32_t width, int32_t kv_heads, int32_t q_heads,
+                                         int32_t head_dim);
+
+/* Decode attention over the FP8 paged cache for sequences that share leading
+ * blocks: as fp8_decode_attention (q in fp16),
+ *   out[b, hq] = softmax(q[b, hq] . (k_scale K)^T * softmax_scale) (v_scale V)
+ * over tokens 0 .. seq_lens[b] - 1 of sequence b, zeros where seq_lens[b] <= 0,
+ * but the blocks that a group's sequences share are read (and converted) once a group:
+ *   q             : device fp16, row b at q + b * q_row_stride is [q_heads, D]
+ *   block_table   : device int32 [batch, max_blocks]
+ *   seq_lens      : device int32 [batch], the new tokens included
+ *   shared_blocks : device int32 [batch / width]: the first shared_blocks[g] table
+ *                   entries of all sequences of group g with a length above 0 are
+ *                   the same, and each of those has at least 16 times as many tokens (kv_blocks_fork
+ *                   writes such numbers; a smaller one, 0 included, only costs time)
+ *   out           : device [batch, q_heads, D], fp32 if out_fp32, else fp16
+ * Rows of a block behind a sequence's last token do not reach it, NaN bytes
+ * included. softmax_scale <= 0 selects 1/sqrt(D). max_seq_len bounds seq_lens[b];
+ * max_seq_len <= max_blocks * 16. Lengths, counts and table entries are clamped on the
+ * device: a bad one gives wrong numbers, never an access outside the buffers.
+ * The softmax weights go into the value product in two fp16 parts (2^-22
+ * relative), but over shared blocks for fp16 output with width * (q_heads /
+ * kv_heads) > 16 in one (2^-11 relative, as the output itself). Scores, sums and
+ * outputs accumulate in fp32. The same call gives the same bits.
+ * KVQ_ERR_UNSUPPORTED for batch > KVQ_SPEC_MAX_BATCH, width >
+ * KVQ_BEAM_MAX_WIDTH or q_heads / kv_heads > KVQ_TREE_MAX_GQA; KVQ_ERR_SHAPE for
+ * batch % width != 0. */
+KVQ_API kvq_status fp8_group_attention(const uint16_t* q, int64_t q_row_stride, const fp8_pool* k, const fp8_pool* v,
+                                       const int32_t* block_table, const int32_t* seq_lens,
+                                       const int32_t* shared_blocks, int32_t batch, int32_t width, int32_t q_heads,
+                                       int32_t max_blocks, int32_t max_seq_len, void* out, int32_t out_fp32,
+                                       float softmax_scale, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

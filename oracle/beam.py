@@ -7,6 +7,8 @@ from __future__ import annotations
 
 import numpy as np
 
+from . import spec
+
 
 def select(logits, scores, n_out, finished=None, end_token=-1):
     """(scores float64, parents, tokens), each [R, n_out], of logits [R * W, V] and scores [R, W]."""
@@ -112,3 +114,18 @@ def compact(table, held, keep, shares, free, max_copies):
             if 0 <= table[i, j] < blocks:
                 table[i, j] = moved[table[i, j]]
     return dict(table=table, shares=shares, free=targets[len(movers):][::-1], pairs=pairs, moved_to=moved, done=1)
+
+
+def group_attention(q16, k_pool, v_pool, k_scale, v_scale, fmt, table, seq_lens, scale):
+    """Float64 decode attention over natural pools [nb, H, 16, D], sequence by sequence: each one's last token is a tree of
+    one node behind the others. Returns what spec.tree_attention returns; zeros for an empty sequence."""
+    n = len(seq_lens)
+    outs = [np.zeros(q16.shape) for _ in range(3)] + [np.zeros(q16.shape[:2])]
+    live = [b for b in range(n) if seq_lens[b] > 0]
+    if live:
+        got = spec.tree_attention(q16[live], k_pool, v_pool, k_scale, v_scale, fmt, np.asarray(table)[live],
+                                  [int(seq_lens[b]) - 1 for b in live], np.arange(len(live) + 1),
+                                  np.ones((len(live), 1), bool), scale)
+        for o, g in zip(outs, got):
+            o[live] = g
+    return tuple(outs)

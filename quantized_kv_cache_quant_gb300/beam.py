@@ -19,15 +19,16 @@ import ctypes
 import torch
 
 from . import kvq
-from .kvq import _check, _lib, c_i32, c_sz, c_vp
-from .spec import _I32, _arg, _here, _on, _table, BlockTables, c_i64
+from .kvq import _check, _lib, _P_F8, c_f32, c_i32, c_sz, c_vp
+from .spec import _F16, _I32, _arg, _here, _on, _rows, _table, BlockTables, c_i64
 
 MAX_WIDTH = 64        # sequences of a request
 MAX_OUT = 128         # candidates of a request
 COPY_MAX_BUFFERS = 160
 LOGITS = {torch.float16: 0, torch.float32: 1, torch.bfloat16: 2}
 
-EXPORTED = ("beam_select", "kv_blocks_workspace_bytes", "kv_blocks_fork", "kv_blocks_copy", "kv_blocks_compact")
+EXPORTED = ("beam_select", "kv_blocks_workspace_bytes", "kv_blocks_fork", "kv_blocks_copy", "kv_blocks_compact",
+            "fp8_group_workspace_bytes", "fp8_group_attention")
 
 
 class block_buffer(ctypes.Structure):
@@ -42,6 +43,9 @@ _SIG = {
     "kv_blocks_copy": ([ctypes.POINTER(block_buffer), c_i32, c_i32, c_vp, c_vp, c_i32, c_vp, c_vp], ctypes.c_int),
     "kv_blocks_compact": ([c_vp, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp,
                            c_sz, c_vp], ctypes.c_int),
+    "fp8_group_workspace_bytes": ([c_i32, c_i32, c_i32, c_i32, c_i32], c_sz),
+    "fp8_group_attention": ([c_vp, c_i64, _P_F8, _P_F8, c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_i32, c_f32,
+                             c_vp, c_sz, c_vp], ctypes.c_int),
 }
 for _name, (_args, _res) in _SIG.items():
     _fn = getattr(_lib, _name)
@@ -166,6 +170,46 @@ def kv_blocks_compact(block_table, n_held, keep_blocks: int, shares, free_blocks
         _on(stream, d))
     if code:
         _check(code, "kv_blocks_compact")
+
+
+def fp8_group_workspace_bytes(batch: int, width: int, kv_heads: int, q_heads: int, head_dim: int) -> int:
+    return int(_lib.fp8_group_workspace_bytes(batch, width, kv_heads, q_heads, head_dim))
+
+
+def group_workspace(batch: int, kv_heads: int, q_heads: int, head_dim: int, width: int, device="cuda"):
+    """A zeroed workspace of fp8_group_attention for these shapes."""
+    n = fp8_group_workspace_bytes(batch, width, kv_heads, q_heads, head_dim)
+    if n == 0:
+        raise kvq.KvqError(6, "fp8_group_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def fp8_group_attention(q, k_pool, v_pool, block_table, seq_lens, shared_blocks, width: int, max_seq_len: int, out,
+                        softmax_scale: float, ws, stream=None) -> None:
+    """Decode attention of sequences in groups of ``width`` whose first
+    shared_blocks int32 [B / width] table entries are the same: these blocks are
+    read once a group. q fp16 [B, Hq, D] (rows may lie apart); out fp16 or fp32
+    [B, Hq, D]; block_table int32 [B, max_blocks]; seq_lens int32 [B] (0: an empty
+    sequence, whose output is 0); ws uint8, zeroed once, at least
+    fp8_group_workspace_bytes."""
+    d = _here(q)
+    if q.dim() != 3:
+        raise ValueError(f"q: [B, Hq, D] expected, not {tuple(q.shape)}")
+    n, hq, dim = q.shape
+    qp, qs = _rows("q", q, n, hq, k_pool.head_dim, d)
+    b, max_blocks = _table(block_table)
+    if b != n:
+        raise ValueError(f"block_table: {n} rows expected, not {b}")
+    if out.shape != q.shape:
+        raise ValueError(f"out: shape {tuple(q.shape)} expected, not {tuple(out.shape)}")
+    wide, size = out.dtype is torch.float32, ws.numel()
+    code = _lib.fp8_group_attention(
+        qp, qs, k_pool, v_pool, _arg("block_table", block_table, _I32, b * max_blocks, d),
+        _arg("seq_lens", seq_lens, _I32, b, d), _arg("shared_blocks", shared_blocks, _I32, b // max(width, 1), d), b, width, hq,
+        max_blocks, max_seq_len, _arg("out", out, torch.float32 if wide else _F16, n * hq * dim, d), int(wide), softmax_scale,
+        _arg("ws", ws, torch.uint8, size, d), size, _on(stream, d))
+    if code:
+        _check(code, "fp8_group_attention")
 
 
 class BeamTables(BlockTables):

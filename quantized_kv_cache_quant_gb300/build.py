@@ -20,7 +20,8 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libkvq.so")
 SOURCES = ["api.cu", "kivi_kernels.cu", "kivi_decode_tr.cu", "fp8_kernels.cu", "nvfp4_kernels.cu",
            "spec_api.cu", "spec_kernels.cu", "tree_kernels.cu", "tree_tc_kernels.cu",
-           "beam_api.cu", "beam_select.cu", "beam_blocks.cu"]
+           "beam_api.cu", "beam_select.cu", "beam_blocks.cu", "group_kernels.cu",
+           "group_tc_kernels.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -31,6 +31,39 @@ kvq_status check_workspace(const void* ws, size_t ws_bytes, int32_t groups, int3
   return ws_bytes < need ? KVQ_ERR_WORKSPACE : KVQ_OK;
 }
 
+// Group attention workspace: [status word | 256 B][records of shared, of own pairs][slots of the 16-row kernel][slots of
+// the tcgen05 kernel][own pairs taken whole][shared pairs taken whole, each copy of a row].
+struct GroupLayout {
+  size_t records[2], slots[2], whole[2], bytes;  // offsets: kind 0 shared, 1 own
+  size_t slot_rows[2], rows;
+  kvq::GroupTile tile;
+};
+GroupLayout group_layout(int32_t batch, int32_t width, int32_t kv_heads, int32_t q_heads, int32_t head_dim) {
+  GroupLayout l{};
+  const int gq = q_heads / kv_heads;
+  l.tile = kvq::group_tile(width * gq);
+  l.rows = static_cast<size_t>(batch) * q_heads;
+  const size_t pairs[2] = {static_cast<size_t>(batch / width) * kv_heads * ((width * gq + l.tile.rows - 1) / l.tile.rows),
+                           static_cast<size_t>(batch) * kv_heads * ((gq + kvq::kGroupRows16 - 1) / kvq::kGroupRows16)};
+  const bool tc = l.tile.rows != kvq::kGroupRows16;
+  l.slot_rows[1] = 2 * kvq::kGroupMaxBlocks * kvq::kGroupRows16;
+  l.slot_rows[0] = tc ? 2 * kvq::kGroupTcMaxBlocks * kvq::kGroupTcRows : l.slot_rows[1];
+  size_t at = kvq::kWsHeader;
+  auto take = [&](size_t n) {
+    const size_t here = at;
+    at += padded(n);
+    return here;
+  };
+  const size_t row = (static_cast<size_t>(head_dim) + 2) * sizeof(float);
+  for (int kind = 0; kind < 2; ++kind) l.records[kind] = take(pairs[kind] * sizeof(kvq::GroupRecord));
+  l.slots[1] = take(l.slot_rows[1] * row);
+  l.slots[0] = tc ? take(l.slot_rows[0] * row) : l.slots[1];
+  l.whole[1] = take(l.rows * row);
+  l.whole[0] = take(l.rows * l.tile.fold * row);
+  l.bytes = at;
+  return l;
+}
+
 }  // namespace
 
 kvq_status beam_select(const void* logits, int32_t logits_type, int64_t row_stride, const float* scores,
@@ -176,4 +209,74 @@ kvq_status kv_blocks_compact(int32_t* block_table, int32_t batch, int32_t max_bl
   a.num_blocks = num_blocks;
   a.max_copies = max_copies;
   return from_cuda(kvq::launch_blocks_compact(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fp8_group_workspace_bytes(int32_t batch, int32_t width, int32_t kv_heads, int32_t q_heads, int32_t head_dim) {
+  if (batch <= 0 || batch > KVQ_SPEC_MAX_BATCH || width <= 0 || width > KVQ_BEAM_MAX_WIDTH || batch % width != 0 ||
+      kv_heads <= 0 || kv_heads > 65535 || q_heads <= 0 || q_heads % kv_heads != 0 ||
+      q_heads / kv_heads > KVQ_TREE_MAX_GQA || (head_dim != 64 && head_dim != 128))
+    return 0;
+  return group_layout(batch, width, kv_heads, q_heads, head_dim).bytes;
+}
+
+kvq_status fp8_group_attention(const uint16_t* q, int64_t q_row_stride, const fp8_pool* k, const fp8_pool* v,
+                               const int32_t* block_table, const int32_t* seq_lens, const int32_t* shared_blocks,
+                               int32_t batch, int32_t width, int32_t q_heads, int32_t max_blocks, int32_t max_seq_len,
+                               void* out, int32_t out_fp32, float softmax_scale, void* ws, size_t ws_bytes, void* stream) {
+  const kvq_status st = check_pools(k, v);
+  if (st != KVQ_OK) return st;
+  if (!q || !block_table || !seq_lens || !shared_blocks || !out) return KVQ_ERR_NULL;
+  if (batch <= 0 || width <= 0 || q_heads <= 0 || max_blocks <= 0 || max_seq_len <= 0) return KVQ_ERR_ARG;
+  const int kv_heads = k->kv_heads, head_dim = k->head_dim;
+  if (batch > KVQ_SPEC_MAX_BATCH || width > KVQ_BEAM_MAX_WIDTH) return KVQ_ERR_UNSUPPORTED;
+  if (batch % width != 0 || q_heads % kv_heads != 0) return KVQ_ERR_SHAPE;
+  if (q_heads / kv_heads > KVQ_TREE_MAX_GQA) return KVQ_ERR_UNSUPPORTED;
+  if (q_row_stride < static_cast<int64_t>(q_heads) * head_dim || q_row_stride % 8 != 0) return KVQ_ERR_ARG;
+  if (max_blocks > INT_MAX / 16) return KVQ_ERR_UNSUPPORTED;
+  if (max_seq_len > max_blocks * 16) return KVQ_ERR_CAPACITY;
+  if (!aligned16(q) || !aligned(block_table) || !aligned(seq_lens) || !aligned(shared_blocks) || !aligned(out))
+    return KVQ_ERR_ALIGN;
+  if (ws == nullptr) return KVQ_ERR_WORKSPACE;
+  if (!aligned(ws)) return KVQ_ERR_ALIGN;
+  const GroupLayout l = group_layout(batch, width, kv_heads, q_heads, head_dim);
+  if (ws_bytes < l.bytes) return KVQ_ERR_WORKSPACE;
+  if (!(softmax_scale == softmax_scale) || std::isinf(softmax_scale)) return KVQ_ERR_ARG;
+  const float scale = softmax_scale > 0.0f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
+  kvq::GroupArgs a{};
+  a.q = q;
+  a.q_stride = q_row_stride;
+  a.k_pool = k->pool;
+  a.v_pool = v->pool;
+  a.k_scale = k->scale;
+  a.v_scale = v->scale;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.shared_blocks = shared_blocks;
+  a.batch = batch;
+  a.width = width;
+  a.q_heads = q_heads;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.max_blocks = max_blocks;
+  a.num_blocks = k->num_blocks;
+  a.max_seq_len = max_seq_len;
+  a.per_head = k->per_head;
+  a.fmt = k->fp8_format;
+  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  a.out = out;
+  a.out_fp32 = out_fp32;
+  uint8_t* const base = static_cast<uint8_t*>(ws);
+  a.status = reinterpret_cast<uint32_t*>(base);
+  for (int kind = 0; kind < 2; ++kind) {
+    kvq::GroupPartials& p = a.part[kind];
+    p.tile_rows = kind == 0 ? l.tile.rows : kvq::kGroupRows16;
+    p.fold = kind == 0 ? l.tile.fold : 1;
+    p.records = reinterpret_cast<kvq::GroupRecord*>(base + l.records[kind]);
+    // (outputs first: their rows are whole 256 bytes)
+    p.o = reinterpret_cast<float*>(base + l.slots[kind]);
+    p.ml = p.o + l.slot_rows[kind] * head_dim;
+    p.whole_o = reinterpret_cast<float*>(base + l.whole[kind]);
+    p.whole_ml = p.whole_o + l.rows * p.fold * head_dim;
+  }
+  return from_cuda(kvq::launch_group_attention(a, static_cast<cudaStream_t>(stream)));
 }

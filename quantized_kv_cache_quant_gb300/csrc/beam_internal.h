@@ -75,4 +75,56 @@ struct BlocksCompactArgs {
 };
 cudaError_t launch_blocks_compact(const BlocksCompactArgs& a, cudaStream_t s);
 
+// What a pair of group attention left (group_plan.cuh): its number of parts,
+// and, where there are several, the slot of the first.
+struct GroupRecord {
+  int parts, slot0;
+};
+
+// Partial results of a kind of pair (kind 0: shared blocks, 1: a sequence's
+// own). Row `row` of a slot or of the pairs that one thread block took whole is
+// `fold` partial rows that have to be joined too.
+struct GroupPartials {
+  GroupRecord* records;  // [requests, kv_heads, tiles]
+  float* ml;             // [slots * tile_rows * fold, 2] (exponent, sum) of parts
+  float* o;              // [slots * tile_rows * fold, D]
+  float* whole_ml;       // [fold, batch * q_heads, 2]
+  float* whole_o;        // [fold, batch * q_heads, D]
+  int tile_rows, fold;
+};
+
+struct GroupArgs {
+  const uint16_t* q;
+  long long q_stride;  // fp16 elements between rows of q
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* shared_blocks;
+  int batch, width, q_heads, kv_heads, head_dim, max_blocks, num_blocks, max_seq_len, per_head, fmt;
+  int kinds;         // bit 0: this launch takes the shared blocks, bit 1: the own ones
+  float scale_log2;  // softmax scale * log2(e)
+  void* out;
+  int out_fp32;
+  uint32_t* status;
+  GroupPartials part[2];
+};
+// Rows of the partial results that the thread blocks of one launch leave in
+// slots: two slots a block.
+constexpr int kGroupMaxBlocks = 1024;       // of the 16-row kernel
+constexpr int kGroupTcMaxBlocks = 160;      // of the tcgen05 kernel
+constexpr int kGroupRows16 = 16, kGroupTcRows = 128;
+// Query rows of a tile of shared blocks, as partial rows each: up to 16 rows a kv head the 16-row kernel, beyond the
+// tcgen05 kernel, whose 128 rows hold 32 or 64 rows 4 or 2 times where that is enough.
+struct GroupTile {
+  int rows, fold;
+};
+constexpr GroupTile group_tile(int rows_per_head) {
+  return rows_per_head <= 16 ? GroupTile{16, 1} : rows_per_head <= 32 ? GroupTile{32, 4} : rows_per_head <= 64 ? GroupTile{64, 2} : GroupTile{128, 1};
+}
+cudaError_t launch_group_attention(const GroupArgs& a, cudaStream_t s);
+cudaError_t launch_group_tc(const GroupArgs& a, cudaStream_t s);  // the shared blocks on tcgen05
+
 }  // namespace kvq

@@ -1,5 +1,6 @@
 // How tree attention's work is cut, and how the pieces of one result are
-// joined; shared by its kernels.
+// joined; shared by its kernels, and the cutting by those of group attention
+// (group_plan.cuh), whose "requests" are other stretches of the cache.
 //
 // The query rows of request b and kv head h are its T nodes x gq query heads
 // (row r: node r / gq, head r % gq), in tiles of R rows. A (b, h, tile) is a
@@ -56,6 +57,14 @@ __device__ __forceinline__ TreeRequest tree_request(const TreeArgs& a, int b) {
   return r;
 }
 
+// Requests of a launch, and the pairs that requests of equal trees would have (the host's numbers alone).
+__device__ __forceinline__ int plan_requests(const TreeArgs& a) { return a.batch; }
+template <int R>
+__device__ __forceinline__ long long plan_pairs(const TreeArgs& a) {
+  const int rows = min((a.n_tokens - 1) / a.batch + 1, a.max_tree) * (a.q_heads / a.kv_heads);
+  return static_cast<long long>(a.batch) * a.kv_heads * ((rows + R - 1) / R);
+}
+
 struct TreeSlice {
   long long total;   // units of all pairs
   int blocks;        // slices that share them
@@ -85,13 +94,14 @@ __device__ __forceinline__ int tree_div(long long u, int v) {
 // memory that nothing else uses until the next __syncthreads after the call.
 // shortest(u): the units that slices get at least, where a pair has about u;
 // snap(u): the snap, 1 or more, of slices of u units.
-template <int R, int UNIT, class Shortest, class Snap>
-__device__ __forceinline__ TreeSlice tree_slice(const TreeArgs& a, unsigned long long* sm, Shortest shortest, Snap snap_of) {
+template <int R, int UNIT, class Args, class Shortest, class Snap>
+__device__ __forceinline__ TreeSlice tree_slice(const Args& a, unsigned long long* sm, Shortest shortest, Snap snap_of) {
   TreeSlice s;
+  const int requests = plan_requests(a);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   auto units_of = [&](int b) -> unsigned long long {
-    if (b >= a.batch) return 0ull;
-    const TreeRequest r = tree_request<R, UNIT>(a, b);
+    if (b >= requests) return 0ull;
+    const auto r = tree_request<R, UNIT>(a, b);
     return static_cast<unsigned long long>(r.units) * r.tiles * a.kv_heads;
   };
   // one chunk of blockDim.x requests: exclusive prefix of v, the chunk's sum in `sum`
@@ -118,14 +128,12 @@ __device__ __forceinline__ TreeSlice tree_slice(const TreeArgs& a, unsigned long
   unsigned long long sum;
   const unsigned long long mine_at = scan(mine, sum);
   unsigned long long total = sum;
-  for (int b0 = blockDim.x; b0 < a.batch; b0 += blockDim.x) {
+  for (int b0 = blockDim.x; b0 < requests; b0 += blockDim.x) {
     (void)scan(units_of(b0 + threadIdx.x), sum);
     total += sum;
   }
   s.total = static_cast<long long>(total);
-  // (the pairs that requests of equal trees would have)
-  const int rows = min((a.n_tokens - 1) / a.batch + 1, a.max_tree) * (a.q_heads / a.kv_heads);
-  const int per = shortest(s.total / (static_cast<long long>(a.batch) * a.kv_heads * ((rows + R - 1) / R)));
+  const int per = shortest(s.total / plan_pairs<R>(a));
   s.blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), (s.total + per - 1) / per));
   const int snap = s.blocks > 0 ? snap_of(s.total / s.blocks) : 1;
   s.snap = snap;
@@ -146,9 +154,9 @@ __device__ __forceinline__ TreeSlice tree_slice(const TreeArgs& a, unsigned long
   };
   claim(threadIdx.x, mine_at, mine);
   unsigned long long carry = 0;
-  if (a.batch > static_cast<int>(blockDim.x)) {
+  if (requests > static_cast<int>(blockDim.x)) {
     (void)scan(mine, carry);
-    for (int b0 = blockDim.x; b0 < a.batch; b0 += blockDim.x) {
+    for (int b0 = blockDim.x; b0 < requests; b0 += blockDim.x) {
       const unsigned long long n = units_of(b0 + threadIdx.x);
       const unsigned long long at = carry + scan(n, sum);
       claim(b0 + threadIdx.x, at, n);
@@ -158,7 +166,7 @@ __device__ __forceinline__ TreeSlice tree_slice(const TreeArgs& a, unsigned long
   __syncthreads();
   // the cut at unit u of request b, whose units begin at `before`
   auto snapped = [&](long long u, int b, long long before) -> long long {
-    const TreeRequest r = tree_request<R, UNIT>(a, b);
+    const auto r = tree_request<R, UNIT>(a, b);
     const long long pair_begin = before + static_cast<long long>(tree_div(u - before, r.units)) * r.units;
     const int in = static_cast<int>(u - pair_begin);
     if (in >= snap && r.units - in >= snap) return u;
@@ -173,19 +181,21 @@ __device__ __forceinline__ TreeSlice tree_slice(const TreeArgs& a, unsigned long
 }
 
 // One pair's share of a slice.
-struct TreeSegment {
+template <class Request>
+struct PlanSegment {
   int b, h, tile;
-  TreeRequest r;
+  Request r;
   long long pair_begin;    // the pair's first unit in the range of all
   int u0, u1;              // units of the pair in this slice
   int slot;                // 2 * block (+ 1): where a partial result goes
   int parts;               // blocks that share the pair
 };
 
-struct TreeWalk {
+template <class Request>
+struct PlanWalk {
   long long at, before;
   int b;
-  TreeSegment seg;
+  PlanSegment<Request> seg;
 
   __device__ __forceinline__ void start(const TreeSlice& s) {
     at = s.begin;
@@ -195,17 +205,20 @@ struct TreeWalk {
   }
 };
 
+using TreeSegment = PlanSegment<TreeRequest>;
+using TreeWalk = PlanWalk<TreeRequest>;
+
 // Walks a slice's segments: w.at is the unit to go on from, w.b and w.before
 // its request, w.seg.r that request once w.seg.b names it. Out of line: the
 // roles of a thread block share one copy (their hot loops and five inlined
 // copies together did not fit the instruction cache). Between two segments every
 // role waits for this, so it reads a request once, not once a pair, and divides
 // in 64 bits only for pairs that blocks share.
-template <int R, int UNIT>
-__device__ __noinline__ bool next_segment(const TreeArgs& a, const TreeSlice& s, TreeWalk& w) {
+template <int R, int UNIT, class Args, class Request>
+__device__ __noinline__ bool next_segment(const Args& a, const TreeSlice& s, PlanWalk<Request>& w) {
   long long at = w.at, before = w.before;
   int b = w.b;
-  TreeSegment& g = w.seg;
+  PlanSegment<Request>& g = w.seg;
   if (at >= s.end) return false;
   if (g.b != b) g.r = tree_request<R, UNIT>(a, b);
   long long n = static_cast<long long>(g.r.units) * g.r.tiles * a.kv_heads;

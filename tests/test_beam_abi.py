@@ -156,3 +156,30 @@ def test_oracle_compact_moves_the_upper_blocks_down():
     assert r["pairs"] == [(4, 0), (6, 2)] and r["table"].tolist() == [[2, 1], [0, 2]]
     assert r["free"] == [3] and r["shares"][2] == 1 and r["shares"][6] == 0 and r["done"] == 1
     assert obeam.compact(np.array([[6, 1], [4, 6]]), [2, 2], 4, [0] * 8, [7, 3, 0, 5, 2], 1)["done"] == 0
+
+
+def _pool(role, fmt=0, per_head=0, blocks=8, heads=2, dim=128):
+    return kvq.fp8_pool_init(role, fmt, per_head, blocks, heads, dim, A, 2 * A)
+
+
+def _group_args():
+    return dict(q=A, qs=1024, k=_pool(0), v=_pool(1), table=A, lens=A, shared=A, batch=8, width=4, hq=8, max_blocks=8, most=128,
+                out=A, wide=0, scale=0.0, ws=A, ws_bytes=1 << 40, stream=None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(v=_pool(0)), ARG), (dict(v=_pool(1, fmt=1)), ARG), (dict(v=_pool(1, heads=4)), SHAPE), (dict(q=None), NULL),
+    (dict(table=None), NULL), (dict(lens=None), NULL), (dict(shared=None), NULL), (dict(out=None), NULL), (dict(batch=0), ARG),
+    (dict(width=0), ARG), (dict(most=0), ARG), (dict(width=3), SHAPE), (dict(hq=7), SHAPE), (dict(batch=4100), UNSUPPORTED),
+    (dict(width=65, batch=65), UNSUPPORTED), (dict(hq=130, qs=130 * 128), UNSUPPORTED), (dict(qs=1016), ARG),
+    (dict(qs=1028), ARG), (dict(most=129), CAPACITY), (dict(q=A + 8), ALIGN), (dict(shared=A + 4), ALIGN),
+    (dict(out=A + 16), ALIGN), (dict(ws=None), WORKSPACE), (dict(ws=A + 16), ALIGN), (dict(ws_bytes=1 << 20), WORKSPACE),
+    (dict(scale=float("nan")), ARG), (dict(scale=float("inf")), ARG)])
+def test_group_refusals(change, code):
+    assert _call("fp8_group_attention", _group_args(), change) == code
+
+
+@pytest.mark.parametrize("args", [(0, 1, 2, 8, 128), (8, 3, 2, 8, 128), (8, 0, 2, 8, 128), (65, 65, 2, 8, 128), (8, 4, 0, 8, 128),
+                                  (8, 4, 2, 7, 128), (8, 4, 2, 8, 96), (4097, 1, 2, 8, 128), (8, 4, 1, 65, 128)])
+def test_group_workspace_query_refuses(args):
+    assert beam.fp8_group_workspace_bytes(*args) == 0
