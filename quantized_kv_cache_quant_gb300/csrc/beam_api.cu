@@ -31,8 +31,8 @@ kvq_status check_workspace(const void* ws, size_t ws_bytes, int32_t groups, int3
   return ws_bytes < need ? KVQ_ERR_WORKSPACE : KVQ_OK;
 }
 
-// Group attention workspace: [status word | 256 B][records of shared, of own pairs][slots of the 16-row kernel][slots of
-// the tcgen05 kernel][own pairs taken whole][shared pairs taken whole, each copy of a row].
+// Group attention workspace: [status word | 256 B][records of shared, of own pairs][slots of own pairs][slots of shared
+// pairs][own pairs taken whole][shared pairs taken whole, each copy of a row].
 struct GroupLayout {
   size_t records[2], slots[2], whole[2], bytes;  // offsets: kind 0 shared, 1 own
   size_t slot_rows[2], rows;
@@ -57,7 +57,7 @@ GroupLayout group_layout(int32_t batch, int32_t width, int32_t kv_heads, int32_t
   const size_t row = (static_cast<size_t>(head_dim) + 2) * sizeof(float);
   for (int kind = 0; kind < 2; ++kind) l.records[kind] = take(pairs[kind] * sizeof(kvq::GroupRecord));
   l.slots[1] = take(l.slot_rows[1] * row);
-  l.slots[0] = tc ? take(l.slot_rows[0] * row) : l.slots[1];
+  l.slots[0] = take(l.slot_rows[0] * row);
   l.whole[1] = take(l.rows * row);
   l.whole[0] = take(l.rows * l.tile.fold * row);
   l.bytes = at;

@@ -376,7 +376,7 @@ def random_tables(rng, batch, width, blocks, most):
     for x, c in zip(*np.unique(table[table >= 0], return_counts=True)):
         shares[x] = c - 1
     used = set(table[table >= 0].tolist())
-    outside = [int(x) for x in perm[at:at + max(0, (blocks - at) // 10)]]   # held by nobody in the tables
+    outside = {int(x) for x in perm[at:at + max(0, (blocks - at) // 10)]}   # held by nobody in the tables
     free = [int(x) for x in rng.permutation(blocks) if x not in used and x not in outside]
     return table, held.astype(np.int32), shares, free
 
