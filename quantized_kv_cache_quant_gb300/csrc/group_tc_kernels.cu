@@ -156,30 +156,43 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
   };
 
   if (warp == kCopyWarp) {
-    // ---- copies: lane 2i + r takes block i of a tile, r = 0 keys, 1 values ----
+    // ---- copies: one thread issues those of a tile's blocks. (A copy from each of eight lanes at once is a loop over
+    // the lanes of some 100 clocks a copy: 830 of a tile's 1020 clocks, which was what bounded the kernel.) ----
     unsigned n = 0;  // tiles issued
     bool ok = true;
     while (ok && next()) {
       const int nblk = tree_units(seg.r.len, kBlock);
       const int32_t* table = a.block_table + static_cast<long long>(seg.r.seq) * a.max_blocks + seg.r.block0;
-      const uint8_t* pool = ((lane & 1) ? a.v_pool : a.k_pool) + static_cast<long long>(seg.h) * (kBlock * D);
-      const int i = lane >> 1, u0 = seg.u0, u1 = seg.u1;
-      auto entry = [&](int t) -> int { return (i < UPB && t * UPB + i < nblk) ? table[t * UPB + i] : 0; };
-      int ahead = entry(u0);
+      const long long head = static_cast<long long>(seg.h) * (kBlock * D), stride = static_cast<long long>(a.kv_heads) * (kBlock * D);
+      const int u0 = seg.u0, u1 = seg.u1;
+      // table entries come 32 at a time, a load ahead
+      auto entries = [&](int j) -> int { return j + lane < nblk ? min(max(table[j + lane], 0), a.num_blocks - 1) : 0; };
+      int here32 = entries(u0 * UPB), next32 = entries(u0 * UPB + 32);
       for (int t = u0; t < u1; ++t, ++n) {
-        const int blk = ahead;
-        if (t + 1 < u1) ahead = entry(t + 1);
+        const int off = (t - u0) * UPB & 31;
+        if (off == 0 && t > u0) {
+          here32 = next32;
+          next32 = entries(t * UPB + 32);
+        }
+        int blk[UPB];
+#pragma unroll
+        for (int i = 0; i < UPB; ++i) blk[i] = __shfl_sync(0xffffffffu, here32, off + i);
         const int s = n % kStages;
         if (n >= kStages) ok = role_wait_warp(&sh.empty[s], (n / kStages - 1) & 1, dead, a.status);
         if (!ok) break;
-        const int here = min(UPB, nblk - t * UPB);
-        if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], here * 2 * kBlock * D);
-        __syncwarp();
-        if (i < here) {
-          const long long p = min(max(blk, 0), a.num_blocks - 1);
-          bulk_g2s(smem + s * S::STAGE + (lane & 1) * (kTile * D) + i * (kBlock * D),
-                   pool + p * a.kv_heads * (kBlock * D), kBlock * D, &sh.full[s]);
+        if (elect_one()) {
+          const int here = min(UPB, nblk - t * UPB);
+          mbar_arrive_expect_tx(&sh.full[s], here * 2 * kBlock * D);
+          uint8_t* to = smem + s * S::STAGE;
+#pragma unroll
+          for (int i = 0; i < UPB; ++i) {
+            if (i >= here) break;
+            const long long at = head + blk[i] * stride;
+            bulk_g2s(to + i * (kBlock * D), a.k_pool + at, kBlock * D, &sh.full[s]);
+            bulk_g2s(to + kTile * D + i * (kBlock * D), a.v_pool + at, kBlock * D, &sh.full[s]);
+          }
         }
+        __syncwarp();
       }
     }
     // no copy of this block is in flight when it ends, whichever role gave up
