@@ -4,15 +4,15 @@
 //
 // A cluster of thread blocks takes one request; its rows are cut into parts, and
 // block r of C takes parts r, r + C, ... A part streams through shared memory in
-// chunks of 32 KB, the next ones' copies in flight. Rows may start on any
+// chunks of 16 KB, the next ones' copies in flight. Rows may start on any
 // boundary of their type: copies are of aligned 16 bytes, and a thread puts its
 // 8 or 4 elements together from two of them, so that a row's sum does not depend
 // on where the row lies.
 //   sum    every thread keeps a maximum and a sum of exp(x - maximum) of its own
 //          (fp32, rescaled when the maximum grows); they meet at the part's end
 //   best   within a row the order of the scores is that of the logits, so a part
-//          needs its k = n_out largest logits only. Of the 16 warps' chunk maxima
-//          (their j-th largest lane maxima, 16 j >= k) the smallest is a bound that at
+//          needs its k = n_out largest logits only. Of the 8 warps' maxima of the first
+//          chunk (their j-th largest lane maxima, 8 j >= k) the smallest is a bound that at
 //          least k elements reach and few do; the threads whose own maximum reaches it
 //          put those elements into a list of (value, token) keys. Chunks after the
 //          first have to exceed it. A list that runs full is cut down to its k
@@ -35,13 +35,12 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kVecs = 4;                       // 16-byte vectors a thread holds of a chunk
 constexpr int kChunk = kThreads * kVecs;       // vectors of a chunk
 constexpr int kStages = 3;                     // chunks in shared memory
 constexpr int kStageBytes = (kChunk + 1) * 16; // and one vector more, where elements reach into it
-constexpr int kCap = 1024;                     // keys of a part's list
-constexpr int kCut = 512;                      // cut down to k beyond this many
+constexpr int kCap = 512;                      // keys of a part's list
 constexpr int kMaxParts = 128;                 // parts of a request: four heads a lane
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLog2eLow = 1.925963033500e-8f;  // log2(e) - kLog2e
@@ -64,11 +63,17 @@ __device__ __forceinline__ int key_token(unsigned long long key) { return static
 // NaN counts as -inf, +inf as the largest float; -0 becomes +0.
 __device__ __forceinline__ float clean(float x) { return fminf(fmaxf(x, -INFINITY), FLT_MAX) + 0.0f; }
 
+// A vector of 16 bytes as floats, its largest element (NaN passed over), and -inf in every place.
 template <int TYPE>
 struct Logits;
 template <>
 struct Logits<0> {  // fp16
   static constexpr int SIZE = 2;
+  static constexpr uint32_t LOW = 0xfc00fc00u;
+  __device__ static __forceinline__ float largest(const uint4& v) {
+    const __half2 m = __hmax2(__hmax2(bits_h2(v.x), bits_h2(v.y)), __hmax2(bits_h2(v.z), bits_h2(v.w)));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
   __device__ static __forceinline__ float at(const void* p, long long i) { return __half2float(static_cast<const __half*>(p)[i]); }
   __device__ static __forceinline__ void unpack(const uint4& v, float2 (&x)[4]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -79,6 +84,10 @@ struct Logits<0> {  // fp16
 template <>
 struct Logits<1> {  // fp32
   static constexpr int SIZE = 4;
+  static constexpr uint32_t LOW = 0xff800000u;
+  __device__ static __forceinline__ float largest(const uint4& v) {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
   __device__ static __forceinline__ float at(const void* p, long long i) { return static_cast<const float*>(p)[i]; }
   __device__ static __forceinline__ void unpack(const uint4& v, float2 (&x)[2]) {
     x[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
@@ -88,6 +97,12 @@ struct Logits<1> {  // fp32
 template <>
 struct Logits<2> {  // bf16
   static constexpr int SIZE = 2;
+  static constexpr uint32_t LOW = 0xff80ff80u;
+  __device__ static __forceinline__ float largest(const uint4& v) {
+    auto pair = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+    const __nv_bfloat162 m = __hmax2(__hmax2(pair(v.x), pair(v.y)), __hmax2(pair(v.z), pair(v.w)));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
   __device__ static __forceinline__ float at(const void* p, long long i) {
     return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16);
   }
@@ -114,7 +129,7 @@ struct SelectShared {
   uint32_t bound[kWarps];
   float warp_max[kWarps];
   double warp_sum[kWarps];
-  int count, hits;
+  int added[3], hits;  // keys that chunk it has added: [it % 3]
 };
 
 // exp(x - m) for x <= m: d = x - m rounds relative to d alone, and log2(e) in two parts keeps the product's
@@ -124,22 +139,24 @@ __device__ __forceinline__ float exp_below(float x, float m) {
   return fast_exp2(fmaf(d, kLog2eLow, d * kLog2e));
 }
 
-// The k largest keys of sh.list[0, n) to out[0, k), largest first (kNone behind the n-th). All threads, synchronised
-// before and after.
+// The k largest keys of list[0, n) to out[0, k), largest first (kNone behind the n-th): eight threads count those above a
+// key. All threads, synchronised before and after.
 __device__ __forceinline__ void rank_list(const unsigned long long* list, int n, int k, unsigned long long* out) {
-  for (int i = threadIdx.x; i < k; i += kThreads)
-    if (i >= n) out[i] = kNone;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const unsigned long long key = list[i];
+  for (int i = n + threadIdx.x; i < k; i += kThreads) out[i] = kNone;
+  for (int i0 = 0; i0 < n; i0 += kThreads / 8) {
+    const int i = i0 + threadIdx.x / 8;
+    const unsigned long long key = i < n ? list[i] : kNone;
     int larger = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) larger += list[j] > key;
-    if (larger < k) out[larger] = key;
+    for (int j = threadIdx.x % 8; j < n; j += 8) larger += list[j] > key;
+    larger += __shfl_xor_sync(0xffffffffu, larger, 1);
+    larger += __shfl_xor_sync(0xffffffffu, larger, 2);
+    larger += __shfl_xor_sync(0xffffffffu, larger, 4);
+    if (threadIdx.x % 8 == 0 && i < n && larger < k) out[larger] = key;
   }
 }
 
 template <int TYPE>
-__global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSelectArgs a, int splits) {
+__global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSelectArgs a, int splits) {
   using L = Logits<TYPE>;
   constexpr int E = 16 / L::SIZE;  // elements of a vector
   extern __shared__ __align__(16) uint8_t dyn[];
@@ -169,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSele
     const int nv = (a.vocab + E - 1) / E;
     const int v0 = static_cast<int>(static_cast<long long>(nv) * split / splits);
     const int v1 = static_cast<int>(static_cast<long long>(nv) * (split + 1) / splits);
-    if (tid == 0) sh.count = 0;
+    if (tid < 3) sh.added[tid] = 0;
 
     auto copy = [&](uint8_t* stage, int c, int i) {  // aligned vector c + i; what lies outside the row becomes -inf
       const long long e0 = static_cast<long long>(c + i) * E - lead;
@@ -198,10 +215,15 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSele
       const int c = v0 + it * kChunk;
       if (c < v1) {
         uint8_t* stage = ring + it % kStages * kStageBytes;
+        if (c * static_cast<long long>(E) >= lead && c + kChunk < reach &&
+            (static_cast<long long>(c) + kChunk + 1) * E - lead <= a.vocab) {  // all within the row
 #pragma unroll
-        for (int u = 0; u < kVecs; ++u)
-          if (c + u * kThreads + tid < reach) copy(stage, c, u * kThreads + tid);
-        if (tid == 0 && lead > 0 && c + kChunk < reach) copy(stage, c, kChunk);
+          for (int u = 0; u < kVecs; ++u)
+            cp_async16(reinterpret_cast<uint4*>(stage) + u * kThreads + tid, vecs + c + u * kThreads + tid);
+          if (tid == 0) cp_async16(reinterpret_cast<uint4*>(stage) + kChunk, vecs + c + kChunk);
+        } else {
+          for (int i = tid; i <= kChunk && c + i < reach; i += kThreads) copy(stage, c, i);
+        }
       }
       cp_async_commit();
     };
@@ -218,132 +240,84 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSele
 
     float m = -INFINITY, s = 0.0f;  // of this thread
     float bound = -INFINITY;        // at least k elements so far reach it (-inf: not yet)
-    __syncthreads();  // the part before is done with the ring
-#pragma unroll
-    for (int it = 0; it < kStages - 1; ++it) issue(it);
-    for (int it = 0, c = v0; c < v1; ++it, c += kChunk) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-      __syncthreads();  // this chunk has landed, the one before has been read
-      issue(it + kStages - 1);
-      uint4 v[kVecs];
-      const uint4* here = reinterpret_cast<const uint4*>(ring + it % kStages * kStageBytes) + tid;
-      if (lead == 0) {
-#pragma unroll
-        for (int u = 0; u < kVecs; ++u) v[u] = here[u * kThreads];
-      } else {
-#pragma unroll
-        for (int u = 0; u < kVecs; ++u) v[u] = join(here[u * kThreads], here[u * kThreads + 1]);
-      }
-      const int held = min(kVecs, (v1 - c - tid + kThreads - 1) / kThreads);  // vectors of this thread (may be below 1)
-      // f(value, token) of every element
-      auto each = [&](auto f) {
-#pragma unroll
-        for (int u = 0; u < kVecs; ++u) {
-          if (u >= held) continue;
-          float2 x[E / 2];
-          L::unpack(v[u], x);
-#pragma unroll
-          for (int e = 0; e < E / 2; ++e) {
-            f(clean(x[e].x), (c + u * kThreads + tid) * E + 2 * e);
-            f(clean(x[e].y), (c + u * kThreads + tid) * E + 2 * e + 1);
-          }
-        }
-      };
-      float top = -INFINITY;  // (fmaxf passes over NaN)
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u) {
-        if (u >= held) continue;
-        float2 x[E / 2];
-        L::unpack(v[u], x);
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) top = fmaxf(top, fmaxf(x[e].x, x[e].y));
-      }
-      const bool infinite = top == INFINITY;
-      top = clean(top);
-      if (top > m) {
-        s = m == -INFINITY ? 0.0f : s * exp_below(m, top);
-        m = top;
-      }
-      if (m > -INFINITY) {
-        // (a chunk's terms first: fewer roundings at the sum's size)
-        if (infinite) {
-          float add = 0.0f;
-          each([&](float x, int) { add += exp_below(x, m); });
-          s += add;
-        } else {
-          float2 add = make_float2(0.0f, 0.0f);
-          const float2 m2 = make_float2(-m, -m), high = make_float2(kLog2e, kLog2e), low = make_float2(kLog2eLow, kLog2eLow);
-#pragma unroll
-          for (int u = 0; u < kVecs; ++u) {
-            if (u >= held) continue;
-            float2 x[E / 2];
-            L::unpack(v[u], x);
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) {
-              const float2 d = __fadd2_rn(x[e], m2);
-              float2 p = __ffma2_rn(d, low, __fmul2_rn(d, high));
-              // (NaN and -inf: below every normal number)
-              p.x = fast_exp2(fmaxf(p.x, -200.0f));
-              p.y = fast_exp2(fmaxf(p.y, -200.0f));
-              add = __fadd2_rn(add, p);
-            }
-          }
-          s += add.x + add.y;
-        }
-      }
+    int held = 0;                   // keys in the list before the chunk (at most 2 k + 32)
+    float top = -INFINITY;          // of this thread's elements of the chunk
 
-      // the bound of this chunk: each warp's j-th largest lane maximum, the smallest of the warps' ones
-      const bool first = c == v0;
-      auto chunk_bound = [&]() {
-        uint32_t code = float_code(top), best = 0u;
-        const int times = (k + kWarps - 1) / kWarps;
-        for (int t = 0; t < times; ++t) {
-          best = __reduce_max_sync(0xffffffffu, code);
-          const uint32_t who = __ballot_sync(0xffffffffu, code == best);
-          if (lane == __ffs(who) - 1) code = 0u;
-        }
-        if (lane == 0) sh.bound[warp] = best;
-        __syncthreads();
-        uint32_t low = sh.bound[lane % kWarps];
-        return code_float(max(__reduce_min_sync(0xffffffffu, low), float_code(-INFINITY)));
-      };
-      if (first) bound = chunk_bound();
-      // (in later chunks tokens are higher, so an equal value does not displace one in the list)
-      auto wanted = [&](float x, float limit, bool equal) { return x > limit || (equal && x == limit && x > -INFINITY); };
-      auto collect = [&](float limit, bool equal) {
-        if (!wanted(top, limit, equal)) return;
-        each([&](float x, int token) {
-          if (wanted(x, limit, equal)) {
-            const int i = atomicAdd(&sh.count, 1);
-            if (i < kCap) sh.list[i] = make_key(x, token);
+    // Vector u of chunk it; behind the part's last one: -inf.
+    auto vec = [&](int it, int u) -> uint4 {
+      if (v0 + it * kChunk + u * kThreads + tid >= v1) return make_uint4(L::LOW, L::LOW, L::LOW, L::LOW);
+      const uint4* here = reinterpret_cast<const uint4*>(ring + it % kStages * kStageBytes) + u * kThreads + tid;
+      return lead == 0 ? here[0] : join(here[0], here[1]);
+    };
+    // f(value, token) of every element of chunk it: the less frequent passes, a vector at a time, in little code
+    auto each = [&](int it, auto f) {
+#pragma unroll 1
+      for (int u = 0; u < kVecs; ++u) {
+        float2 x[E / 2];
+        L::unpack(vec(it, u), x);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          f(clean(e % 2 ? x[e / 2].y : x[e / 2].x), (v0 + it * kChunk + u * kThreads + tid) * E + e);
+      }
+    };
+    // A bound of a chunk: each warp's j-th largest lane maximum, the smallest of the warps' ones.
+    auto chunk_bound = [&]() {
+      uint32_t code = float_code(top), best = 0u;
+      const int times = (k + kWarps - 1) / kWarps;
+      for (int t = 0; t < times; ++t) {
+        best = __reduce_max_sync(0xffffffffu, code);
+        const uint32_t who = __ballot_sync(0xffffffffu, code == best);
+        if (lane == __ffs(who) - 1) code = 0u;
+      }
+      if (lane == 0) sh.bound[warp] = best;
+      __syncthreads();
+      const uint32_t low = sh.bound[lane % kWarps];
+      return code_float(max(__reduce_min_sync(0xffffffffu, low), float_code(-INFINITY)));
+    };
+    // (in chunks after the first tokens are higher, so an equal value does not displace one in the list)
+    auto wanted = [&](float x, float limit, bool equal) { return x > limit || (equal && x == limit && x > -INFINITY); };
+    auto collect = [&](int it, float limit, bool equal) {
+      if (!wanted(top, limit, equal)) return;
+#pragma unroll 1
+      for (int u = 0; u < kVecs; ++u) {
+        const uint4 w = vec(it, u);
+        if (!wanted(L::largest(w), limit, equal)) continue;
+        float2 x[E / 2];
+        L::unpack(w, x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float y = e % 2 ? x[e / 2].y : x[e / 2].x;
+          if (wanted(y, limit, equal)) {
+            const int i = held + atomicAdd(&sh.added[it % 3], 1);
+            if (i < kCap) sh.list[i] = make_key(clean(y), (v0 + it * kChunk + u * kThreads + tid) * E + e);
           }
-        });
-      };
-      __syncthreads();
-      const int had = sh.count;  // (at most kCut)
-      __syncthreads();
-      collect(bound, first);
-      __syncthreads();
-      int n = sh.count;
-      if (n > kCap && !first) {  // a bound of this chunk's own may let fewer through
+        }
+      }
+    };
+    // What chunk it added, once all threads have collected: the list is cut down where it has grown.
+    auto settle = [&](int it, bool last) {
+      const int had = held;
+      held += sh.added[it % 3];
+      if (tid == 0) sh.added[(it + 2) % 3] = 0;  // (of chunk it - 1, which all have read)
+      if (held > kCap && it > 0) {  // a bound of this chunk's own may let fewer through
         const float tight = chunk_bound();
         if (tight > bound) {
+          if (tid == 0) sh.added[it % 3] = 0;
           __syncthreads();
-          if (tid == 0) sh.count = had;
+          held = had;
+          collect(it, tight, true);
           __syncthreads();
-          collect(tight, true);
-          __syncthreads();
-          n = sh.count;
+          held += sh.added[it % 3];
         }
       }
-      if (n > kCap) {
+      if (held > kCap) {
         // the k-th largest key of what was had and this chunk, bit by bit
         unsigned long long kth = 0ull;
         for (int bit = 63; bit >= 0; --bit) {
           const unsigned long long trial = kth | (1ull << bit);
           int reach = 0;
           if (make_key(top, 0) >= trial)
-            each([&](float x, int token) { reach += x > -INFINITY && make_key(x, token) >= trial; });
+            each(it, [&](float x, int token) { reach += x > -INFINITY && make_key(x, token) >= trial; });
           for (int i = tid; i < had; i += kThreads) reach += sh.list[i] >= trial;
           if (tid == 0) sh.hits = 0;
           __syncthreads();
@@ -353,28 +327,86 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSele
           if (sh.hits >= k) kth = trial;
           __syncthreads();
         }
-        unsigned long long keep = kNone;
-        if (tid < had) keep = sh.list[tid];
-        if (tid == 0) sh.count = 0;
+        constexpr int kHad = (2 * kBeamMaxOut + 32 + kThreads - 1) / kThreads;
+        unsigned long long keep[kHad];
+#pragma unroll
+        for (int q = 0; q < kHad; ++q) keep[q] = tid + q * kThreads < had ? sh.list[tid + q * kThreads] : kNone;
+        if (tid == 0) sh.hits = 0;
         __syncthreads();
         auto put = [&](unsigned long long key) {
-          if (key >= kth) sh.list[atomicAdd(&sh.count, 1)] = key;  // (k keys, they are distinct)
+          if (key >= kth) sh.list[atomicAdd(&sh.hits, 1)] = key;  // (k keys, they are distinct)
         };
-        if (keep != kNone) put(keep);
-        each([&](float x, int token) {
+#pragma unroll
+        for (int q = 0; q < kHad; ++q)
+          if (keep[q] != kNone) put(keep[q]);
+        each(it, [&](float x, int token) {
           if (x > -INFINITY) put(make_key(x, token));
         });
         __syncthreads();
+        held = k;
         bound = code_float(static_cast<uint32_t>(kth >> 32));
-      } else if (n > kCut) {
-        rank_list(sh.list, n, k, out);
+      } else if (!last && held > (it == 0 ? k : 2 * k + 32)) {
+        // Few elements of later chunks exceed the k-th so far, and a warp without one has nothing to collect.
+        rank_list(sh.list, held, k, out);
         __syncthreads();
         for (int i = tid; i < k; i += kThreads) sh.list[i] = out[i];
-        if (tid == 0) sh.count = min(n, k);
-        bound = code_float(static_cast<uint32_t>(out[k - 1] >> 32));  // (n > kCut >= k)
-        __syncthreads();
+        held = k;
+        bound = code_float(static_cast<uint32_t>(out[k - 1] >> 32));
+        // (keys that the next chunk adds go behind these)
       }
+    };
+
+    __syncthreads();  // the part before is done with the ring
+#pragma unroll
+    for (int it = 0; it < kStages - 1; ++it) issue(it);
+    int it = 0;
+    for (int c = v0; c < v1; ++it, c += kChunk) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncthreads();  // this chunk has landed; what the one before has added is complete
+      if (it > 0) settle(it - 1, false);
+      issue(it + kStages - 1);  // (where the chunk before was; settle reads it again between barriers only)
+      uint4 v[kVecs];
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u) v[u] = vec(it, u);
+      top = L::largest(v[0]);
+#pragma unroll
+      for (int u = 1; u < kVecs; ++u) top = fmaxf(top, L::largest(v[u]));
+      const bool infinite = top == INFINITY;
+      top = clean(top);
+      if (top > m) {
+        s = m == -INFINITY ? 0.0f : s * exp_below(m, top);
+        m = top;
+      }
+      if (m > -INFINITY) {
+        // (a chunk's terms first: fewer roundings at the sum's size)
+        float2 add = make_float2(0.0f, 0.0f);
+        const float2 m2 = make_float2(-m, -m), high = make_float2(kLog2e, kLog2e), low = make_float2(kLog2eLow, kLog2eLow);
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) {
+          if (c + u * kThreads >= v1) break;
+          float2 x[E / 2];
+          L::unpack(v[u], x);
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) {
+            const float2 d = __fadd2_rn(x[e], m2);
+            float2 p = __ffma2_rn(d, low, __fmul2_rn(d, high));
+            p.x = fast_exp2(p.x);
+            p.y = fast_exp2(p.y);
+            add = __fadd2_rn(add, p);
+          }
+        }
+        float sum = add.x + add.y;
+        if (infinite || sum != sum) {  // infinities and NaN, as their values count
+          sum = 0.0f;
+          each(it, [&](float x, int) { sum += exp_below(x, m); });
+        }
+        s += sum;
+      }
+      if (it == 0) bound = chunk_bound();
+      collect(it, bound, it == 0);
     }
+    __syncthreads();
+    if (it > 0) settle(it - 1, true);  // (a part of a short row may have no vector)
 
     // the part's maximum and sum, its sorted list
     const float wm = code_float(__reduce_max_sync(0xffffffffu, float_code(m)));
@@ -386,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSele
       sh.warp_max[warp] = wm;
       sh.warp_sum[warp] = ws;
     }
-    const int n = min(sh.count, kCap);
+    const int n = held;
     rank_list(sh.list, n, k, out);
     __syncthreads();
     if (warp == 0) {
@@ -531,6 +563,7 @@ constexpr int shared_bytes(int mine, int parts, int k) {
 }
 // Of the widest request with the most candidates in one block, rows whole.
 constexpr int kMostShared = shared_bytes(kBeamMaxWidth, kBeamMaxWidth, kBeamMaxOut);
+static_assert(2 * kBeamMaxOut + 32 <= kCap, "a list that is not cut down leaves room");
 static_assert(kMostShared + sizeof(SelectShared) + 2048 <= 232448, "shared memory of a thread block");
 
 struct SelectPlan {
@@ -538,13 +571,13 @@ struct SelectPlan {
 };
 
 // Blocks of a cluster and parts of a row. Small batches take large clusters (up to 16 blocks, one request is one
-// cluster), so that about two blocks an SM work; a row is cut so that the parts spread evenly over them, where a part
+// cluster), so that up to four blocks an SM work; a row is cut so that the parts spread evenly over them, where a part
 // costs what `fixed` bytes of logits do beside its own.
 SelectPlan plan_select(const BeamSelectArgs& a, int size, int most_ranks) {
   SelectPlan best{1, 1, 0};
-  const long long fixed = 32768;
+  const long long fixed = 16384;
   int ranks = 1;
-  while (ranks < most_ranks && static_cast<long long>(a.groups) * ranks * 2 <= 2ll * device_sm_count()) ranks *= 2;
+  while (ranks < most_ranks && static_cast<long long>(a.groups) * ranks * 2 <= 4ll * device_sm_count()) ranks *= 2;
   long long best_cost = LLONG_MAX;
   for (int splits = 1; splits <= 32 && a.width * splits <= kMaxParts; ++splits) {
     const long long rounds = (a.width * splits + ranks - 1) / ranks;
