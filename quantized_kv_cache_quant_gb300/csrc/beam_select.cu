@@ -3,23 +3,27 @@
 // logits and one launch.
 //
 // A cluster of thread blocks takes one request; its rows are cut into parts, and
-// block r of C takes parts r, r + C, ... A part streams through shared memory in
-// chunks of 16 KB, the next ones' copies in flight. Rows may start on any
-// boundary of their type: copies are of aligned 16 bytes, and a thread puts its
-// 8 or 4 elements together from two of them, so that a row's sum does not depend
-// on where the row lies.
+// block r of C takes parts r, r + C, ... The warps of a block go through a part on
+// their own, 2 KB at a time, the next 2 KB on their way. Rows may start on any
+// boundary of their type: loads are of aligned 16 bytes, and a thread puts its 8
+// or 4 elements together from two of them, so that a row's sum does not depend on
+// where the row lies.
 //   sum    every thread keeps a maximum and a sum of exp(x - maximum) of its own
 //          (fp32, rescaled when the maximum grows); they meet at the part's end
 //   best   within a row the order of the scores is that of the logits, so a part
-//          needs its k = n_out largest logits only. Of the 8 warps' maxima of the first
-//          chunk (their j-th largest lane maxima, 8 j >= k) the smallest is a bound that at
-//          least k elements reach and few do; the threads whose own maximum reaches it
-//          put those elements into a list of (value, token) keys. Chunks after the
-//          first have to exceed it. A list that runs full is cut down to its k
-//          largest, found bit by bit where even one chunk does not fit.
+//          needs its k = n_out largest logits only. The k-th largest of the threads'
+//          maxima is a bound that at least k elements reach, and only the threads whose
+//          maximum reaches it have such elements, k of them but for ties: their
+//          elements are read once more (k / 256 of the part, from L2), by a warp each.
+//          Every warp keeps a list of (value, token) keys, which is cut down to its k
+//          largest where it runs full; in the end the lists are ranked together.
 // Then the first block of the cluster has every part's maximum, sum and sorted
 // list (read through distributed shared memory), turns them into scores in fp64,
 // and one warp takes the largest head of all lists n_out times.
+//
+// (Lists that elements enter on the way cost more than the sums: one list a block,
+// with barriers between chunks of 32 KB in shared memory, 134 us for 512 rows of
+// 128000 bf16 logits, 67 with one barrier a chunk; a list a warp 184.)
 #include <cfloat>
 #include <climits>
 #include <cooperative_groups.h>
@@ -36,11 +40,8 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kVecs = 4;                       // 16-byte vectors a thread holds of a chunk
-constexpr int kChunk = kThreads * kVecs;       // vectors of a chunk
-constexpr int kStages = 3;                     // chunks in shared memory
-constexpr int kStageBytes = (kChunk + 1) * 16; // and one vector more, where elements reach into it
-constexpr int kCap = 512;                      // keys of a part's list
+constexpr int kVecs = 4;                       // 16-byte vectors a thread holds of a warp's 2 KB
+constexpr int kStep = 32 * kVecs;              // vectors of them
 constexpr int kMaxParts = 128;                 // parts of a request: four heads a lane
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLog2eLow = 1.925963033500e-8f;  // log2(e) - kLog2e
@@ -124,12 +125,18 @@ __host__ __device__ constexpr int list_bytes(int mine, int k) {
   return (mine * static_cast<int>(sizeof(PartSum) + k * sizeof(unsigned long long)) + 15) / 16 * 16;
 }
 
+// Keys of a warp's list: it is cut down to k before 32 more might not fit.
+__host__ __device__ constexpr int list_cap(int k) { return (2 * k + 64 + 31) / 32 * 32; }
+// Two lists a warp: cutting down writes the other one.
+__host__ __device__ constexpr int warp_list_bytes(int k) { return 2 * kWarps * list_cap(k) * static_cast<int>(sizeof(unsigned long long)); }
+
 struct SelectShared {
-  unsigned long long list[kCap];
-  uint32_t bound[kWarps];
   float warp_max[kWarps];
   double warp_sum[kWarps];
-  int added[3], hits;  // keys that chunk it has added: [it % 3]
+  uint32_t top[kThreads];  // codes of the threads' maxima
+  uint8_t rich[kThreads];  // threads whose maximum reaches the bound
+  uint32_t bound;          // code of a value that at least k elements of the part reach
+  int riches, count;       // such threads; keys in the common list
 };
 
 // exp(x - m) for x <= m: d = x - m rounds relative to d alone, and log2(e) in two parts keeps the product's
@@ -143,7 +150,7 @@ __device__ __forceinline__ float exp_below(float x, float m) {
 // key. All threads, synchronised before and after.
 __device__ __forceinline__ void rank_list(const unsigned long long* list, int n, int k, unsigned long long* out) {
   for (int i = n + threadIdx.x; i < k; i += kThreads) out[i] = kNone;
-  for (int i0 = 0; i0 < n; i0 += kThreads / 8) {
+  for (int i0 = 0; i0 + static_cast<int>(threadIdx.x & ~31u) / 8 < n; i0 += kThreads / 8) {
     const int i = i0 + threadIdx.x / 8;
     const unsigned long long key = i < n ? list[i] : kNone;
     int larger = 0;
@@ -155,8 +162,21 @@ __device__ __forceinline__ void rank_list(const unsigned long long* list, int n,
   }
 }
 
+// The k largest of a warp's n keys (k <= n), largest first, into the other list.
+__device__ __noinline__ void cut_list(const unsigned long long* from, int n, int k, unsigned long long* to) {
+  const int lane = threadIdx.x & 31;
+  for (int i = lane; i < n; i += 32) {
+    const unsigned long long key = from[i];
+    int larger = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) larger += from[j] > key;
+    if (larger < k) to[larger] = key;
+  }
+  __syncwarp();
+}
+
 template <int TYPE>
-__global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSelectArgs a, int splits) {
+__global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamSelectArgs a, int splits) {
   using L = Logits<TYPE>;
   constexpr int E = 16 / L::SIZE;  // elements of a vector
   extern __shared__ __align__(16) uint8_t dyn[];
@@ -165,11 +185,12 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
   const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
   const int group = blockIdx.x / ranks, k = a.n_out, parts = a.width * splits;
   const int mine = (parts + ranks - 1) / ranks;  // parts of a block at most
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // the ring, and after the last part the scores of all lists
-  uint8_t* const ring = dyn + list_bytes(mine, k);
-  PartSum* sums = reinterpret_cast<PartSum*>(dyn);                                          // [mine]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cap = list_cap(k);
+  // the parts' sums and lists; the warps' lists, and after the last part the scores of all lists
+  PartSum* sums = reinterpret_cast<PartSum*>(dyn);                                                  // [mine]
   unsigned long long* lists = reinterpret_cast<unsigned long long*>(dyn + mine * sizeof(PartSum));  // [mine][k]
+  uint8_t* const area = dyn + list_bytes(mine, k);
+  unsigned long long* const warp_lists = reinterpret_cast<unsigned long long*>(area);               // [2][kWarps][cap]
 
   for (int slot = 0, part = rank; part < parts; ++slot, part += ranks) {
     const int beam = part / splits, split = part % splits;
@@ -186,46 +207,24 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
     const int nv = (a.vocab + E - 1) / E;
     const int v0 = static_cast<int>(static_cast<long long>(nv) * split / splits);
     const int v1 = static_cast<int>(static_cast<long long>(nv) * (split + 1) / splits);
-    if (tid < 3) sh.added[tid] = 0;
+    if (tid == 0) sh.riches = sh.count = 0;
+    __syncthreads();  // (the part before is done with the lists too)
 
-    auto copy = [&](uint8_t* stage, int c, int i) {  // aligned vector c + i; what lies outside the row becomes -inf
-      const long long e0 = static_cast<long long>(c + i) * E - lead;
-      uint4* to = reinterpret_cast<uint4*>(stage) + i;
-      if (e0 >= 0 && e0 + E <= a.vocab) {
-        cp_async16(to, vecs + c + i);
-      } else {
-        uint32_t w[4];
+    // vector j of elements by single loads; what lies outside the row becomes -inf
+    auto edge = [&](int j) -> uint4 {
+      const long long e0 = static_cast<long long>(j) * E;
+      uint32_t w[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if constexpr (L::SIZE == 4) {
-            w[q] = e0 + q >= 0 && e0 + q < a.vocab ? reinterpret_cast<const uint32_t*>(base)[e0 + q] : 0xff800000u;
-          } else {
-            constexpr uint32_t kLow = TYPE == 0 ? 0xfc00u : 0xff80u;
-            const uint16_t* p = reinterpret_cast<const uint16_t*>(base);
-            const long long x = e0 + 2 * q;
-            w[q] = x >= 0 && x < a.vocab ? p[x] : kLow;
-            w[q] |= (x + 1 >= 0 && x + 1 < a.vocab ? p[x + 1] : kLow) << 16;
-          }
-        }
-        *to = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    };
-    const int reach = v1 + (lead > 0);  // aligned vectors up to here
-    auto issue = [&](int it) {
-      const int c = v0 + it * kChunk;
-      if (c < v1) {
-        uint8_t* stage = ring + it % kStages * kStageBytes;
-        if (c * static_cast<long long>(E) >= lead && c + kChunk < reach &&
-            (static_cast<long long>(c) + kChunk + 1) * E - lead <= a.vocab) {  // all within the row
-#pragma unroll
-          for (int u = 0; u < kVecs; ++u)
-            cp_async16(reinterpret_cast<uint4*>(stage) + u * kThreads + tid, vecs + c + u * kThreads + tid);
-          if (tid == 0) cp_async16(reinterpret_cast<uint4*>(stage) + kChunk, vecs + c + kChunk);
+      for (int q = 0; q < 4; ++q) {
+        if constexpr (L::SIZE == 4) {
+          w[q] = e0 + q < a.vocab ? reinterpret_cast<const uint32_t*>(base)[e0 + q] : L::LOW;
         } else {
-          for (int i = tid; i <= kChunk && c + i < reach; i += kThreads) copy(stage, c, i);
+          const uint16_t* p = reinterpret_cast<const uint16_t*>(base);
+          w[q] = e0 + 2 * q < a.vocab ? p[e0 + 2 * q] : L::LOW & 0xffffu;
+          w[q] |= (e0 + 2 * q + 1 < a.vocab ? p[e0 + 2 * q + 1] : L::LOW & 0xffffu) << 16;
         }
       }
-      cp_async_commit();
+      return make_uint4(w[0], w[1], w[2], w[3]);
     };
     // 16 bytes of elements from two aligned vectors
     const int lead_words = lead * L::SIZE / 4, lead_bits = lead * L::SIZE % 4 * 8;
@@ -237,140 +236,48 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
       return make_uint4(__funnelshift_r(w[0], w[1], lead_bits), __funnelshift_r(w[1], w[2], lead_bits),
                         __funnelshift_r(w[2], w[3], lead_bits), __funnelshift_r(w[3], w[4], lead_bits));
     };
-
-    float m = -INFINITY, s = 0.0f;  // of this thread
-    float bound = -INFINITY;        // at least k elements so far reach it (-inf: not yet)
-    int held = 0;                   // keys in the list before the chunk (at most 2 k + 32)
-    float top = -INFINITY;          // of this thread's elements of the chunk
-
-    // Vector u of chunk it; behind the part's last one: -inf.
-    auto vec = [&](int it, int u) -> uint4 {
-      if (v0 + it * kChunk + u * kThreads + tid >= v1) return make_uint4(L::LOW, L::LOW, L::LOW, L::LOW);
-      const uint4* here = reinterpret_cast<const uint4*>(ring + it % kStages * kStageBytes) + u * kThreads + tid;
-      return lead == 0 ? here[0] : join(here[0], here[1]);
+    // vector j of elements (behind the part's last: -inf)
+    auto vec = [&](int j) -> uint4 {
+      if (j >= v1) return make_uint4(L::LOW, L::LOW, L::LOW, L::LOW);
+      if (lead == 0 ? (j + 1) * static_cast<long long>(E) > a.vocab : j == 0 || (j + 2) * static_cast<long long>(E) - lead > a.vocab)
+        return edge(j);
+      if (lead == 0) return __ldg(vecs + j);
+      const uint4 x = __ldg(vecs + j), y = __ldg(vecs + j + 1);
+      return join(x, y);
     };
-    // f(value, token) of every element of chunk it: the less frequent passes, a vector at a time, in little code
-    auto each = [&](int it, auto f) {
-#pragma unroll 1
-      for (int u = 0; u < kVecs; ++u) {
-        float2 x[E / 2];
-        L::unpack(vec(it, u), x);
+    // a step's vectors c + 32 u + lane
+    auto load = [&](int c, uint4 (&v)[kVecs]) {
+      // all within the row, the vector behind too
+      const bool inner = c + kStep <= v1 && (lead == 0 ? (c + kStep) * static_cast<long long>(E) <= a.vocab
+                                                       : c > 0 && (c + kStep + 1) * static_cast<long long>(E) - lead <= a.vocab);
+      if (inner && lead == 0) {
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          f(clean(e % 2 ? x[e / 2].y : x[e / 2].x), (v0 + it * kChunk + u * kThreads + tid) * E + e);
-      }
-    };
-    // A bound of a chunk: each warp's j-th largest lane maximum, the smallest of the warps' ones.
-    auto chunk_bound = [&]() {
-      uint32_t code = float_code(top), best = 0u;
-      const int times = (k + kWarps - 1) / kWarps;
-      for (int t = 0; t < times; ++t) {
-        best = __reduce_max_sync(0xffffffffu, code);
-        const uint32_t who = __ballot_sync(0xffffffffu, code == best);
-        if (lane == __ffs(who) - 1) code = 0u;
-      }
-      if (lane == 0) sh.bound[warp] = best;
-      __syncthreads();
-      const uint32_t low = sh.bound[lane % kWarps];
-      return code_float(max(__reduce_min_sync(0xffffffffu, low), float_code(-INFINITY)));
-    };
-    // (in chunks after the first tokens are higher, so an equal value does not displace one in the list)
-    auto wanted = [&](float x, float limit, bool equal) { return x > limit || (equal && x == limit && x > -INFINITY); };
-    auto collect = [&](int it, float limit, bool equal) {
-      if (!wanted(top, limit, equal)) return;
-#pragma unroll 1
-      for (int u = 0; u < kVecs; ++u) {
-        const uint4 w = vec(it, u);
-        if (!wanted(L::largest(w), limit, equal)) continue;
-        float2 x[E / 2];
-        L::unpack(w, x);
+        for (int u = 0; u < kVecs; ++u) v[u] = __ldg(vecs + c + 32 * u + lane);
+      } else if (inner) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float y = e % 2 ? x[e / 2].y : x[e / 2].x;
-          if (wanted(y, limit, equal)) {
-            const int i = held + atomicAdd(&sh.added[it % 3], 1);
-            if (i < kCap) sh.list[i] = make_key(clean(y), (v0 + it * kChunk + u * kThreads + tid) * E + e);
-          }
+        for (int u = 0; u < kVecs; ++u) {
+          const uint4 x = __ldg(vecs + c + 32 * u + lane), y = __ldg(vecs + c + 32 * u + lane + 1);
+          v[u] = join(x, y);
         }
-      }
-    };
-    // What chunk it added, once all threads have collected: the list is cut down where it has grown.
-    auto settle = [&](int it, bool last) {
-      const int had = held;
-      held += sh.added[it % 3];
-      if (tid == 0) sh.added[(it + 2) % 3] = 0;  // (of chunk it - 1, which all have read)
-      if (held > kCap && it > 0) {  // a bound of this chunk's own may let fewer through
-        const float tight = chunk_bound();
-        if (tight > bound) {
-          if (tid == 0) sh.added[it % 3] = 0;
-          __syncthreads();
-          held = had;
-          collect(it, tight, true);
-          __syncthreads();
-          held += sh.added[it % 3];
-        }
-      }
-      if (held > kCap) {
-        // the k-th largest key of what was had and this chunk, bit by bit
-        unsigned long long kth = 0ull;
-        for (int bit = 63; bit >= 0; --bit) {
-          const unsigned long long trial = kth | (1ull << bit);
-          int reach = 0;
-          if (make_key(top, 0) >= trial)
-            each(it, [&](float x, int token) { reach += x > -INFINITY && make_key(x, token) >= trial; });
-          for (int i = tid; i < had; i += kThreads) reach += sh.list[i] >= trial;
-          if (tid == 0) sh.hits = 0;
-          __syncthreads();
-          reach = __reduce_add_sync(0xffffffffu, reach);
-          if (lane == 0) atomicAdd(&sh.hits, reach);
-          __syncthreads();
-          if (sh.hits >= k) kth = trial;
-          __syncthreads();
-        }
-        constexpr int kHad = (2 * kBeamMaxOut + 32 + kThreads - 1) / kThreads;
-        unsigned long long keep[kHad];
+      } else {
 #pragma unroll
-        for (int q = 0; q < kHad; ++q) keep[q] = tid + q * kThreads < had ? sh.list[tid + q * kThreads] : kNone;
-        if (tid == 0) sh.hits = 0;
-        __syncthreads();
-        auto put = [&](unsigned long long key) {
-          if (key >= kth) sh.list[atomicAdd(&sh.hits, 1)] = key;  // (k keys, they are distinct)
-        };
-#pragma unroll
-        for (int q = 0; q < kHad; ++q)
-          if (keep[q] != kNone) put(keep[q]);
-        each(it, [&](float x, int token) {
-          if (x > -INFINITY) put(make_key(x, token));
-        });
-        __syncthreads();
-        held = k;
-        bound = code_float(static_cast<uint32_t>(kth >> 32));
-      } else if (!last && held > (it == 0 ? k : 2 * k + 32)) {
-        // Few elements of later chunks exceed the k-th so far, and a warp without one has nothing to collect.
-        rank_list(sh.list, held, k, out);
-        __syncthreads();
-        for (int i = tid; i < k; i += kThreads) sh.list[i] = out[i];
-        held = k;
-        bound = code_float(static_cast<uint32_t>(out[k - 1] >> 32));
-        // (keys that the next chunk adds go behind these)
+        for (int u = 0; u < kVecs; ++u) v[u] = vec(c + 32 * u + lane);
       }
     };
 
-    __syncthreads();  // the part before is done with the ring
-#pragma unroll
-    for (int it = 0; it < kStages - 1; ++it) issue(it);
-    int it = 0;
-    for (int c = v0; c < v1; ++it, c += kChunk) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-      __syncthreads();  // this chunk has landed; what the one before has added is complete
-      if (it > 0) settle(it - 1, false);
-      issue(it + kStages - 1);  // (where the chunk before was; settle reads it again between barriers only)
+    float m = -INFINITY, s = 0.0f;  // of this thread
+    uint4 next[kVecs];
+    int c = v0 + warp * kStep;
+    if (c < v1) load(c, next);
+    for (; c < v1; c += kWarps * kStep) {
       uint4 v[kVecs];
 #pragma unroll
-      for (int u = 0; u < kVecs; ++u) v[u] = vec(it, u);
-      top = L::largest(v[0]);
+      for (int u = 0; u < kVecs; ++u) v[u] = next[u];
+      if (c + kWarps * kStep < v1) load(c + kWarps * kStep, next);
+      float tops[kVecs];
 #pragma unroll
-      for (int u = 1; u < kVecs; ++u) top = fmaxf(top, L::largest(v[u]));
+      for (int u = 0; u < kVecs; ++u) tops[u] = L::largest(v[u]);
+      float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
       const bool infinite = top == INFINITY;
       top = clean(top);
       if (top > m) {
@@ -378,12 +285,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
         m = top;
       }
       if (m > -INFINITY) {
-        // (a chunk's terms first: fewer roundings at the sum's size)
+        // (a step's terms first: fewer roundings at the sum's size)
         float2 add = make_float2(0.0f, 0.0f);
         const float2 m2 = make_float2(-m, -m), high = make_float2(kLog2e, kLog2e), low = make_float2(kLog2eLow, kLog2eLow);
 #pragma unroll
         for (int u = 0; u < kVecs; ++u) {
-          if (c + u * kThreads >= v1) break;
           float2 x[E / 2];
           L::unpack(v[u], x);
 #pragma unroll
@@ -398,28 +304,103 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
         float sum = add.x + add.y;
         if (infinite || sum != sum) {  // infinities and NaN, as their values count
           sum = 0.0f;
-          each(it, [&](float x, int) { sum += exp_below(x, m); });
+#pragma unroll
+          for (int u = 0; u < kVecs; ++u) {
+            float2 x[E / 2];
+            L::unpack(v[u], x);
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) sum += exp_below(clean(x[e].x), m) + exp_below(clean(x[e].y), m);
+          }
         }
         s += sum;
       }
-      if (it == 0) bound = chunk_bound();
-      collect(it, bound, it == 0);
+    }
+
+    // the k-th largest of the threads' maxima, to 16 bits and rounded down
+    sh.top[tid] = float_code(m);
+    __syncthreads();
+    if (warp == 0) {
+      uint32_t code[kWarps], bound = 0u;
+#pragma unroll
+      for (int q = 0; q < kWarps; ++q) code[q] = sh.top[lane + 32 * q];
+#pragma unroll 1
+      for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1) {
+        int reach = 0;
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q) reach += code[q] >= (bound | bit);
+        if (__reduce_add_sync(0xffffffffu, reach) >= k) bound |= bit;
+      }
+      if (lane == 0) sh.bound = bound;
     }
     __syncthreads();
-    if (it > 0) settle(it - 1, true);  // (a part of a short row may have no vector)
+    const uint32_t bound = sh.bound;
+    if (m > -INFINITY && float_code(m) >= bound) sh.rich[atomicAdd(&sh.riches, 1)] = static_cast<uint8_t>(tid);
+    __syncthreads();
+
+    // their elements once more, a warp for a thread's
+    unsigned long long* list = warp_lists + warp * cap;
+    unsigned long long* other = warp_lists + (kWarps + warp) * cap;
+    unsigned long long own = kNone;  // the warp's k-th largest key (kNone: fewer than k so far)
+    int n = 0;                       // keys in the warp's list
+    auto cut = [&]() {
+      __syncwarp();
+      cut_list(list, n, k, other);
+      unsigned long long* const x = list;
+      list = other;
+      other = x;
+      n = k;
+      own = list[k - 1];
+    };
+    const int steps = (v1 - v0 + kWarps * kStep - 1) / (kWarps * kStep);
+    for (int r = warp; r < sh.riches; r += kWarps) {
+      const int thread = sh.rich[r], first = v0 + thread / 32 * kStep + thread % 32;
+      for (int q0 = 0; q0 < steps * kVecs; q0 += 32) {
+        const int q = q0 + lane, j = first + q / kVecs * (kWarps * kStep) + q % kVecs * 32;
+        const uint4 w = q < steps * kVecs ? vec(j) : make_uint4(L::LOW, L::LOW, L::LOW, L::LOW);
+        const float most = clean(L::largest(w));
+        if (!__any_sync(0xffffffffu, most > -INFINITY && float_code(most) >= bound)) continue;
+        float2 x[E / 2];
+        L::unpack(w, x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float y = clean(e % 2 ? x[e / 2].y : x[e / 2].x);
+          const unsigned long long key = make_key(y, j * E + e);
+          const bool wanted = y > -INFINITY && static_cast<uint32_t>(key >> 32) >= bound && key > own;
+          const uint32_t who = __ballot_sync(0xffffffffu, wanted);
+          if (who == 0) continue;
+          if (wanted) list[n + __popc(who & ((1u << lane) - 1u))] = key;
+          n += __popc(who);
+          if (n > cap - 32) cut();
+        }
+      }
+    }
+    if (n > k) cut();
+    if (lane == 0 && own != kNone) atomicMax(&sh.bound, static_cast<uint32_t>(own >> 32));  // (k elements reach it)
 
     // the part's maximum and sum, its sorted list
     const float wm = code_float(__reduce_max_sync(0xffffffffu, float_code(m)));
     double ws = m == -INFINITY ? 0.0 : static_cast<double>(s) * static_cast<double>(exp_below(m, wm));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
-    __syncthreads();
     if (lane == 0) {
       sh.warp_max[warp] = wm;
       sh.warp_sum[warp] = ws;
     }
-    const int n = held;
-    rank_list(sh.list, n, k, out);
+    __syncthreads();
+    // keys that reach the bound, of all warps, into one list (the warps' other lists, which nobody reads any more)
+    {
+      const uint32_t reach = sh.bound;
+      unsigned long long keys[(kBeamMaxOut + 31) / 32];
+#pragma unroll
+      for (int q = 0; q < (kBeamMaxOut + 31) / 32; ++q) keys[q] = lane + 32 * q < n ? list[lane + 32 * q] : kNone;
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < (kBeamMaxOut + 31) / 32; ++q)
+        if (static_cast<uint32_t>(keys[q] >> 32) >= reach && keys[q] != kNone) warp_lists[atomicAdd(&sh.count, 1)] = keys[q];
+    }
+    __syncthreads();
+    const int found = sh.count;
+    rank_list(warp_lists, found, k, out);
     __syncthreads();
     if (warp == 0) {
       const float v = lane < kWarps ? sh.warp_max[lane] : -INFINITY;
@@ -432,10 +413,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
         sums[slot].sum = ps;
       }
       // fewer than k finite values: tokens at -inf, by their index
-      const int have = min(n, k);
-      int need = k - have;
-      const int t0 = v0 * E;
-      const int t1 = min(v1 * E, a.vocab);
+      int need = k - min(found, k);
+      const int t0 = v0 * E, t1 = min(v1 * E, a.vocab);
       for (int t = t0; need > 0 && t < t1; t += 32) {
         const bool low = t + lane < t1 && clean(L::at(base, t + lane)) == -INFINITY;
         const uint32_t all = __ballot_sync(0xffffffffu, low);
@@ -449,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
   cluster.sync();
 
   // ---- the first block: scores of all lists, and the best of them ----
-  unsigned long long* code = reinterpret_cast<unsigned long long*>(ring);  // [parts][k]
+  unsigned long long* code = reinterpret_cast<unsigned long long*>(area);  // [parts][k]
   int* token = reinterpret_cast<int*>(code + parts * k);                   // [parts][k]
   __shared__ double log_sum[kBeamMaxWidth];
   __shared__ float row_max[kBeamMaxWidth];
@@ -559,11 +538,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
 // Shared memory of `mine` parts a block, `parts` in all, k candidates each.
 constexpr int shared_bytes(int mine, int parts, int k) {
   const int scores = parts * k * static_cast<int>(sizeof(unsigned long long) + sizeof(int));
-  return list_bytes(mine, k) + (scores > kStages * kStageBytes ? scores : kStages * kStageBytes);
+  return list_bytes(mine, k) + (scores > warp_list_bytes(k) ? scores : warp_list_bytes(k));
 }
 // Of the widest request with the most candidates in one block, rows whole.
 constexpr int kMostShared = shared_bytes(kBeamMaxWidth, kBeamMaxWidth, kBeamMaxOut);
-static_assert(2 * kBeamMaxOut + 32 <= kCap, "a list that is not cut down leaves room");
+static_assert(kWarps * kBeamMaxOut <= 2 * kWarps * list_cap(kBeamMaxOut), "the keys of all warps, cut down, fit where their lists were");
 static_assert(kMostShared + sizeof(SelectShared) + 2048 <= 232448, "shared memory of a thread block");
 
 struct SelectPlan {
@@ -571,7 +550,7 @@ struct SelectPlan {
 };
 
 // Blocks of a cluster and parts of a row. Small batches take large clusters (up to 16 blocks, one request is one
-// cluster), so that up to four blocks an SM work; a row is cut so that the parts spread evenly over them, where a part
+// cluster), so that up to three blocks an SM work; a row is cut so that the parts spread evenly over them, where a part
 // costs what `fixed` bytes of logits do beside its own.
 SelectPlan plan_select(const BeamSelectArgs& a, int size, int most_ranks) {
   SelectPlan best{1, 1, 0};
