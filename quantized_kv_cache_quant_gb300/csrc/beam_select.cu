@@ -114,15 +114,17 @@ struct Logits<2> {  // bf16
   }
 };
 
-// What a part leaves for the first block of its cluster.
+// What a part leaves for the first block of its cluster, beside its sorted list: its maximum and the sum of exp(x -
+// maximum) in units of 2^-32 (below 2^62: whole numbers add up to the same whatever the order, and without fp64's waits).
 struct PartSum {
-  double sum;
+  unsigned long long sum;
   float max;
 };
+constexpr float kSumUnits = 4294967296.0f;
 
-// Bytes of the sums and lists of `mine` parts.
-__host__ __device__ constexpr int list_bytes(int mine, int k) {
-  return (mine * static_cast<int>(sizeof(PartSum) + k * sizeof(unsigned long long)) + 15) / 16 * 16;
+// Bytes of the sums and lists of a request's parts.
+__host__ __device__ constexpr int list_bytes(int parts, int k) {
+  return (parts * static_cast<int>(sizeof(PartSum) + k * sizeof(unsigned long long)) + 15) / 16 * 16;
 }
 
 // Keys of a warp's list: it is cut down to k before 32 more might not fit.
@@ -131,13 +133,15 @@ __host__ __device__ constexpr int list_cap(int k) { return (2 * k + 64 + 31) / 3
 __host__ __device__ constexpr int warp_list_bytes(int k) { return 2 * kWarps * list_cap(k) * static_cast<int>(sizeof(unsigned long long)); }
 
 struct SelectShared {
-  float warp_max[kWarps];
-  double warp_sum[kWarps];
   uint32_t top[kThreads];  // codes of the threads' maxima
   uint8_t rich[kThreads];  // threads whose maximum reaches the bound
-  uint32_t bound;          // code of a value that at least k elements of the part reach
-  int riches, count;       // such threads; keys in the common list
+  unsigned long long sum;  // of the part
+  uint32_t max, bound;     // codes of the part's maximum and of a value that at least k of its elements reach
+  int riches, count;       // threads in `rich`; keys in the common list
+  float score[kBeamMaxWidth];
+  uint8_t kind[kBeamMaxWidth];  // of each beam
 };
+constexpr uint8_t kLive = 0, kDead = 1, kEnded = 2;
 
 // exp(x - m) for x <= m: d = x - m rounds relative to d alone, and log2(e) in two parts keeps the product's
 // error from pointing one way over a whole row.
@@ -176,7 +180,7 @@ __device__ __noinline__ void cut_list(const unsigned long long* from, int n, int
 }
 
 template <int TYPE>
-__global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamSelectArgs a, int splits) {
+__global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSelectArgs a, int splits) {
   using L = Logits<TYPE>;
   constexpr int E = 16 / L::SIZE;  // elements of a vector
   extern __shared__ __align__(16) uint8_t dyn[];
@@ -184,21 +188,30 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamSele
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
   const int group = blockIdx.x / ranks, k = a.n_out, parts = a.width * splits;
-  const int mine = (parts + ranks - 1) / ranks;  // parts of a block at most
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cap = list_cap(k);
-  // the parts' sums and lists; the warps' lists, and after the last part the scores of all lists
-  PartSum* sums = reinterpret_cast<PartSum*>(dyn);                                                  // [mine]
-  unsigned long long* lists = reinterpret_cast<unsigned long long*>(dyn + mine * sizeof(PartSum));  // [mine][k]
-  uint8_t* const area = dyn + list_bytes(mine, k);
-  unsigned long long* const warp_lists = reinterpret_cast<unsigned long long*>(area);               // [2][kWarps][cap]
+  // the parts' sums and lists, in the first block's memory, where all blocks write them; the warps' lists, and after the
+  // last part the scores of all lists
+  PartSum* const sums = reinterpret_cast<PartSum*>(cluster.map_shared_rank(dyn, 0));  // [parts]
+  unsigned long long* const lists = reinterpret_cast<unsigned long long*>(sums + parts);  // [parts][k]
+  uint8_t* const area = dyn + list_bytes(parts, k);
+  unsigned long long* const warp_lists = reinterpret_cast<unsigned long long*>(area);  // [2][kWarps][cap]
 
-  for (int slot = 0, part = rank; part < parts; ++slot, part += ranks) {
+  // (all blocks have to run before one writes into the first's memory)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  for (int i = tid; i < a.width; i += kThreads) {
+    const long long row = static_cast<long long>(group) * a.width + i;
+    const float score = a.scores[row];
+    sh.score[i] = isfinite(score) ? score : -INFINITY;
+    sh.kind[i] = a.finished != nullptr && a.finished[row] != 0 ? kEnded : isfinite(score) ? kLive : kDead;
+  }
+  __syncthreads();
+  bool all_run = false;
+  for (int part = rank; part < parts; part += ranks) {
     const int beam = part / splits, split = part % splits;
     const long long row = static_cast<long long>(group) * a.width + beam;
-    const float score = a.scores[row];
-    unsigned long long* out = lists + slot * k;
     // a beam that has ended or is dead: its candidates follow without a look at the logits
-    if ((a.finished != nullptr && a.finished[row] != 0) || !isfinite(score)) continue;
+    if (sh.kind[beam] != kLive) continue;
+    unsigned long long* const out = lists + part * k;
     const uint8_t* base = static_cast<const uint8_t*>(a.logits) + row * a.row_stride * L::SIZE;
     // aligned vector i holds elements i * E - lead .. of the row; a thread's vector j is elements j * E .., from aligned
     // vectors j and, where the row does not start on 16 bytes, j + 1
@@ -207,7 +220,10 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamSele
     const int nv = (a.vocab + E - 1) / E;
     const int v0 = static_cast<int>(static_cast<long long>(nv) * split / splits);
     const int v1 = static_cast<int>(static_cast<long long>(nv) * (split + 1) / splits);
-    if (tid == 0) sh.riches = sh.count = 0;
+    if (tid == 0) {
+      sh.riches = sh.count = 0;
+      sh.sum = 0ull;
+    }
     __syncthreads();  // (the part before is done with the lists too)
 
     // vector j of elements by single loads; what lies outside the row becomes -inf
@@ -245,39 +261,45 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamSele
       const uint4 x = __ldg(vecs + j), y = __ldg(vecs + j + 1);
       return join(x, y);
     };
-    // a step's vectors c + 32 u + lane
-    auto load = [&](int c, uint4 (&v)[kVecs]) {
-      // all within the row, the vector behind too
-      const bool inner = c + kStep <= v1 && (lead == 0 ? (c + kStep) * static_cast<long long>(E) <= a.vocab
-                                                       : c > 0 && (c + kStep + 1) * static_cast<long long>(E) - lead <= a.vocab);
-      if (inner && lead == 0) {
+    // A step, vectors c + 32 u + lane, as it is loaded: the aligned vectors and the one behind them where all of that
+    // lies within the row (`whole`; neighbours exchange what they need when the step's turn comes), else the elements.
+    struct Step {
+      uint4 v[kVecs], behind;
+      bool whole;
+    };
+    auto load = [&](int c, Step& x) {
+      x.whole = c + kStep <= v1 && (lead == 0 ? (c + kStep) * static_cast<long long>(E) <= a.vocab
+                                              : c > 0 && (c + kStep + 1) * static_cast<long long>(E) - lead <= a.vocab);
 #pragma unroll
-        for (int u = 0; u < kVecs; ++u) v[u] = __ldg(vecs + c + 32 * u + lane);
-      } else if (inner) {
+      for (int u = 0; u < kVecs; ++u) x.v[u] = x.whole ? __ldg(vecs + c + 32 * u + lane) : vec(c + 32 * u + lane);
+      if (x.whole && lead != 0) x.behind = __ldg(vecs + c + kStep);
+    };
+    auto elements = [&](const Step& x, uint4 (&v)[kVecs]) {
 #pragma unroll
-        for (int u = 0; u < kVecs; ++u) {
-          const uint4 x = __ldg(vecs + c + 32 * u + lane), y = __ldg(vecs + c + 32 * u + lane + 1);
-          v[u] = join(x, y);
+      for (int u = 0; u < kVecs; ++u) {
+        v[u] = x.v[u];
+        if (lead != 0 && x.whole) {
+          // the vector behind comes from the next lane, lane 31's from lane 0 of the next 32
+          const uint4 from = lane == 0 ? (u + 1 < kVecs ? x.v[u + 1 < kVecs ? u + 1 : 0] : x.behind) : x.v[u];
+          const int next_lane = (lane + 1) & 31;
+          const uint4 y = make_uint4(__shfl_sync(0xffffffffu, from.x, next_lane), __shfl_sync(0xffffffffu, from.y, next_lane),
+                                     __shfl_sync(0xffffffffu, from.z, next_lane), __shfl_sync(0xffffffffu, from.w, next_lane));
+          v[u] = join(x.v[u], y);
         }
-      } else {
-#pragma unroll
-        for (int u = 0; u < kVecs; ++u) v[u] = vec(c + 32 * u + lane);
       }
     };
 
     float m = -INFINITY, s = 0.0f;  // of this thread
-    uint4 next[kVecs];
+    Step next;
     int c = v0 + warp * kStep;
     if (c < v1) load(c, next);
     for (; c < v1; c += kWarps * kStep) {
       uint4 v[kVecs];
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u) v[u] = next[u];
+      elements(next, v);
       if (c + kWarps * kStep < v1) load(c + kWarps * kStep, next);
-      float tops[kVecs];
+      float top = L::largest(v[0]);
 #pragma unroll
-      for (int u = 0; u < kVecs; ++u) tops[u] = L::largest(v[u]);
-      float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+      for (int u = 1; u < kVecs; ++u) top = fmaxf(top, L::largest(v[u]));
       const bool infinite = top == INFINITY;
       top = clean(top);
       if (top > m) {
@@ -316,25 +338,43 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamSele
       }
     }
 
-    // the k-th largest of the threads' maxima, to 16 bits and rounded down
+    // the largest of the threads' maxima and the k-th, to 16 bits and rounded down, two bits at a time
     sh.top[tid] = float_code(m);
     __syncthreads();
     if (warp == 0) {
-      uint32_t code[kWarps], bound = 0u;
+      uint32_t code[kWarps], bound = 0u, most = 0u;
 #pragma unroll
-      for (int q = 0; q < kWarps; ++q) code[q] = sh.top[lane + 32 * q];
-#pragma unroll 1
-      for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1) {
-        int reach = 0;
-#pragma unroll
-        for (int q = 0; q < kWarps; ++q) reach += code[q] >= (bound | bit);
-        if (__reduce_add_sync(0xffffffffu, reach) >= k) bound |= bit;
+      for (int q = 0; q < kWarps; ++q) {
+        code[q] = sh.top[lane + 32 * q];
+        most = max(most, code[q]);
       }
-      if (lane == 0) sh.bound = bound;
+      most = __reduce_max_sync(0xffffffffu, most);
+#pragma unroll 1
+      for (int shift = 30; shift >= 16; shift -= 2) {
+        uint32_t reach = 0;  // three counts of up to 256
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q)
+#pragma unroll
+          for (uint32_t x = 1; x < 4; ++x) reach += code[q] >= (bound | x << shift) ? 1u << (10 * (x - 1)) : 0u;
+        reach = __reduce_add_sync(0xffffffffu, reach);
+        const uint32_t above = ((reach & 1023u) >= k) + ((reach >> 10 & 1023u) >= k) + ((reach >> 20) >= k);
+        bound |= above << shift;
+      }
+      if (lane == 0) {
+        sh.max = most;
+        sh.bound = bound;
+      }
     }
     __syncthreads();
     const uint32_t bound = sh.bound;
+    const float part_max = code_float(sh.max);
     if (m > -INFINITY && float_code(m) >= bound) sh.rich[atomicAdd(&sh.riches, 1)] = static_cast<uint8_t>(tid);
+    {
+      unsigned long long units = m > -INFINITY ? __float2ull_rn(s * exp_below(m, part_max) * kSumUnits) : 0ull;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
+      if (lane == 0) atomicAdd(&sh.sum, units);
+    }
     __syncthreads();
 
     // their elements once more, a warp for a thread's
@@ -374,18 +414,8 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamSele
         }
       }
     }
-    if (n > k) cut();
+    if (n > max(k, 32)) cut();
     if (lane == 0 && own != kNone) atomicMax(&sh.bound, static_cast<uint32_t>(own >> 32));  // (k elements reach it)
-
-    // the part's maximum and sum, its sorted list
-    const float wm = code_float(__reduce_max_sync(0xffffffffu, float_code(m)));
-    double ws = m == -INFINITY ? 0.0 : static_cast<double>(s) * static_cast<double>(exp_below(m, wm));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
-    if (lane == 0) {
-      sh.warp_max[warp] = wm;
-      sh.warp_sum[warp] = ws;
-    }
     __syncthreads();
     // keys that reach the bound, of all warps, into one list (the warps' other lists, which nobody reads any more)
     {
@@ -400,32 +430,29 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamSele
     }
     __syncthreads();
     const int found = sh.count;
+    if (!all_run) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    all_run = true;
     rank_list(warp_lists, found, k, out);
-    __syncthreads();
-    if (warp == 0) {
-      const float v = lane < kWarps ? sh.warp_max[lane] : -INFINITY;
-      const float pm = code_float(__reduce_max_sync(0xffffffffu, float_code(v)));
-      double ps = v == -INFINITY ? 0.0 : sh.warp_sum[lane] * static_cast<double>(exp_below(v, pm));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
-      if (lane == 0) {
-        sums[slot].max = pm;
-        sums[slot].sum = ps;
-      }
-      // fewer than k finite values: tokens at -inf, by their index
-      int need = k - min(found, k);
-      const int t0 = v0 * E, t1 = min(v1 * E, a.vocab);
-      for (int t = t0; need > 0 && t < t1; t += 32) {
-        const bool low = t + lane < t1 && clean(L::at(base, t + lane)) == -INFINITY;
-        const uint32_t all = __ballot_sync(0xffffffffu, low);
-        const int at = __popc(all & ((1u << lane) - 1u));
-        if (low && at < need) out[k - need + at] = make_key(-INFINITY, t + lane);
-        need -= __popc(all);
+    if (tid == 0) sums[part] = PartSum{sh.sum, part_max};
+    if (found < k) {  // tokens at -inf, by their index
+      __syncthreads();
+      if (warp == 0) {
+        int need = k - found;
+        const int t0 = v0 * E, t1 = min(v1 * E, a.vocab);
+        for (int t = t0; need > 0 && t < t1; t += 32) {
+          const bool low = t + lane < t1 && clean(L::at(base, t + lane)) == -INFINITY;
+          const uint32_t all = __ballot_sync(0xffffffffu, low);
+          const int at = __popc(all & ((1u << lane) - 1u));
+          if (low && at < need) out[k - need + at] = make_key(-INFINITY, t + lane);
+          need -= __popc(all);
+        }
       }
     }
     __syncthreads();
   }
+  if (!all_run) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   cluster.sync();
+  if (rank != 0) return;
 
   // ---- the first block: scores of all lists, and the best of them ----
   unsigned long long* code = reinterpret_cast<unsigned long long*>(area);  // [parts][k]
@@ -437,62 +464,70 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamSele
     const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(x));
     return u >> 63 ? ~u : u | (1ull << 63);
   };
-  auto ended = [&](int beam) {
-    const long long row = static_cast<long long>(group) * a.width + beam;
-    return a.finished != nullptr && a.finished[row] != 0;
-  };
-  if (rank == 0) {
-    for (int beam = tid; beam < a.width; beam += kThreads) {
-      const float score = a.scores[static_cast<long long>(group) * a.width + beam];
-      double sum = 0.0;
-      float most = -INFINITY;
-      if (!ended(beam) && isfinite(score)) {
-        for (int split = 0; split < splits; ++split) {
-          const int part = beam * splits + split;
-          most = fmaxf(most, cluster.map_shared_rank(sums, part % ranks)[part / ranks].max);
-        }
-        for (int split = 0; most > -INFINITY && split < splits; ++split) {
-          const int part = beam * splits + split;
-          const PartSum p = cluster.map_shared_rank(sums, part % ranks)[part / ranks];
-          if (p.max > -INFINITY) sum += p.sum * static_cast<double>(exp_below(p.max, most));
-        }
+  for (int beam = tid; beam < a.width; beam += kThreads) {
+    double sum = 0.0;
+    float most = -INFINITY;
+    if (sh.kind[beam] == kLive) {
+      for (int split = 0; split < splits; ++split) most = fmaxf(most, sums[beam * splits + split].max);
+      for (int split = 0; most > -INFINITY && split < splits; ++split) {
+        const PartSum p = sums[beam * splits + split];
+        if (p.max > -INFINITY) sum += static_cast<double>(p.sum) * static_cast<double>(exp_below(p.max, most));
       }
-      log_sum[beam] = most == -INFINITY ? 0.0 : log(sum);
-      row_max[beam] = most;
     }
-    __syncthreads();
-    for (int i = tid; i < parts * k; i += kThreads) {
-      const int part = i / k, at = i % k, beam = part / splits;
-      const float score = a.scores[static_cast<long long>(group) * a.width + beam];
-      unsigned long long c = 0ull;
-      int t = 0;
-      const bool end = ended(beam);
-      if (end || !isfinite(score)) {
-        // the end token first, then the others by their index, all in the row's first part
-        if (part % splits == 0) {
-          if (end && at == 0) {
-            t = a.end_token;
-            c = score_code(isfinite(score) ? static_cast<double>(score) : -INFINITY);
-          } else {
-            t = end ? at - 1 + (at - 1 >= a.end_token) : at;
-            c = score_code(-INFINITY);
-          }
-        }
-      } else {
-        const unsigned long long key = cluster.map_shared_rank(lists, part % ranks)[(part / ranks) * k + at];
-        if (key != kNone) {
-          const float x = code_float(static_cast<uint32_t>(key >> 32));
-          t = key_token(key);
-          c = score_code(x == -INFINITY ? -INFINITY
-                                        : static_cast<double>(score) + ((static_cast<double>(x) - static_cast<double>(row_max[beam])) - log_sum[beam]));
-        }
-      }
-      code[i] = c;
-      token[i] = t;
-    }
+    log_sum[beam] = most == -INFINITY ? 0.0 : log(sum * (1.0 / kSumUnits));
+    row_max[beam] = most;
   }
-  cluster.sync();  // (no block ends while the first one reads its lists)
-  if (rank != 0 || warp != 0) return;
+  __syncthreads();
+  for (int i = tid; i < parts * k; i += kThreads) {
+    const int part = i / k, at = i % k, beam = part / splits;
+    const float score = sh.score[beam];
+    unsigned long long c = 0ull;
+    int t = 0;
+    if (sh.kind[beam] != kLive) {
+      // the end token first, then the others by their index, all in the row's first part
+      const bool end = sh.kind[beam] == kEnded;
+      if (part % splits == 0) {
+        t = !end ? at : at == 0 ? a.end_token : at - 1 + (at - 1 >= a.end_token);
+        c = score_code(end && at == 0 ? static_cast<double>(score) : -INFINITY);
+      }
+    } else {
+      const unsigned long long key = lists[i];
+      if (key != kNone) {
+        const float x = code_float(static_cast<uint32_t>(key >> 32));
+        t = key_token(key);
+        c = score_code(x == -INFINITY ? -INFINITY
+                                      : static_cast<double>(score) + ((static_cast<double>(x) - static_cast<double>(row_max[beam])) - log_sum[beam]));
+      }
+    }
+    code[i] = c;
+    token[i] = t;
+  }
+  __syncthreads();
+  auto put = [&](int o, int i) {  // candidate i is the o-th best
+    const unsigned long long u = code[i];
+    const double x = __longlong_as_double(static_cast<long long>(u >> 63 ? u & ~(1ull << 63) : ~u));
+    const long long to = static_cast<long long>(group) * k + o;
+    a.out_scores[to] = static_cast<float>(x);
+    a.out_parents[to] = i / k / splits;
+    a.out_tokens[to] = token[i];
+  };
+  // Equal scores: the lower beam, then the lower token (the lists' order: parts of a row go up in tokens).
+  const int total = parts * k;
+  if (total <= kThreads) {
+    // few: eight threads count those before a candidate
+    for (int i0 = 0; i0 + (warp << 2) < total; i0 += kThreads / 8) {
+      const int i = i0 + tid / 8;
+      const unsigned long long c = i < total ? code[i] : 0ull;
+      int before = 0;
+      for (int j = tid % 8; j < total; j += 8) before += code[j] > c || (code[j] == c && j < i);
+      before += __shfl_xor_sync(0xffffffffu, before, 1);
+      before += __shfl_xor_sync(0xffffffffu, before, 2);
+      before += __shfl_xor_sync(0xffffffffu, before, 4);
+      if (tid % 8 == 0 && i < total && c != 0ull && before < k) put(before, i);
+    }
+    return;
+  }
+  if (warp != 0) return;
   // lane l's lists are l, l + 32, ...: a head each
   constexpr int kLists = kMaxParts / 32;
   int at[kLists];
@@ -500,34 +535,25 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamSele
   for (int q = 0; q < kLists; ++q) at[q] = 0;
   for (int o = 0; o < k; ++o) {
     unsigned long long best = 0ull;
-    int best_q = 0, best_part = INT_MAX, best_token = INT_MAX;
+    int best_q = 0, best_at = INT_MAX;
 #pragma unroll
     for (int q = 0; q < kLists; ++q) {
       const int part = lane + 32 * q;
       if (part >= parts || at[q] >= k) continue;
       const unsigned long long c = code[part * k + at[q]];
-      // (a lane's lists go up in beams and, within one, in tokens)
       if (c > best) {
         best = c;
         best_q = q;
-        best_part = part;
-        best_token = token[part * k + at[q]];
+        best_at = part * k + at[q];
       }
     }
     const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(best >> 32));
     const bool in_hi = static_cast<uint32_t>(best >> 32) == hi;
     const uint32_t lo = __reduce_max_sync(0xffffffffu, in_hi ? static_cast<uint32_t>(best) : 0u);
     const bool tie = in_hi && static_cast<uint32_t>(best) == lo && best != 0ull;
-    // equal scores: the lower beam, then the lower token (parts of a row go up in tokens, but equal values in two parts
-    // of one row follow the parts)
-    const uint32_t part = __reduce_min_sync(0xffffffffu, tie ? static_cast<uint32_t>(best_part) : 0xffffffffu);
-    if (tie && static_cast<uint32_t>(best_part) == part) {
-      const unsigned long long u = best;
-      const double x = __longlong_as_double(static_cast<long long>(u >> 63 ? u & ~(1ull << 63) : ~u));
-      const long long to = static_cast<long long>(group) * k + o;
-      a.out_scores[to] = static_cast<float>(x);
-      a.out_parents[to] = best_part / splits;
-      a.out_tokens[to] = best_token;
+    const uint32_t first = __reduce_min_sync(0xffffffffu, tie ? static_cast<uint32_t>(best_at) : 0xffffffffu);
+    if (tie && static_cast<uint32_t>(best_at) == first) {
+      put(o, best_at);
 #pragma unroll
       for (int q = 0; q < kLists; ++q) at[q] += q == best_q;
     }
@@ -535,13 +561,13 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamSele
   }
 }
 
-// Shared memory of `mine` parts a block, `parts` in all, k candidates each.
-constexpr int shared_bytes(int mine, int parts, int k) {
+// Shared memory of a request of `parts` parts, k candidates each.
+constexpr int shared_bytes(int parts, int k) {
   const int scores = parts * k * static_cast<int>(sizeof(unsigned long long) + sizeof(int));
-  return list_bytes(mine, k) + (scores > warp_list_bytes(k) ? scores : warp_list_bytes(k));
+  return list_bytes(parts, k) + (scores > warp_list_bytes(k) ? scores : warp_list_bytes(k));
 }
 // Of the widest request with the most candidates in one block, rows whole.
-constexpr int kMostShared = shared_bytes(kBeamMaxWidth, kBeamMaxWidth, kBeamMaxOut);
+constexpr int kMostShared = shared_bytes(kBeamMaxWidth, kBeamMaxOut);
 static_assert(kWarps * kBeamMaxOut <= 2 * kWarps * list_cap(kBeamMaxOut), "the keys of all warps, cut down, fit where their lists were");
 static_assert(kMostShared + sizeof(SelectShared) + 2048 <= 232448, "shared memory of a thread block");
 
@@ -549,27 +575,24 @@ struct SelectPlan {
   int ranks, splits, smem;
 };
 
-// Blocks of a cluster and parts of a row. Small batches take large clusters (up to 16 blocks, one request is one
-// cluster), so that up to three blocks an SM work; a row is cut so that the parts spread evenly over them, where a part
-// costs what `fixed` bytes of logits do beside its own.
-SelectPlan plan_select(const BeamSelectArgs& a, int size, int most_ranks) {
+// Blocks of a cluster (up to 16: one request is one cluster), as many as have room at once, and parts of a row, so that
+// the block with the most to do has little of it; a part costs what `fixed` bytes of logits do beside its own.
+SelectPlan plan_select(const BeamSelectArgs& a, int size) {
   SelectPlan best{1, 1, 0};
   const long long fixed = 16384;
   int ranks = 1;
-  while (ranks < most_ranks && static_cast<long long>(a.groups) * ranks * 2 <= 4ll * device_sm_count()) ranks *= 2;
+  while (ranks < 16 && static_cast<long long>(a.groups) * ranks * 2 <= 4ll * device_sm_count()) ranks *= 2;
   long long best_cost = LLONG_MAX;
   for (int splits = 1; splits <= 32 && a.width * splits <= kMaxParts; ++splits) {
-    const long long rounds = (a.width * splits + ranks - 1) / ranks;
-    const long long cost = rounds * (static_cast<long long>(a.vocab) * size / splits + fixed);
     const int parts = a.width * splits;
-    const int smem = shared_bytes(static_cast<int>(rounds), parts, a.n_out);
+    const long long rounds = (parts + ranks - 1) / ranks;
+    const long long cost = rounds * (static_cast<long long>(a.vocab) * size / splits + fixed);
+    const int smem = shared_bytes(parts, a.n_out);
     if (cost < best_cost && (splits == 1 || smem <= kMostShared)) {
       best_cost = cost;
-      best.splits = splits;
-      best.smem = smem;
+      best = SelectPlan{ranks, splits, smem};
     }
   }
-  best.ranks = ranks;
   return best;
 }
 
@@ -581,7 +604,7 @@ cudaError_t launch_select(const BeamSelectArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
-  const SelectPlan p = plan_select(a, Logits<TYPE>::SIZE, 16);
+  const SelectPlan p = plan_select(a, Logits<TYPE>::SIZE);
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
