@@ -58,218 +58,240 @@ __global__ void __launch_bounds__(128) group_rows16_kernel(const __grid_constant
     for (int s = 0; s < kStages; ++s) mbar_init(&bar[s], 1);
     fence_mbar_init();
   }
-  if (tid == 0) args_s = a;
+  // Thread blocks of their own for each kind, cut into slices of their own: own pairs are many and short, and a few blocks
+  // would have nothing else if both kinds were cut as one (8 groups of 4 over 32K shared tokens: 267 us so, 121 apart).
+  if (tid == 0) {
+    args_s = a;
+    if (a.kinds == 3) args_s.kinds = 1 << blockIdx.y;
+  }
+  __syncthreads();
+  const TreeSlice slice = tree_slice<kRows, kUnit>(
+      args_s, plan_s, [](long long pair) { return pair >= 32 ? 4 : 2; }, [](long long u) { return u >= 4 ? 4 : 2; });
+  if (slice.begin >= slice.end) return;
+  if (tid == 0) slice_s = slice;
+  __syncthreads();
   GroupWalk walk;
+  walk.start(slice);
   const GroupSegment& seg = walk.seg;
   unsigned it = 0;         // blocks this warp has taken through its ring
   bool dead = false;       // a wait ran out: no more copies
-  // One kind after the other, each cut into slices of its own: own pairs are many and short, and a few thread blocks
-  // would have nothing else if both kinds were cut as one (8 groups of 4 over 32K shared tokens: 267 us so, 0 as here).
-#pragma unroll 1
-  for (int kind = 0; kind < 2; ++kind) {
-    __syncthreads();
-    if (tid == 0) args_s.kinds = a.kinds & (1 << kind);
-    __syncthreads();
-    if (args_s.kinds == 0) continue;
-    const TreeSlice slice = tree_slice<kRows, kUnit>(
-        args_s, plan_s, [](long long pair) { return pair >= 32 ? 4 : 2; }, [](long long u) { return u >= 4 ? 4 : 2; });
-    if (slice.begin >= slice.end) continue;
-    if (tid == 0) slice_s = slice;
-    __syncthreads();
-    walk.start(slice);
-    while (next_segment<kRows, kUnit>(args_s, slice_s, walk)) {
-      const int h = seg.h, total = seg.r.len, row0 = seg.tile * kRows;
-      const int rows = min(kRows, seg.r.nodes * gq - row0);
-      const int nblk = tree_units(total, kBlock);
-      const int j_begin = seg.u0 * 4, j_end = min(seg.u1 * 4, nblk);
-      const int n_mine = (!dead && j_end - j_begin > warp) ? (j_end - j_begin - warp + 3) / 4 : 0;
-      const int32_t* table = a.block_table + static_cast<long long>(seg.r.seq) * a.max_blocks + seg.r.block0;
-      auto phys = [&](int j) -> long long {
-        return min(max(table[j_begin + warp + 4 * j], 0), a.num_blocks - 1);
-      };
-      auto issue = [&](int j, long long blk) {
-        const long long off = (blk * a.kv_heads + h) * (kBlock * D);
-        const int s = (it + j) % kStages;
-        uint8_t* dst = ring + s * S::STAGE;
-        mbar_arrive_expect_tx(&bar[s], S::STAGE);
-        bulk_g2s(dst, a.k_pool + off, kBlock * D, &bar[s]);
-        bulk_g2s(dst + kBlock * D, a.v_pool + off, kBlock * D, &bar[s]);
-      };
-      if (lane == 0) {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        for (int j = 0; j < kStages && j < n_mine; ++j) issue(j, phys(j));
-      }
+  int turn = 0;            // the warp whose turn it is to take a short segment alone
+  while (next_segment<kRows, kUnit>(args_s, slice_s, walk)) {
+    const int h = seg.h, total = seg.r.len, row0 = seg.tile * kRows;
+    const int rows = min(kRows, seg.r.nodes * gq - row0);
+    const int nblk = tree_units(total, kBlock);
+    const int j_begin = seg.u0 * 4, j_end = min(seg.u1 * 4, nblk);
+    // A short segment among others is one warp's alone, beside the other warps' segments, with no barriers: 2048 pairs of
+    // 20 to 100 tokens took 47 us with all four warps at each of them.
+    const int units = seg.u1 - seg.u0;
+    const bool alone = units <= 4 && slice.end - slice.begin >= 3 * units;
+    if (alone) {
+      turn = (turn + 1) & 3;
+      if (turn != warp) continue;
+    }
+    const int first = alone ? 0 : warp, step = alone ? 1 : 4;
+    const int n_mine = (!dead && j_end - j_begin > first) ? (j_end - j_begin - first + step - 1) / step : 0;
+    const int32_t* table = a.block_table + static_cast<long long>(seg.r.seq) * a.max_blocks + seg.r.block0;
+    auto phys = [&](int j) -> long long {
+      return min(max(table[j_begin + first + step * j], 0), a.num_blocks - 1);
+    };
+    auto issue = [&](int j, long long blk) {
+      const long long off = (blk * a.kv_heads + h) * (kBlock * D);
+      const int s = (it + j) % kStages;
+      uint8_t* dst = ring + s * S::STAGE;
+      mbar_arrive_expect_tx(&bar[s], S::STAGE);
+      bulk_g2s(dst, a.k_pool + off, kBlock * D, &bar[s]);
+      bulk_g2s(dst + kBlock * D, a.v_pool + off, kBlock * D, &bar[s]);
+    };
+    if (lane == 0) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      for (int j = 0; j < kStages && j < n_mine; ++j) issue(j, phys(j));
+    }
 
-      // query rows g and g + 8 of the tile, A fragments of m16n8k16
-      uint32_t qa[KS][4];
+    // query rows g and g + 8 of the tile, A fragments of m16n8k16
+    uint32_t qa[KS][4];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = row0 + g + 8 * e;
-        const bool ok = g + 8 * e < rows;
-        const __half* qrow = reinterpret_cast<const __half*>(a.q) + (seg.r.first + (ok ? r / gq : 0)) * a.q_stride +
-                             static_cast<long long>(h * gq + (ok ? r % gq : 0)) * D;
+    for (int e = 0; e < 2; ++e) {
+      const int r = row0 + g + 8 * e;
+      const bool ok = g + 8 * e < rows;
+      const __half* qrow = reinterpret_cast<const __half*>(a.q) + (seg.r.first + (ok ? r / gq : 0)) * a.q_stride +
+                           static_cast<long long>(h * gq + (ok ? r % gq : 0)) * D;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const uint2 w = ok ? *reinterpret_cast<const uint2*>(qrow + 16 * ks + 4 * tig) : make_uint2(0u, 0u);
+        qa[ks][e] = w.x;
+        qa[ks][2 + e] = w.y;
+      }
+    }
+    const float kmul = a.k_scale[a.per_head ? h : 0] * a.scale_log2;
+
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.0f, 0.0f};
+    float o_acc[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o_acc[i][0] = o_acc[i][1] = o_acc[i][2] = o_acc[i][3] = 0.0f;
+
+    int j = 0;
+    bool timed_out = false;
+    for (; j < n_mine; ++j) {
+      const int s = (it + j) % kStages;
+      const long long next_blk = (lane == 0 && j + kStages < n_mine) ? phys(j + kStages) : 0;
+      if (__any_sync(0xffffffffu, !mbar_wait_bounded(&bar[s], ((it + j) / kStages) & 1))) {
+        timed_out = true;
+        break;
+      }
+      const uint4* kb = reinterpret_cast<const uint4*>(ring + s * S::STAGE);
+      const uint4* vb = reinterpret_cast<const uint4*>(ring + s * S::STAGE + kBlock * D);
+      const int tok_base = (j_begin + first + step * j) * kBlock;
+      uint32_t kw[2 * KS];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const uint4 x = kb[c * 32 + lane];
+        kw[4 * c] = x.x;
+        kw[4 * c + 1] = x.y;
+        kw[4 * c + 2] = x.z;
+        kw[4 * c + 3] = x.w;
+      }
+      float sacc[2][4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        sacc[nt][0] = sacc[nt][1] = sacc[nt][2] = sacc[nt][3] = 0.0f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          const uint2 w = ok ? *reinterpret_cast<const uint2*>(qrow + 16 * ks + 4 * tig) : make_uint2(0u, 0u);
-          qa[ks][e] = w.x;
-          qa[ks][2 + e] = w.y;
+          const uint32_t w = kw[nt * KS + ks];
+          mma16816(sacc[nt], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], fp8_lo_pair<FMT>(w), fp8_hi_pair<FMT>(w));
         }
       }
-      const float kmul = a.k_scale[a.per_head ? h : 0] * a.scale_log2;
-
-      float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.0f, 0.0f};
-      float o_acc[NT][4];
+      uint32_t vw[NT];
 #pragma unroll
-      for (int i = 0; i < NT; ++i) o_acc[i][0] = o_acc[i][1] = o_acc[i][2] = o_acc[i][3] = 0.0f;
-
-      int j = 0;
-      bool timed_out = false;
-      for (; j < n_mine; ++j) {
-        const int s = (it + j) % kStages;
-        const long long next_blk = (lane == 0 && j + kStages < n_mine) ? phys(j + kStages) : 0;
-        if (__any_sync(0xffffffffu, !mbar_wait_bounded(&bar[s], ((it + j) / kStages) & 1))) {
-          timed_out = true;
-          break;
-        }
-        const uint4* kb = reinterpret_cast<const uint4*>(ring + s * S::STAGE);
-        const uint4* vb = reinterpret_cast<const uint4*>(ring + s * S::STAGE + kBlock * D);
-        const int tok_base = (j_begin + warp + 4 * j) * kBlock;
-        uint32_t kw[2 * KS];
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const uint4 x = kb[c * 32 + lane];
-          kw[4 * c] = x.x;
-          kw[4 * c + 1] = x.y;
-          kw[4 * c + 2] = x.z;
-          kw[4 * c + 3] = x.w;
-        }
-        float sacc[2][4];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          sacc[nt][0] = sacc[nt][1] = sacc[nt][2] = sacc[nt][3] = 0.0f;
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            const uint32_t w = kw[nt * KS + ks];
-            mma16816(sacc[nt], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], fp8_lo_pair<FMT>(w), fp8_hi_pair<FMT>(w));
-          }
-        }
-        uint32_t vw[NT];
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const uint4 x = vb[c * 32 + lane];
-          vw[4 * c] = x.x;
-          vw[4 * c + 1] = x.y;
-          vw[4 * c + 2] = x.z;
-          vw[4 * c + 3] = x.w;
-        }
-        // scores of rows g (sc[0]) and g + 8 (sc[1]): tokens 2tig, 2tig + 1, 8 + 2tig, 9 + 2tig
-        float sc[2][4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sc[e][i] = sacc[i >> 1][2 * e + (i & 1)] * kmul;
-        if (tree_beyond(tok_base, kBlock, total)) {  // rows of the block behind the last token: not seen, values as 0
-          uint32_t keep = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (tok_base + 8 * (i >> 1) + 2 * tig + (i & 1) < total) keep |= 0xFFu << (8 * i);
-            else sc[0][i] = sc[1][i] = -INFINITY;
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) vw[nt] &= keep;
-        }
-        uint32_t A[4], L[4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float mx = quad_max(fmaxf(fmaxf(sc[e][0], sc[e][1]), fmaxf(sc[e][2], sc[e][3])));
-          const float m_new = fmaxf(m_run[e], mx);
-          if (m_new != m_run[e]) {
-            const float alpha = fast_exp2(m_run[e] - m_new);
-            l_run[e] *= alpha;
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              o_acc[i][2 * e] *= alpha;
-              o_acc[i][2 * e + 1] *= alpha;
-            }
-            m_run[e] = m_new;
-          }
-          const float sub = (m_new == -INFINITY ? 0.0f : m_new) - kBias;
-          float p[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) p[i] = fast_exp2(sc[e][i] - sub);
-          l_run[e] += (p[0] + p[1]) + (p[2] + p[3]);
-          const __half2 h0 = __floats2half2_rn(p[0], p[1]), h1 = __floats2half2_rn(p[2], p[3]);
-          A[e] = h2_bits(h0);
-          A[2 + e] = h2_bits(h1);
-          const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-          L[e] = pack_rn_f16x2(p[0] - f0.x, p[1] - f0.y);
-          L[2 + e] = pack_rn_f16x2(p[2] - f1.x, p[3] - f1.y);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint32_t b0 = fp8_lo_pair<FMT>(vw[nt]), b1 = fp8_hi_pair<FMT>(vw[nt]);
-          mma16816(o_acc[nt], A[0], A[1], A[2], A[3], b0, b1);
-          mma16816(o_acc[nt], L[0], L[1], L[2], L[3], b0, b1);
-        }
-        __syncwarp();
-        if (lane == 0 && j + kStages < n_mine) {
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          issue(j + kStages, next_blk);
-        }
+      for (int c = 0; c < CH; ++c) {
+        const uint4 x = vb[c * 32 + lane];
+        vw[4 * c] = x.x;
+        vw[4 * c + 1] = x.y;
+        vw[4 * c + 2] = x.z;
+        vw[4 * c + 3] = x.w;
       }
-      if (timed_out) {
-        if (lane == 0) report_timeout(a.status);
-        for (int jj = j; jj < n_mine && jj < j + kStages; ++jj)
-          (void)mbar_wait_bounded(&bar[(it + jj) % kStages], ((it + jj) / kStages) & 1);
-        dead = true;
-        m_run[0] = m_run[1] = -INFINITY;
-        l_run[0] = l_run[1] = 0.0f;
+      // scores of rows g (sc[0]) and g + 8 (sc[1]): tokens 2tig, 2tig + 1, 8 + 2tig, 9 + 2tig
+      float sc[2][4];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) o_acc[i][0] = o_acc[i][1] = o_acc[i][2] = o_acc[i][3] = 0.0f;
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[e][i] = sacc[i >> 1][2 * e + (i & 1)] * kmul;
+      if (tree_beyond(tok_base, kBlock, total)) {  // rows of the block behind the last token: not seen, values as 0
+        uint32_t keep = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (tok_base + 8 * (i >> 1) + 2 * tig + (i & 1) < total) keep |= 0xFFu << (8 * i);
+          else sc[0][i] = sc[1][i] = -INFINITY;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) vw[nt] &= keep;
       }
-      it += n_mine;
-      l_run[0] = quad_sum(l_run[0]);
-      l_run[1] = quad_sum(l_run[1]);
-
-      __syncthreads();  // all rings are drained: their memory takes the warps' results
+      uint32_t A[4], L[4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = warp * kRows + g + 8 * e;
+        const float mx = quad_max(fmaxf(fmaxf(sc[e][0], sc[e][1]), fmaxf(sc[e][2], sc[e][3])));
+        const float m_new = fmaxf(m_run[e], mx);
+        if (m_new != m_run[e]) {
+          const float alpha = fast_exp2(m_run[e] - m_new);
+          l_run[e] *= alpha;
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            o_acc[i][2 * e] *= alpha;
+            o_acc[i][2 * e + 1] *= alpha;
+          }
+          m_run[e] = m_new;
+        }
+        const float sub = (m_new == -INFINITY ? 0.0f : m_new) - kBias;
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = fast_exp2(sc[e][i] - sub);
+        l_run[e] += (p[0] + p[1]) + (p[2] + p[3]);
+        const __half2 h0 = __floats2half2_rn(p[0], p[1]), h1 = __floats2half2_rn(p[2], p[3]);
+        A[e] = h2_bits(h0);
+        A[2 + e] = h2_bits(h1);
+        const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+        L[e] = pack_rn_f16x2(p[0] - f0.x, p[1] - f0.y);
+        L[2 + e] = pack_rn_f16x2(p[2] - f1.x, p[3] - f1.y);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint32_t b0 = fp8_lo_pair<FMT>(vw[nt]), b1 = fp8_hi_pair<FMT>(vw[nt]);
+        mma16816(o_acc[nt], A[0], A[1], A[2], A[3], b0, b1);
+        mma16816(o_acc[nt], L[0], L[1], L[2], L[3], b0, b1);
+      }
+      __syncwarp();
+      if (lane == 0 && j + kStages < n_mine) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        issue(j + kStages, next_blk);
+      }
+    }
+    if (timed_out) {
+      if (lane == 0) report_timeout(a.status);
+      for (int jj = j; jj < n_mine && jj < j + kStages; ++jj)
+        (void)mbar_wait_bounded(&bar[(it + jj) % kStages], ((it + jj) / kStages) & 1);
+      dead = true;
+      m_run[0] = m_run[1] = -INFINITY;
+      l_run[0] = l_run[1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) o_acc[i][0] = o_acc[i][1] = o_acc[i][2] = o_acc[i][3] = 0.0f;
+    }
+    it += n_mine;
+    l_run[0] = quad_sum(l_run[0]);
+    l_run[1] = quad_sum(l_run[1]);
+
+    if (alone) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = g + 8 * e;
+        if (r >= rows) continue;
+        const GroupPlace to = group_place<D>(args_s, seg, gq, row0, r, 0, r, kRows);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          *reinterpret_cast<float2*>(o_s + r * D + 8 * nt + 2 * tig) = make_float2(o_acc[nt][2 * e], o_acc[nt][2 * e + 1]);
-        if (tig == 0) {
-          m_s[r] = m_run[e];
-          l_s[r] = l_run[e];
-        }
+          *reinterpret_cast<float2*>(to.o + 8 * nt + 2 * tig) = make_float2(o_acc[nt][2 * e], o_acc[nt][2 * e + 1]);
+        if (tig == 0) *reinterpret_cast<float2*>(to.ml) = make_float2(m_run[e] - kBias, l_run[e]);
       }
-      __syncthreads();
-      constexpr int V = D / 4;
-      for (int i = tid; i < rows * V; i += 128) {
-        const int r = i / V, c4 = i % V;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) M = fmaxf(M, m_s[w * kRows + r]);
-        float L = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          // (a warp without a maximum has the sum 0, or NaN, which stays)
-          const float f = M == -INFINITY ? 1.0f : fast_exp2(m_s[w * kRows + r] - M);
-          const float4 x = *reinterpret_cast<const float4*>(o_s + (w * kRows + r) * D + 4 * c4);
-          L = fmaf(l_s[w * kRows + r], f, L);
-          o.x = fmaf(x.x, f, o.x);
-          o.y = fmaf(x.y, f, o.y);
-          o.z = fmaf(x.z, f, o.z);
-          o.w = fmaf(x.w, f, o.w);
-        }
-        const GroupPlace to = group_place<D>(args_s, seg, gq, row0, r, 0, r, kRows);
-        *reinterpret_cast<float4*>(to.o + 4 * c4) = o;
-        if (c4 == 0) *reinterpret_cast<float2*>(to.ml) = make_float2(M - kBias, L);
-      }
-      if (tid == 0) group_record(args_s, seg);
-      __syncthreads();  // the next segment's copies overwrite what was read here
+      if (lane == 0) group_record(args_s, seg);
+      __syncwarp();
+      continue;
     }
+    __syncthreads();  // all rings are drained: their memory takes the warps' results
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = warp * kRows + g + 8 * e;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        *reinterpret_cast<float2*>(o_s + r * D + 8 * nt + 2 * tig) = make_float2(o_acc[nt][2 * e], o_acc[nt][2 * e + 1]);
+      if (tig == 0) {
+        m_s[r] = m_run[e];
+        l_s[r] = l_run[e];
+      }
+    }
+    __syncthreads();
+    constexpr int V = D / 4;
+    for (int i = tid; i < rows * V; i += 128) {
+      const int r = i / V, c4 = i % V;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) M = fmaxf(M, m_s[w * kRows + r]);
+      float L = 0.0f;
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        // (a warp without a maximum has the sum 0, or NaN, which stays)
+        const float f = M == -INFINITY ? 1.0f : fast_exp2(m_s[w * kRows + r] - M);
+        const float4 x = *reinterpret_cast<const float4*>(o_s + (w * kRows + r) * D + 4 * c4);
+        L = fmaf(l_s[w * kRows + r], f, L);
+        o.x = fmaf(x.x, f, o.x);
+        o.y = fmaf(x.y, f, o.y);
+        o.z = fmaf(x.z, f, o.z);
+        o.w = fmaf(x.w, f, o.w);
+      }
+      const GroupPlace to = group_place<D>(args_s, seg, gq, row0, r, 0, r, kRows);
+      *reinterpret_cast<float4*>(to.o + 4 * c4) = o;
+      if (c4 == 0) *reinterpret_cast<float2*>(to.ml) = make_float2(M - kBias, L);
+    }
+    if (tid == 0) group_record(args_s, seg);
+    __syncthreads();  // the next segment's copies overwrite what was read here
   }
 }
 
@@ -359,7 +381,7 @@ cudaError_t launch_rows16(const GroupArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   int grid = device_sm_count() * per_sm;
   if (grid > kGroupMaxBlocks) grid = kGroupMaxBlocks;
-  kern<<<grid, 128, smem, s>>>(a);
+  kern<<<dim3(grid, a.kinds == 3 ? 2 : 1), 128, smem, s>>>(a);
   return cudaGetLastError();
 }
 
