@@ -296,72 +296,88 @@ __global__ void __launch_bounds__(128) group_rows16_kernel(const __grid_constant
 }
 
 // ---------------------------------------------------------------------------
-// Joining: a warp per output row. Lanes weigh the row's partial results of both
-// kinds (log2 units), then its outputs are added up part by part, in a fixed
-// order.
+// Joining: a warp per output row. What it has to know of the row's two pairs is
+// read at once, then lanes weigh the partial results (log2 units), 32 at a time
+// and the shared ones first, then the outputs are added up in that order: three
+// dependent reads in all.
 // ---------------------------------------------------------------------------
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) group_join_kernel(const __grid_constant__ GroupArgs a) {
   constexpr int V = D / 32;  // floats of a row a lane holds
   const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
-  if (row >= static_cast<long long>(a.batch) * a.q_heads) return;
-  const int b = static_cast<int>(row / a.q_heads), hq = static_cast<int>(row % a.q_heads);
+  const unsigned row = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);  // (at most 4096 sequences of 65535 x 64 heads)
+  if (row >= static_cast<unsigned>(a.batch) * a.q_heads) return;
+  const int b = row / a.q_heads, hq = row - b * a.q_heads;
   const int gq = a.q_heads / a.kv_heads, h = hq / gq, group = b / a.width;
-  const int len = min(a.seq_lens[b], min(a.max_blocks * 16, a.max_seq_len)), shared = len > 0 ? group_shared(a, group) : 0;
+  const GroupPartials &p0 = a.part[0], &p1 = a.part[1];
+  // the row's place in its pair, and that pair's record
+  const int in0 = (b - group * a.width) * gq + hq - h * gq, in1 = hq - h * gq;
+  const int tile0 = in0 / p0.tile_rows, tile1 = in1 / p1.tile_rows;
+  const int tiles0 = (a.width * gq + p0.tile_rows - 1) / p0.tile_rows, tiles1 = (gq + p1.tile_rows - 1) / p1.tile_rows;
+  const GroupRecord r0 = p0.records[(static_cast<long long>(group) * a.kv_heads + h) * tiles0 + tile0];
+  const GroupRecord r1 = p1.records[(static_cast<long long>(b) * a.kv_heads + h) * tiles1 + tile1];
+  const int len = min(a.seq_lens[b], min(a.max_blocks * 16, a.max_seq_len)), shared = group_shared(a, group);
+  const float v_scale = a.v_scale[a.per_head ? h : 0];
+  // (a pair without tokens has no record)
+  const int n0 = len > 0 && shared > 0 ? r0.parts * p0.fold : 0, n1 = len > 0 && len > shared * 16 ? r1.parts : 0;
+  // partial result i: its place, shared ones first
+  auto part_of = [&](int i, const float*& ml, const float*& o) {
+    const bool first = i < n0;
+    const GroupPartials& p = first ? p0 : p1;
+    const GroupRecord r = first ? r0 : r1;
+    const int fold = first ? p.fold : 1, at = first ? i : i - n0, part = at / fold, f = at - part * fold;
+    const int tile_row = first ? in0 - tile0 * p.tile_rows : in1 - tile1 * p.tile_rows;
+    if (r.parts == 1) {
+      const long long place = static_cast<long long>(f) * a.batch * a.q_heads + row;
+      ml = p.whole_ml + place * 2;
+      o = p.whole_o + place * D;
+    } else {
+      const int slot = part == 0 ? r.slot0 : (r.slot0 & ~1) + 2 * part;
+      const long long place = (static_cast<long long>(slot) * fold + f) * p.tile_rows + tile_row;
+      ml = p.ml + place * 2;
+      o = p.o + place * D;
+    }
+  };
   float acc[V], M = -INFINITY, L = 0.0f;
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.0f;
-#pragma unroll 1
-  for (int kind = 0; kind < 2; ++kind) {
-    if (kind == 0 ? shared <= 0 : len <= shared * 16) continue;
-    const GroupPartials& p = a.part[kind];
-    const int in = kind == 0 ? (b % a.width) * gq + hq % gq : hq % gq;  // row among the pair's
-    const int rows = kind == 0 ? a.width * gq : gq, tiles = (rows + p.tile_rows - 1) / p.tile_rows;
-    const int tile = in / p.tile_rows, tile_row = in % p.tile_rows, lanes = p.tile_rows * p.fold;
-    const GroupRecord rec = p.records[(static_cast<long long>(kind == 0 ? group : b) * a.kv_heads + h) * tiles + tile];
-    const int n = rec.parts * p.fold;
-    auto place = [&](int i) -> long long {  // partial result i
-      const int part = i / p.fold, f = i % p.fold;
-      if (rec.parts == 1) return static_cast<long long>(f) * a.batch * a.q_heads + row;
-      const int slot = part == 0 ? rec.slot0 : (rec.slot0 & ~1) + 2 * part;
-      return static_cast<long long>(slot) * lanes + f * p.tile_rows + tile_row;
-    };
-    const float* ml = rec.parts == 1 ? p.whole_ml : p.ml;
-    const float* po = (rec.parts == 1 ? p.whole_o : p.o) + V * lane;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int i = i0 + lane, here = min(32, n - i0);
-      float2 x = make_float2(-INFINITY, 0.0f);
-      if (i < n) x = *reinterpret_cast<const float2*>(ml + place(i) * 2);
-      // (a part without a maximum has the sum 0, or NaN, which stays)
-      const float Mn = fmaxf(M, warp_max(x.x));
-      const float old = Mn == -INFINITY ? 1.0f : fast_exp2(M - Mn);
-      const float w = Mn == -INFINITY ? 1.0f : fast_exp2(x.x - Mn);
-      L = L * old + warp_sum(x.y * w);
-      M = Mn;
+  const int n = n0 + n1;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int here = min(32, n - i0);
+    float2 x = make_float2(-INFINITY, 0.0f);
+    const float *ml = nullptr, *o = nullptr;
+    if (i0 + lane < n) {
+      part_of(i0 + lane, ml, o);
+      x = *reinterpret_cast<const float2*>(ml);
+    }
+    // (a part without a maximum has the sum 0, or NaN, which stays)
+    const float Mn = fmaxf(M, warp_max(x.x));
+    const float old = Mn == -INFINITY ? 1.0f : fast_exp2(M - Mn);
+    const float w = Mn == -INFINITY ? 1.0f : fast_exp2(x.x - Mn);
+    L = L * old + warp_sum(x.y * w);
+    M = Mn;
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] *= old;
+    for (int e = 0; e < V; ++e) acc[e] *= old;
 #pragma unroll 4
-      for (int q = 0; q < here; ++q) {
-        const float wq = __shfl_sync(0xffffffffu, w, q);
-        const float* o = po + place(i0 + q) * D;
-        float v[V];
-        if constexpr (V == 4) {
-          const float4 y = *reinterpret_cast<const float4*>(o);
-          v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
-        } else {
-          const float2 y = *reinterpret_cast<const float2*>(o);
-          v[0] = y.x, v[1] = y.y;
-        }
-#pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = fmaf(v[e], wq, acc[e]);
+    for (int q = 0; q < here; ++q) {
+      const float wq = __shfl_sync(0xffffffffu, w, q);
+      const float* from = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), q)) + V * lane;
+      float v[V];
+      if constexpr (V == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(from);
+        v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(from);
+        v[0] = y.x, v[1] = y.y;
       }
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = fmaf(v[e], wq, acc[e]);
     }
   }
-  const float f = L == 0.0f ? 0.0f : a.v_scale[a.per_head ? h : 0] / L;
-  const long long at = row * D + V * lane;
+  const float f = L == 0.0f ? 0.0f : v_scale / L;
+  const long long at = static_cast<long long>(row) * D + V * lane;
 #pragma unroll
   for (int e = 0; e < V; e += 2) {
     if (a.out_fp32)
