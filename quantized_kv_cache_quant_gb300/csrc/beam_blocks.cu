@@ -28,23 +28,29 @@ constexpr int kForkWarps = 4;
 
 __global__ void __launch_bounds__(32 * kForkWarps) fork_entries_kernel(const BlocksForkArgs a) {
   extern __shared__ int old_all[];  // [kForkWarps][width][32]
-  __shared__ int parent_s[kBeamMaxWidth], held_s[kBeamMaxWidth], want_s[kBeamMaxWidth];
+  __shared__ int parent_s[kBeamMaxWidth], held_s[kBeamMaxWidth], len_s[kBeamMaxWidth], want_s[kBeamMaxWidth];
   __shared__ int most_s, full_s;
   const int g = blockIdx.x, w = a.width, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     most_s = 0;
     full_s = INT_MAX;
   }
   for (int i = threadIdx.x; i < w; i += blockDim.x) {
-    const int b = g * w + i, p = a.parents[b];
+    const int b = g * w + i;
+    parent_s[i] = a.parents[b];
     held_s[i] = min(max(a.n_held[b], 0), a.max_blocks);
+    len_s[i] = max(a.seq_lens[b], 0);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < w; i += blockDim.x) {
+    const int p = parent_s[i];
     int want = 0;
-    parent_s[i] = -1;
     if (p >= 0 && p < w) {
-      const int held = min(max(a.n_held[g * w + p], 0), a.max_blocks);
-      const long long len = min(static_cast<long long>(max(a.seq_lens[g * w + p], 0)), static_cast<long long>(held) * a.block_tokens);
+      const long long len = min(static_cast<long long>(len_s[p]), static_cast<long long>(held_s[p]) * a.block_tokens);
       want = static_cast<int>((len + a.block_tokens - 1) / a.block_tokens);
-      parent_s[i] = p;
+    } else {
+      parent_s[i] = -1;  // (read by this thread alone until the barrier)
     }
     want_s[i] = want;
   }
@@ -99,7 +105,9 @@ __global__ void __launch_bounds__(32 * kForkWarps) fork_entries_kernel(const Blo
 //   A = blocks free after the push; freed block number e (ascending) of n goes
 //   to place count + n - 1 - e, copy r takes place A - 1 - r.
 // Every block of the cluster counts its part of the bits; the first one knows
-// the sequences.
+// the sequences. It starts while the first launch runs and reads the sequences'
+// lengths meanwhile; what that launch writes (entries, counts, bits) it reads
+// after it.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(1024) fork_tails_kernel(const BlocksForkArgs a) {
   extern __shared__ int sm[];
@@ -111,24 +119,47 @@ __global__ void __launch_bounds__(1024) fork_tails_kernel(const BlocksForkArgs a
   const int words = (a.num_blocks + 31) / 32;
   const int per = (words + ranks - 1) / ranks, w0 = min(words, rank * per), w1 = min(words, w0 + per);
   const int count = min(max(*a.free_count, 0), a.num_blocks);
+  if (rank == 0) {
+    for (int b = threadIdx.x; b < a.batch; b += blockDim.x) {
+      const int first = b / a.width * a.width, p = a.parents[b];
+      int len = 0;
+      if (p >= 0 && p < a.width) {
+        const int held = min(max(a.n_held[first + p], 0), a.max_blocks);
+        len = static_cast<int>(min(static_cast<long long>(max(a.seq_lens[first + p], 0)), static_cast<long long>(held) * a.block_tokens));
+      }
+      len_s[b] = len;
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // the freed blocks of this part
+  // the last blocks (each thread's own lengths), and the freed blocks of this part
+  if (rank == 0) {
+    for (int b = threadIdx.x; b < a.batch; b += blockDim.x) {
+      const int len = len_s[b], column = len / a.block_tokens;
+      int tail = -1;
+      if (len != column * a.block_tokens) tail = __ldcg(a.block_table + static_cast<long long>(b) * a.max_blocks + column);
+      tail_s[b] = tail >= 0 && tail < a.num_blocks ? tail : -1;
+    }
+  }
   unsigned long long mine = 0, ignore;
-  for (int i = w0 + threadIdx.x; i < w1; i += blockDim.x) mine += __popc(a.bits[i]);
+  for (int i = w0 + threadIdx.x; i < w1; i += blockDim.x) mine += __popc(__ldcg(a.bits + i));
   (void)block_scan(mine, scan_ws, ignore);
-  if (threadIdx.x == 0) freed_s = ignore;
-  cluster.sync();
-  long long before = 0, freed = 0;
-  for (int r = 0; r < ranks; ++r) {
-    const long long n = static_cast<long long>(*cluster.map_shared_rank(&freed_s, r));
-    if (r < rank) before += n;
-    freed += n;
+  long long before = 0, freed = static_cast<long long>(ignore);
+  if (ranks > 1) {
+    if (threadIdx.x == 0) freed_s = ignore;
+    cluster.sync();
+    freed = 0;
+    for (int r = 0; r < ranks; ++r) {
+      const long long n = static_cast<long long>(*cluster.map_shared_rank(&freed_s, r));
+      if (r < rank) before += n;
+      freed += n;
+    }
   }
   const int top = static_cast<int>(min(count + freed, static_cast<long long>(a.num_blocks)));
   if (freed > 0) {
     for (int i0 = w0; i0 < w1; i0 += blockDim.x) {
       const int i = i0 + threadIdx.x;
-      uint32_t word = i < w1 ? a.bits[i] : 0u;
+      uint32_t word = i < w1 ? __ldcg(a.bits + i) : 0u;
       __syncthreads();
       unsigned long long total;
       long long e = before + static_cast<long long>(block_scan(__popc(word), scan_ws, total));
@@ -140,21 +171,8 @@ __global__ void __launch_bounds__(1024) fork_tails_kernel(const BlocksForkArgs a
       }
     }
   }
-  if (rank == 0) {
-    for (int b = threadIdx.x; b < a.batch; b += blockDim.x) {
-      const int g = b / a.width, p = a.parents[b];
-      int tail = -1;
-      long long len = 0;
-      if (p >= 0 && p < a.width) {
-        const int held = min(max(a.n_held[g * a.width + p], 0), a.max_blocks);
-        len = min(static_cast<long long>(max(a.seq_lens[g * a.width + p], 0)), static_cast<long long>(held) * a.block_tokens);
-        if (len % a.block_tokens != 0) tail = a.block_table[static_cast<long long>(b) * a.max_blocks + len / a.block_tokens];
-      }
-      len_s[b] = static_cast<int>(min(len, static_cast<long long>(INT_MAX)));
-      tail_s[b] = tail >= 0 && tail < a.num_blocks ? tail : -1;
-    }
-  }
-  cluster.sync();  // the pushes are done, nobody reads n_held or seq_lens any more
+  if (ranks > 1) cluster.sync();  // the pushes are done, nobody reads another block's count any more
+  else __syncthreads();
   if (rank != 0) return;
   int copies = 0;  // of the sequences before
   for (int b0 = 0; b0 < a.batch; b0 += blockDim.x) {
@@ -162,6 +180,7 @@ __global__ void __launch_bounds__(1024) fork_tails_kernel(const BlocksForkArgs a
     bool copier = false;
     int tail = -1;
     if (b < a.batch && (tail = tail_s[b]) >= 0) {
+      const int shares = __ldcg(a.shares + tail);
       const int first = b / a.width * a.width;
       int among = 0;
       bool earlier = false;
@@ -169,24 +188,22 @@ __global__ void __launch_bounds__(1024) fork_tails_kernel(const BlocksForkArgs a
         among += tail_s[i] == tail;
         earlier |= tail_s[i] == tail && i < b;
       }
-      copier = earlier || __ldcg(a.shares + tail) + 1 != among;
+      copier = earlier || shares + 1 != among;
     }
     unsigned long long total;
     const int r = copies + static_cast<int>(block_scan(copier ? 1ull : 0ull, scan_ws, total));
     copies += static_cast<int>(total);
-    __syncthreads();  // all counts of this round are read (a request may lie in two rounds: see below)
     if (b < a.batch) {
-      const long long len = len_s[b];
-      const int held = static_cast<int>((len + a.block_tokens - 1) / a.block_tokens);
+      const int len = len_s[b];
       const bool made = copier && r < top;
       if (made) {
         const int fresh = __ldcg(a.free_blocks + (top - 1 - r));
-        a.block_table[static_cast<long long>(b) * a.max_blocks + held - 1] = fresh;
+        a.block_table[static_cast<long long>(b) * a.max_blocks + len / a.block_tokens] = fresh;
         a.copy_src[r] = tail;
         a.copy_dst[r] = fresh;
       }
-      // the old block's count falls once all sequences have looked at it
-      len_s[b] = made ? -1 - static_cast<int>(len) : static_cast<int>(len);
+      // the old block's count falls once all sequences have looked at it: a copy is marked in its length
+      if (made) len_s[b] = -1 - len;
       if (a.granted != nullptr) a.granted[b] = !copier || made;
     }
     __syncthreads();
@@ -196,18 +213,18 @@ __global__ void __launch_bounds__(1024) fork_tails_kernel(const BlocksForkArgs a
     if (len < 0) {
       len = -1 - len;
       atomicSub(a.shares + tail_s[b], 1);
+      len_s[b] = len;
     }
-    len_s[b] = len;
     a.seq_lens[b] = len;
     a.n_held[b] = static_cast<int>((static_cast<long long>(len) + a.block_tokens - 1) / a.block_tokens);
   }
   __syncthreads();
   for (int g = threadIdx.x; g < a.batch / a.width; g += blockDim.x) {
+    const int alike = __ldcg(a.alike + g);
     int full = INT_MAX;
     for (int i = 0; i < a.width; ++i)
       if (len_s[g * a.width + i] > 0) full = min(full, len_s[g * a.width + i] / a.block_tokens);
-    const int alike = a.alike[g];
-    a.alike[g] = 0;
+    if (alike != 0) a.alike[g] = 0;
     if (a.shared_blocks != nullptr)
       a.shared_blocks[g] = full == INT_MAX ? 0 : min(full, alike == 0 ? a.max_blocks : a.max_blocks - alike);
   }
@@ -277,46 +294,59 @@ __device__ __forceinline__ uint32_t mover_bits(const BlocksCompactArgs& a, int i
 __device__ __forceinline__ int mover_rank(const BlocksCompactArgs& a, int x, uint32_t word) {
   const int i = x >> 5;
   // (the word that keep cuts counts the targets before it; it is the first with movers)
-  return (i > a.keep >> 5 ? a.before[i] : 0) + __popc(mover_bits(a, i, word) & ((1u << (x & 31)) - 1u));
+  return (i > a.keep >> 5 ? __ldcg(a.before + i) : 0) + __popc(mover_bits(a, i, word) & ((1u << (x & 31)) - 1u));
 }
 
-__global__ void __launch_bounds__(kCompactThreads) compact_mark_kernel(const BlocksCompactArgs a) {
+// The four passes, by thread `me` of `threads`.
+__device__ __forceinline__ void compact_mark(const BlocksCompactArgs& a, long long me, long long threads) {
   const int count = min(max(*a.free_count, 0), a.num_blocks);
-  for (long long i = static_cast<long long>(blockIdx.x) * kCompactThreads + threadIdx.x; i < count;
-       i += static_cast<long long>(gridDim.x) * kCompactThreads) {
+  for (long long i = me; i < count; i += threads) {
     const int x = a.free_blocks[i];
     if (x >= 0 && x < a.num_blocks) atomicOr(a.bits + (x >> 5), 1u << (x & 31));
   }
 }
 
-__global__ void __launch_bounds__(1024) compact_rank_kernel(const BlocksCompactArgs a) {
-  __shared__ unsigned long long scan_ws[32], sums_s;
+// By a cluster: each block ranks its part of the words.
+__device__ __forceinline__ void compact_rank(const BlocksCompactArgs& a, unsigned long long* scan_ws, unsigned long long* sums) {
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
   const int words = (a.num_blocks + 31) / 32, cut = a.keep >> 5;
-  const int per = (words + ranks - 1) / ranks, w0 = min(words, rank * per), w1 = min(words, w0 + per);
+  const int per = ((words + ranks - 1) / ranks + 3) & ~3, w0 = min(words, rank * per), w1 = min(words, w0 + per);
   // low half: targets, high half: movers
-  auto both = [&](int i) -> unsigned long long {
-    const uint32_t word = a.bits[i];
+  auto both = [&](int i, uint32_t word) -> unsigned long long {
     return static_cast<unsigned long long>(__popc(target_bits(a, i, word))) |
            (static_cast<unsigned long long>(__popc(mover_bits(a, i, word))) << 32);
   };
-  unsigned long long mine = 0, total;
-  for (int i = w0 + threadIdx.x; i < w1; i += blockDim.x) mine += both(i);
+  // a thread's four words from i on (the bits' memory is a multiple of 256 bytes), and their counts
+  auto four = [&](int i, unsigned long long (&n)[4]) -> unsigned long long {
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (i < w1) w = __ldcg(reinterpret_cast<const uint4*>(a.bits + i));
+    const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) n[e] = i + e < w1 ? both(i + e, word[e]) : 0ull;
+    return (n[0] + n[1]) + (n[2] + n[3]);
+  };
+  unsigned long long mine = 0, total, n[4];
+  for (int i = w0 + 4 * threadIdx.x; i < w1; i += 4 * blockDim.x) mine += four(i, n);
   (void)block_scan(mine, scan_ws, total);
-  if (threadIdx.x == 0) sums_s = total;
+  if (threadIdx.x == 0) *sums = total;
   cluster.sync();
   unsigned long long before = 0, all = 0;
   for (int r = 0; r < ranks; ++r) {
-    const unsigned long long n = *cluster.map_shared_rank(&sums_s, r);
+    const unsigned long long n = *cluster.map_shared_rank(sums, r);
     if (r < rank) before += n;
     all += n;
   }
-  for (int i0 = w0; i0 < w1; i0 += blockDim.x) {
-    const int i = i0 + threadIdx.x;
+  for (int i0 = w0; i0 < w1; i0 += 4 * blockDim.x) {
+    const int i = i0 + 4 * threadIdx.x;
     __syncthreads();
-    const unsigned long long at = before + block_scan(i < w1 ? both(i) : 0ull, scan_ws, total);
-    if (i < w1) a.before[i] = static_cast<int32_t>(i <= cut ? at & 0xffffffffu : at >> 32);
+    const unsigned long long sum = four(i, n);
+    unsigned long long at = before + block_scan(sum, scan_ws, total);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (i + e < w1) a.before[i + e] = static_cast<int32_t>(i + e <= cut ? at & 0xffffffffu : at >> 32);
+      at += n[e];
+    }
     before += total;
   }
   if (rank == 0 && threadIdx.x == 0) {
@@ -332,39 +362,44 @@ __global__ void __launch_bounds__(1024) compact_rank_kernel(const BlocksCompactA
   cluster.sync();  // (no block ends while another reads its sums)
 }
 
-__global__ void __launch_bounds__(kCompactThreads) compact_lists_kernel(const BlocksCompactArgs a) {
-  const CompactState st = *a.state;
-  if (!st.done) return;
+__device__ __forceinline__ void compact_lists(const BlocksCompactArgs& a, long long me, long long threads) {
+  const int movers = __ldcg(&a.state->movers), targets = __ldcg(&a.state->targets);
+  if (__ldcg(&a.state->done) == 0) return;
   const int lane = threadIdx.x & 31, words = (a.num_blocks + 31) / 32;
   const uint32_t below = (1u << lane) - 1u;
-  for (int i = (blockIdx.x * kCompactThreads + threadIdx.x) >> 5; i < words; i += gridDim.x * (kCompactThreads / 32)) {
-    const uint32_t word = a.bits[i], targets = target_bits(a, i, word), movers = mover_bits(a, i, word);
-    const int x = 32 * i + lane;
-    if (targets >> lane & 1u) {
-      const int r = a.before[i] + __popc(targets & below);
-      if (r < st.movers) a.copy_dst[r] = x;
-      else a.free_blocks[st.targets - 1 - r] = x;
+  for (long long i = me >> 5; i < words; i += threads >> 5) {
+    const uint32_t word = __ldcg(a.bits + i), to = target_bits(a, i, word), from = mover_bits(a, i, word);
+    const int x = 32 * static_cast<int>(i) + lane;
+    if (to >> lane & 1u) {
+      const int r = __ldcg(a.before + i) + __popc(to & below);
+      if (r < movers) a.copy_dst[r] = x;
+      else a.free_blocks[targets - 1 - r] = x;
     }
-    if (movers >> lane & 1u) a.copy_src[mover_rank(a, x, word)] = x;
+    if (from >> lane & 1u) a.copy_src[mover_rank(a, x, word)] = x;
   }
 }
 
-__global__ void __launch_bounds__(kCompactThreads) compact_follow_kernel(const BlocksCompactArgs a) {
-  const bool done = a.state->done != 0;
-  const long long me = static_cast<long long>(blockIdx.x) * kCompactThreads + threadIdx.x;
-  const long long threads = static_cast<long long>(gridDim.x) * kCompactThreads;
+__device__ __forceinline__ void compact_follow(const BlocksCompactArgs& a, long long me, long long threads) {
+  const bool done = __ldcg(&a.state->done) != 0;
   // where block x is now
   auto now = [&](int x) -> int {
     if (!done || x < a.keep) return x;
-    const uint32_t word = a.bits[x >> 5];
-    return word >> (x & 31) & 1u ? x : a.copy_dst[mover_rank(a, x, word)];
+    const uint32_t word = __ldcg(a.bits + (x >> 5));
+    return word >> (x & 31) & 1u ? x : __ldcg(a.copy_dst + mover_rank(a, x, word));
   };
-  for (long long x = me; x < a.num_blocks; x += threads) {
-    const int to = now(static_cast<int>(x));
-    a.moved_to[x] = to;
-    if (to != x) {
-      a.shares[to] = a.shares[x];
-      a.shares[x] = 0;
+  for (long long x0 = me; x0 < a.num_blocks; x0 += 4 * threads) {
+    int to[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) to[e] = x0 + e * threads < a.num_blocks ? now(static_cast<int>(x0 + e * threads)) : 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const long long x = x0 + e * threads;
+      if (x >= a.num_blocks) break;
+      a.moved_to[x] = to[e];
+      if (to[e] != x) {
+        a.shares[to[e]] = a.shares[x];
+        a.shares[x] = 0;
+      }
     }
   }
   if (!done) return;
@@ -373,17 +408,61 @@ __global__ void __launch_bounds__(kCompactThreads) compact_follow_kernel(const B
   for (long long item = me >> 5; item < static_cast<long long>(a.batch) * chunks; item += threads >> 5) {
     const int b = static_cast<int>(item / chunks), c0 = static_cast<int>(item % chunks) * 128;
     const int held = min(max(a.n_held[b], 0), a.max_blocks);
+    if (c0 >= held) continue;
     int32_t* row = a.block_table + static_cast<long long>(b) * a.max_blocks;
-    int x[4];
+    int x[4], to[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = c0 + 32 * e + lane < held ? row[c0 + 32 * e + lane] : -1;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (x[e] < a.keep || x[e] >= a.num_blocks) continue;
-      const int to = now(x[e]);
-      if (to != x[e]) row[c0 + 32 * e + lane] = to;
-    }
+    for (int e = 0; e < 4; ++e) to[e] = x[e] >= a.keep && x[e] < a.num_blocks ? now(x[e]) : x[e];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (to[e] != x[e]) row[c0 + 32 * e + lane] = to[e];
   }
+}
+
+// Each launch but the last lets the next one in at once, which waits for it.
+__device__ __forceinline__ void compact_begin() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ long long grid_thread() { return static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; }
+__device__ __forceinline__ long long grid_threads() { return static_cast<long long>(gridDim.x) * blockDim.x; }
+
+__global__ void __launch_bounds__(kCompactThreads) compact_clear_kernel(const BlocksCompactArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (long long i = grid_thread(); i < (a.num_blocks + 31) / 32; i += grid_threads()) a.bits[i] = 0u;
+}
+__global__ void __launch_bounds__(kCompactThreads) compact_mark_kernel(const BlocksCompactArgs a) {
+  compact_begin();
+  compact_mark(a, grid_thread(), grid_threads());
+}
+__global__ void __launch_bounds__(1024) compact_rank_kernel(const BlocksCompactArgs a) {
+  __shared__ unsigned long long scan_ws[32], sums_s;
+  compact_begin();
+  compact_rank(a, scan_ws, &sums_s);
+}
+__global__ void __launch_bounds__(kCompactThreads) compact_lists_kernel(const BlocksCompactArgs a) {
+  compact_begin();
+  compact_lists(a, grid_thread(), grid_threads());
+}
+__global__ void __launch_bounds__(kCompactThreads) compact_follow_kernel(const BlocksCompactArgs a) {
+  // (the last launch: what comes behind it may read the tables before it waits, so it is not let in early)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  compact_follow(a, grid_thread(), grid_threads());
+}
+// Small pools: all of it in one cluster. (Every launch of five costs some 2 to 3 us: 4096 blocks in 19 us.)
+__global__ void __launch_bounds__(1024) compact_cluster_kernel(const BlocksCompactArgs a) {
+  __shared__ unsigned long long scan_ws[32], sums_s;
+  cg::cluster_group cluster = cg::this_cluster();
+  for (long long i = grid_thread(); i < (a.num_blocks + 31) / 32; i += grid_threads()) a.bits[i] = 0u;
+  cluster.sync();
+  compact_mark(a, grid_thread(), grid_threads());
+  cluster.sync();
+  compact_rank(a, scan_ws, &sums_s);
+  compact_lists(a, grid_thread(), grid_threads());
+  cluster.sync();
+  compact_follow(a, grid_thread(), grid_threads());
 }
 
 int blocks_for(long long items, int per_block, int per_sm) {
@@ -391,20 +470,29 @@ int blocks_for(long long items, int per_block, int per_sm) {
   return static_cast<int>(want < 1 ? 1 : want < full ? want : full);
 }
 
-// One cluster of `ranks` blocks (8 is the portable most).
+// One cluster of `ranks` blocks (8 is the portable most); ranks 0: `blocks` blocks without clusters. `early`: it may start
+// while the launch before runs, for which it waits itself.
 template <class Args>
-cudaError_t launch_cluster(void (*kern)(Args), const Args& a, int ranks, int threads, int smem, cudaStream_t s) {
+cudaError_t launch(void (*kern)(Args), const Args& a, int ranks, int blocks, int threads, int smem, bool early, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = ranks;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.gridDim = dim3(ranks);
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = dim3(ranks > 0 ? ranks : blocks);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 0;
+  if (ranks > 0) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = ranks;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (early) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -421,7 +509,7 @@ cudaError_t launch_blocks_fork(const BlocksForkArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int words = (a.num_blocks + 31) / 32;
   static_assert(2 * kSpecMaxBatch * sizeof(int) <= 48 * 1024, "no more shared memory than a kernel has without asking");
-  return launch_cluster(fork_tails_kernel, a, words <= 4096 ? 1 : 8, 1024, 2 * a.batch * static_cast<int>(sizeof(int)), s);
+  return launch(fork_tails_kernel, a, words <= 4096 ? 1 : 8, 0, 1024, 2 * a.batch * static_cast<int>(sizeof(int)), true, s);
 }
 
 cudaError_t launch_blocks_copy(const BlocksCopyArgs& a, cudaStream_t s) {
@@ -432,16 +520,16 @@ cudaError_t launch_blocks_copy(const BlocksCopyArgs& a, cudaStream_t s) {
 
 cudaError_t launch_blocks_compact(const BlocksCompactArgs& a, cudaStream_t s) {
   const int words = (a.num_blocks + 31) / 32;
-  cudaError_t e = cudaMemsetAsync(a.bits, 0, static_cast<size_t>(words) * sizeof(uint32_t), s);
-  if (e != cudaSuccess) return e;
-  compact_mark_kernel<<<blocks_for(a.num_blocks, 4 * kCompactThreads, 8), kCompactThreads, 0, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if ((e = launch_cluster(compact_rank_kernel, a, words <= 4096 ? 1 : 8, 1024, 0, s)) != cudaSuccess) return e;
-  compact_lists_kernel<<<blocks_for(words, 2 * kCompactThreads / 32, 8), kCompactThreads, 0, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const long long entries = static_cast<long long>(a.batch) * a.max_blocks;
-  compact_follow_kernel<<<blocks_for(entries > a.num_blocks ? entries : a.num_blocks, 4 * kCompactThreads, 8), kCompactThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  if (a.num_blocks <= 65536 && entries <= 65536) return launch(compact_cluster_kernel, a, 8, 0, 1024, 0, false, s);
+  auto grid = [&](long long items, int per_thread) { return blocks_for(items, per_thread * kCompactThreads, 8); };
+  cudaError_t e = launch(compact_clear_kernel, a, 0, grid(words, 1), kCompactThreads, 0, false, s);
+  if (e == cudaSuccess) e = launch(compact_mark_kernel, a, 0, grid(a.num_blocks, 4), kCompactThreads, 0, true, s);
+  if (e == cudaSuccess) e = launch(compact_rank_kernel, a, words <= 4096 ? 1 : 8, 0, 1024, 0, true, s);
+  if (e == cudaSuccess) e = launch(compact_lists_kernel, a, 0, grid(32ll * words, 2), kCompactThreads, 0, true, s);
+  if (e == cudaSuccess)
+    e = launch(compact_follow_kernel, a, 0, grid(entries > a.num_blocks ? entries : a.num_blocks, 4), kCompactThreads, 0, true, s);
+  return e;
 }
 
 }  // namespace kvq
