@@ -290,11 +290,17 @@ __device__ __forceinline__ uint32_t target_bits(const BlocksCompactArgs& a, int 
 __device__ __forceinline__ uint32_t mover_bits(const BlocksCompactArgs& a, int i, uint32_t word) {
   return ~word & low_bits(a.num_blocks - 32 * i) & ~low_bits(a.keep - 32 * i);
 }
+// What a pass of the same launch has written is read past L1 (SAME), that of a launch before through it.
+template <bool SAME, class T>
+__device__ __forceinline__ T passed(const T* p) {
+  return SAME ? __ldcg(p) : *p;
+}
 // Rank of mover x among the movers.
+template <bool SAME>
 __device__ __forceinline__ int mover_rank(const BlocksCompactArgs& a, int x, uint32_t word) {
   const int i = x >> 5;
   // (the word that keep cuts counts the targets before it; it is the first with movers)
-  return (i > a.keep >> 5 ? __ldcg(a.before + i) : 0) + __popc(mover_bits(a, i, word) & ((1u << (x & 31)) - 1u));
+  return (i > a.keep >> 5 ? passed<SAME>(a.before + i) : 0) + __popc(mover_bits(a, i, word) & ((1u << (x & 31)) - 1u));
 }
 
 // The four passes, by thread `me` of `threads`.
@@ -362,44 +368,39 @@ __device__ __forceinline__ void compact_rank(const BlocksCompactArgs& a, unsigne
   cluster.sync();  // (no block ends while another reads its sums)
 }
 
+template <bool SAME>
 __device__ __forceinline__ void compact_lists(const BlocksCompactArgs& a, long long me, long long threads) {
-  const int movers = __ldcg(&a.state->movers), targets = __ldcg(&a.state->targets);
-  if (__ldcg(&a.state->done) == 0) return;
+  const int movers = passed<SAME>(&a.state->movers), targets = passed<SAME>(&a.state->targets);
+  if (passed<SAME>(&a.state->done) == 0) return;
   const int lane = threadIdx.x & 31, words = (a.num_blocks + 31) / 32;
   const uint32_t below = (1u << lane) - 1u;
   for (long long i = me >> 5; i < words; i += threads >> 5) {
-    const uint32_t word = __ldcg(a.bits + i), to = target_bits(a, i, word), from = mover_bits(a, i, word);
+    const uint32_t word = passed<SAME>(a.bits + i), to = target_bits(a, i, word), from = mover_bits(a, i, word);
     const int x = 32 * static_cast<int>(i) + lane;
     if (to >> lane & 1u) {
-      const int r = __ldcg(a.before + i) + __popc(to & below);
+      const int r = passed<SAME>(a.before + i) + __popc(to & below);
       if (r < movers) a.copy_dst[r] = x;
       else a.free_blocks[targets - 1 - r] = x;
     }
-    if (from >> lane & 1u) a.copy_src[mover_rank(a, x, word)] = x;
+    if (from >> lane & 1u) a.copy_src[mover_rank<SAME>(a, x, word)] = x;
   }
 }
 
+template <bool SAME>
 __device__ __forceinline__ void compact_follow(const BlocksCompactArgs& a, long long me, long long threads) {
-  const bool done = __ldcg(&a.state->done) != 0;
+  const bool done = passed<SAME>(&a.state->done) != 0;
   // where block x is now
   auto now = [&](int x) -> int {
     if (!done || x < a.keep) return x;
-    const uint32_t word = __ldcg(a.bits + (x >> 5));
-    return word >> (x & 31) & 1u ? x : __ldcg(a.copy_dst + mover_rank(a, x, word));
+    const uint32_t word = passed<SAME>(a.bits + (x >> 5));
+    return word >> (x & 31) & 1u ? x : passed<SAME>(a.copy_dst + mover_rank<SAME>(a, x, word));
   };
-  for (long long x0 = me; x0 < a.num_blocks; x0 += 4 * threads) {
-    int to[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) to[e] = x0 + e * threads < a.num_blocks ? now(static_cast<int>(x0 + e * threads)) : 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const long long x = x0 + e * threads;
-      if (x >= a.num_blocks) break;
-      a.moved_to[x] = to[e];
-      if (to[e] != x) {
-        a.shares[to[e]] = a.shares[x];
-        a.shares[x] = 0;
-      }
+  for (long long x = me; x < a.num_blocks; x += threads) {
+    const int to = now(static_cast<int>(x));
+    a.moved_to[x] = to;
+    if (to != x) {
+      a.shares[to] = a.shares[x];
+      a.shares[x] = 0;
     }
   }
   if (!done) return;
@@ -444,12 +445,12 @@ __global__ void __launch_bounds__(1024) compact_rank_kernel(const BlocksCompactA
 }
 __global__ void __launch_bounds__(kCompactThreads) compact_lists_kernel(const BlocksCompactArgs a) {
   compact_begin();
-  compact_lists(a, grid_thread(), grid_threads());
+  compact_lists<false>(a, grid_thread(), grid_threads());
 }
 __global__ void __launch_bounds__(kCompactThreads) compact_follow_kernel(const BlocksCompactArgs a) {
   // (the last launch: what comes behind it may read the tables before it waits, so it is not let in early)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  compact_follow(a, grid_thread(), grid_threads());
+  compact_follow<false>(a, grid_thread(), grid_threads());
 }
 // Small pools: all of it in one cluster. (Every launch of five costs some 2 to 3 us: 4096 blocks in 19 us.)
 __global__ void __launch_bounds__(1024) compact_cluster_kernel(const BlocksCompactArgs a) {
@@ -460,9 +461,9 @@ __global__ void __launch_bounds__(1024) compact_cluster_kernel(const BlocksCompa
   compact_mark(a, grid_thread(), grid_threads());
   cluster.sync();
   compact_rank(a, scan_ws, &sums_s);
-  compact_lists(a, grid_thread(), grid_threads());
+  compact_lists<true>(a, grid_thread(), grid_threads());
   cluster.sync();
-  compact_follow(a, grid_thread(), grid_threads());
+  compact_follow<true>(a, grid_thread(), grid_threads());
 }
 
 int blocks_for(long long items, int per_block, int per_sm) {
