@@ -20,10 +20,11 @@
  * Sequences come in groups of `width`: sequence b belongs to request b / width,
  * and a request with fewer continuations leaves the others empty (length 0).
  * Several table entries may name one block. shares[block], device int32
- * [num_blocks], counts the references beyond the first: 0 for a free block and for one
- * that a single entry names, so that blocks which kv_blocks_resize grants need
- * no care (and a resize that shrinks has to give up unshared blocks only). A
- * holder outside the tables, such as a prefix cache, counts itself in shares.
+ * [num_blocks], counts the references beyond the first: 0 for a free block and
+ * for one that a single entry names, so that blocks which kv_blocks_resize
+ * grants need no care (and a resize that shrinks has to give up unshared blocks
+ * only). A holder outside the tables, such as a prefix cache, counts itself in
+ * shares.
  */
 #ifndef KVQ_BEAM_H_
 #define KVQ_BEAM_H_
@@ -62,10 +63,12 @@ extern "C" {
  *   out_parents : device int32 [groups, n_out], i, the beam within its request
  *   out_tokens  : device int32 [groups, n_out], t
  * A NaN logit counts as -inf and +inf as the largest float32; a token at -inf
- * scores -inf, and candidates at -inf fill up what finite ones leave, by their index. Candidates of one beam
- * are ordered by their logits. Sums are float32 within a thread (at most some
- * hundred terms a partial sum, each relative to the maximum) and float64 beyond; scores are compared in
- * float64 and rounded once.
+ * scores -inf, and candidates at -inf fill up what finite ones leave, by their
+ * index. Candidates of one beam are ordered by their logits. Sums are float32
+ * within a thread (some hundred terms, relative to the thread's maximum) and
+ * whole numbers beyond; the logarithm of a sum is off by some 2^-23. Scores are
+ * compared in float64 and rounded once. A row gives the same wherever it starts,
+ * and the same call the same bits.
  * One launch. KVQ_ERR_UNSUPPORTED for width > KVQ_BEAM_MAX_WIDTH or n_out >
  * KVQ_BEAM_MAX_OUT, KVQ_ERR_ARG for n_out > vocab. */
 KVQ_API kvq_status beam_select(const void* logits, int32_t logits_type, int64_t row_stride, const float* scores,
@@ -146,7 +149,8 @@ KVQ_API kvq_status kv_blocks_copy(const kvq_block_buffer* buffers, int32_t n_buf
  *   done          : device int32 [1]: 1, or 0 where the free blocks below or
  *                   max_copies do not suffice: then nothing changes (copy_count
  *                   0, moved_to the identity)
- * To be followed by kv_blocks_copy in every pool. keep_blocks in [0, num_blocks]. */
+ * To be followed by kv_blocks_copy in every pool. keep_blocks in [0, num_blocks].
+ * (A pool that grows again gets its upper blocks back by pushing their numbers.) */
 KVQ_API kvq_status kv_blocks_compact(int32_t* block_table, int32_t batch, int32_t max_blocks, const int32_t* n_held,
                                      int32_t keep_blocks, int32_t* shares, int32_t* free_blocks, int32_t* free_count,
                                      int32_t num_blocks, int32_t* moved_to, int32_t* copy_src, int32_t* copy_dst,
@@ -189,8 +193,8 @@ KVQ_API size_t fp8_group_workspace_bytes(int32_t batch, int32_t width, int32_t k
  * kv_heads) > 16 in one (2^-11 relative, as the output itself). Scores, sums and
  * outputs accumulate in fp32. The same call gives the same bits.
  * KVQ_ERR_UNSUPPORTED for batch > KVQ_SPEC_MAX_BATCH, width >
- * KVQ_BEAM_MAX_WIDTH or q_heads / kv_heads > KVQ_TREE_MAX_GQA; KVQ_ERR_SHAPE for
- * batch % width != 0. */
+ * KVQ_BEAM_MAX_WIDTH, q_heads / kv_heads > KVQ_TREE_MAX_GQA or batch * q_heads >=
+ * 2^31; KVQ_ERR_SHAPE for batch % width != 0. */
 KVQ_API kvq_status fp8_group_attention(const uint16_t* q, int64_t q_row_stride, const fp8_pool* k, const fp8_pool* v,
                                        const int32_t* block_table, const int32_t* seq_lens,
                                        const int32_t* shared_blocks, int32_t batch, int32_t width, int32_t q_heads,

@@ -214,7 +214,8 @@ kvq_status kv_blocks_compact(int32_t* block_table, int32_t batch, int32_t max_bl
 size_t fp8_group_workspace_bytes(int32_t batch, int32_t width, int32_t kv_heads, int32_t q_heads, int32_t head_dim) {
   if (batch <= 0 || batch > KVQ_SPEC_MAX_BATCH || width <= 0 || width > KVQ_BEAM_MAX_WIDTH || batch % width != 0 ||
       kv_heads <= 0 || kv_heads > 65535 || q_heads <= 0 || q_heads % kv_heads != 0 ||
-      q_heads / kv_heads > KVQ_TREE_MAX_GQA || (head_dim != 64 && head_dim != 128))
+      q_heads / kv_heads > KVQ_TREE_MAX_GQA || static_cast<long long>(batch) * q_heads > INT_MAX ||
+      (head_dim != 64 && head_dim != 128))
     return 0;
   return group_layout(batch, width, kv_heads, q_heads, head_dim).bytes;
 }
@@ -230,7 +231,7 @@ kvq_status fp8_group_attention(const uint16_t* q, int64_t q_row_stride, const fp
   const int kv_heads = k->kv_heads, head_dim = k->head_dim;
   if (batch > KVQ_SPEC_MAX_BATCH || width > KVQ_BEAM_MAX_WIDTH) return KVQ_ERR_UNSUPPORTED;
   if (batch % width != 0 || q_heads % kv_heads != 0) return KVQ_ERR_SHAPE;
-  if (q_heads / kv_heads > KVQ_TREE_MAX_GQA) return KVQ_ERR_UNSUPPORTED;
+  if (q_heads / kv_heads > KVQ_TREE_MAX_GQA || static_cast<long long>(batch) * q_heads > INT_MAX) return KVQ_ERR_UNSUPPORTED;
   if (q_row_stride < static_cast<int64_t>(q_heads) * head_dim || q_row_stride % 8 != 0) return KVQ_ERR_ARG;
   if (max_blocks > INT_MAX / 16) return KVQ_ERR_UNSUPPORTED;
   if (max_seq_len > max_blocks * 16) return KVQ_ERR_CAPACITY;

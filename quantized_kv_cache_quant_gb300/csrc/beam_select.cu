@@ -606,11 +606,11 @@ struct SelectPlan {
 
 // Blocks of a cluster (up to 16: one request is one cluster), as many as have room at once, and parts of a row, so that
 // the block with the most to do has little of it; a part costs what `fixed` bytes of logits do beside its own.
-SelectPlan plan_select(const BeamSelectArgs& a, int size) {
+SelectPlan plan_select(const BeamSelectArgs& a, int size, int most_ranks) {
   SelectPlan best{1, 1, 0};
   const long long fixed = 16384;
   int ranks = 1;
-  while (ranks < 16 && static_cast<long long>(a.groups) * ranks * 2 <= 4ll * device_sm_count()) ranks *= 2;
+  while (ranks < most_ranks && static_cast<long long>(a.groups) * ranks * 2 <= 4ll * device_sm_count()) ranks *= 2;
   long long best_cost = LLONG_MAX;
   for (int splits = 1; splits <= 32 && a.width * splits <= kMaxParts; ++splits) {
     const int parts = a.width * splits;
@@ -631,20 +631,35 @@ cudaError_t launch_select(const BeamSelectArgs& a, cudaStream_t s) {
   static SharedMemoryOnce once;
   cudaError_t e = once.set(kern, kMostShared);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
-  const SelectPlan p = plan_select(a, Logits<TYPE>::SIZE);
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = p.ranks;
+  attr.val.clusterDim.x = 16;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(a.groups) * p.ranks);
+  cfg.gridDim = dim3(16);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = p.smem;
+  cfg.dynamicSmemBytes = kMostShared;
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  // clusters of 16 blocks, asked for once per device: 1 they fit, -1 they do not (8 are the portable most)
+  static std::atomic<int> fits[SharedMemoryOnce::kDevices] = {};
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int f = dev < SharedMemoryOnce::kDevices ? fits[dev].load(std::memory_order_relaxed) : 0;
+  if (f == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    int clusters = 0;
+    f = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) == cudaSuccess && clusters > 0 ? 1 : -1;
+    if (f < 0) (void)cudaGetLastError();
+    if (dev < SharedMemoryOnce::kDevices) fits[dev].store(f, std::memory_order_relaxed);
+  }
+  const SelectPlan p = plan_select(a, Logits<TYPE>::SIZE, f > 0 ? 16 : 8);
+  attr.val.clusterDim.x = p.ranks;
+  cfg.gridDim = dim3(static_cast<unsigned>(a.groups) * p.ranks);
+  cfg.dynamicSmemBytes = p.smem;
   e = cudaLaunchKernelEx(&cfg, kern, a, p.splits);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -307,7 +307,7 @@ template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) group_join_kernel(const __grid_constant__ GroupArgs a) {
   constexpr int V = D / 32;  // floats of a row a lane holds
   const int lane = threadIdx.x & 31;
-  const unsigned row = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);  // (at most 4096 sequences of 65535 x 64 heads)
+  const unsigned row = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);  // (below 2^31)
   if (row >= static_cast<unsigned>(a.batch) * a.q_heads) return;
   const int b = row / a.q_heads, hq = row - b * a.q_heads;
   const int gq = a.q_heads / a.kv_heads, h = hq / gq, group = b / a.width;

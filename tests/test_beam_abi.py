@@ -174,12 +174,14 @@ def _group_args():
     (dict(width=65, batch=65), UNSUPPORTED), (dict(hq=130, qs=130 * 128), UNSUPPORTED), (dict(qs=1016), ARG),
     (dict(qs=1028), ARG), (dict(most=129), CAPACITY), (dict(q=A + 8), ALIGN), (dict(shared=A + 4), ALIGN),
     (dict(out=A + 16), ALIGN), (dict(ws=None), WORKSPACE), (dict(ws=A + 16), ALIGN), (dict(ws_bytes=1 << 20), WORKSPACE),
+    (dict(k=_pool(0, heads=65535), v=_pool(1, heads=65535), batch=4096, hq=65535 * 64, qs=65535 * 64 * 128), UNSUPPORTED),
     (dict(scale=float("nan")), ARG), (dict(scale=float("inf")), ARG)])
 def test_group_refusals(change, code):
     assert _call("fp8_group_attention", _group_args(), change) == code
 
 
 @pytest.mark.parametrize("args", [(0, 1, 2, 8, 128), (8, 3, 2, 8, 128), (8, 0, 2, 8, 128), (65, 65, 2, 8, 128), (8, 4, 0, 8, 128),
-                                  (8, 4, 2, 7, 128), (8, 4, 2, 8, 96), (4097, 1, 2, 8, 128), (8, 4, 1, 65, 128)])
+                                  (8, 4, 2, 7, 128), (8, 4, 2, 8, 96), (4097, 1, 2, 8, 128), (8, 4, 1, 65, 128),
+                                  (4096, 4, 65535, 65535 * 64, 128)])
 def test_group_workspace_query_refuses(args):
     assert beam.fp8_group_workspace_bytes(*args) == 0

@@ -175,6 +175,41 @@ def test_select_of_many_elements():
     assert torch.equal(out[2][:, 0], ((r * 7919) % v).int()) and int(out[1].abs().max()) == 0
 
 
+def test_select_on_two_streams_and_captured():
+    import torch
+    beam, _ = _mods()
+    rng = np.random.default_rng(10)
+    x = [logits(rng, 20, 30011, "float16") for _ in range(2)]
+    scores = [dev(rng.uniform(-9, 0, (5, 4)).astype(np.float32)) for _ in range(2)]
+    out = [(empty((5, 8), "float32"), empty((5, 8)), empty((5, 8))) for _ in range(2)]
+    want = []
+    for i in range(2):
+        beam.beam_select(x[i], scores[i], *out[i])
+        torch.cuda.synchronize()
+        want.append([o.clone() for o in out[i]])
+    streams, graphs = [torch.cuda.Stream() for _ in range(2)], []
+    for i in range(2):
+        streams[i].wait_stream(torch.cuda.current_stream())
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i], stream=streams[i]):
+            beam.beam_select(x[i], scores[i], *out[i])
+    for how in ("eager", "argument", "graph"):
+        for o in out[0] + out[1]:
+            o.zero_()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for i in range(2):
+                if how == "argument":
+                    beam.beam_select(x[i], scores[i], *out[i], stream=streams[i])
+                    continue
+                with torch.cuda.stream(streams[i]):
+                    graphs[i].replay() if how == "graph" else beam.beam_select(x[i], scores[i], *out[i])
+        torch.cuda.synchronize()
+        for i in range(2):
+            for a, b in zip(out[i], want[i]):
+                assert torch.equal(a, b)
+
+
 # ---------------------------------------------------------------- fork
 
 class State:
@@ -346,6 +381,43 @@ def test_copy_skips_pairs_outside_the_pool():
     assert host(buf)[:, 0].tolist() == list(range(8))
     beam.kv_blocks_copy(beam.BlockBuffers(8, [buf]), i32([1]), i32([0]), i32([-5]))
     assert host(buf)[:, 0].tolist() == list(range(8))
+
+
+def test_copy_captured_follows_the_count():
+    import torch
+    beam, _ = _mods()
+    buf = torch.arange(40, device="cuda", dtype=torch.uint8)[:, None].repeat(1, 4096)
+    bufs, count = beam.BlockBuffers(40, [buf]), i32([0])
+    src, dst = i32(range(20)), i32(range(20, 40))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        beam.kv_blocks_copy(bufs, src, dst, count)
+    for n in (0, 1, 7, 20):
+        count.fill_(n)
+        graph.replay()
+        want = list(range(20)) + [i if i < n else 20 + i for i in range(20)]
+        assert host(buf).min(1).tolist() == host(buf).max(1).tolist() == want
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_copied_blocks_of_the_other_pools_decode_alike(dim):
+    """NVFP4 pools: a sequence whose blocks are copies of another's decodes to the same bits."""
+    import torch
+    beam, kvq = _mods()
+    rng = np.random.default_rng(dim)
+    x = rng.standard_normal((2, 1, 2, 64, dim)).astype(np.float16)
+    pools = [kvq.Nvfp4Pool(role, 8, 2, dim) for role in (kvq.ROLE_KEY, kvq.ROLE_VALUE)]
+    for p, y in zip(pools, x):
+        p.quantize(dev(y), i32([[0, 1, 2, 3]]), 4)
+    beam.kv_blocks_copy(beam.BlockBuffers(8, [p.view() for p in pools]), i32([0, 1, 2, 3]), i32([7, 5, 4, 6]))
+    q = dev(np.repeat(rng.standard_normal((1, 8, dim)).astype(np.float16), 2, 0))
+    out = torch.empty((2, 8, dim), dtype=torch.float32, device="cuda")
+    n = kvq.nvfp4_decode_workspace_bytes(2, 8, dim)
+    kvq.nvfp4_decode_attention(q, *(p.desc for p in pools), i32([[0, 1, 2, 3], [7, 5, 4, 6]]), i32([60, 60]), 2, 8, 4, 64, out,
+                               True, 0.0, torch.zeros(n, dtype=torch.uint8, device="cuda"), n)
+    assert torch.equal(out[0], out[1]) and float(out.abs().max()) > 0
 
 
 def test_copy_beyond_31_bits():
