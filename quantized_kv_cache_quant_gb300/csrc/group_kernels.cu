@@ -33,10 +33,17 @@ struct GroupSmem {
   static constexpr int BYTES = BAR_BYTES + AREA;
 };
 
+// A launch lets the next one in at once: the own pairs start where the tcgen05 kernel's thread blocks have left, which
+// they do not depend on, and the joining kernel has its rows' places ready. Each waits for the launch before it at its
+// end (or where it needs its results), so that the last one's end is that of all.
+__device__ __forceinline__ void let_next_in() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 template <int D, int FMT>
 __global__ void __launch_bounds__(128) group_rows16_kernel(const __grid_constant__ GroupArgs a) {
   using S = GroupSmem<D>;
   constexpr int KS = D / 16, NT = D / 8, CH = D / 32;
+  let_next_in();
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ unsigned long long plan_s[36];
   // the arguments and the slice, for functions out of line (a reference to a kernel's parameters is read from global
@@ -67,7 +74,10 @@ __global__ void __launch_bounds__(128) group_rows16_kernel(const __grid_constant
   __syncthreads();
   const TreeSlice slice = tree_slice<kRows, kUnit>(
       args_s, plan_s, [](long long pair) { return pair >= 32 ? 4 : 2; }, [](long long u) { return u >= 4 ? 4 : 2; });
-  if (slice.begin >= slice.end) return;
+  if (slice.begin >= slice.end) {
+    wait_for_launch_before();
+    return;
+  }
   if (tid == 0) slice_s = slice;
   __syncthreads();
   GroupWalk walk;
@@ -293,6 +303,7 @@ __global__ void __launch_bounds__(128) group_rows16_kernel(const __grid_constant
     if (tid == 0) group_record(args_s, seg);
     __syncthreads();  // the next segment's copies overwrite what was read here
   }
+  wait_for_launch_before();
 }
 
 // ---------------------------------------------------------------------------
@@ -316,10 +327,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) group_join_kernel(const __gri
   const int in0 = (b - group * a.width) * gq + hq - h * gq, in1 = hq - h * gq;
   const int tile0 = in0 / p0.tile_rows, tile1 = in1 / p1.tile_rows;
   const int tiles0 = (a.width * gq + p0.tile_rows - 1) / p0.tile_rows, tiles1 = (gq + p1.tile_rows - 1) / p1.tile_rows;
-  const GroupRecord r0 = p0.records[(static_cast<long long>(group) * a.kv_heads + h) * tiles0 + tile0];
-  const GroupRecord r1 = p1.records[(static_cast<long long>(b) * a.kv_heads + h) * tiles1 + tile1];
+  const GroupRecord* const at0 = p0.records + (static_cast<long long>(group) * a.kv_heads + h) * tiles0 + tile0;
+  const GroupRecord* const at1 = p1.records + (static_cast<long long>(b) * a.kv_heads + h) * tiles1 + tile1;
   const int len = min(a.seq_lens[b], min(a.max_blocks * 16, a.max_seq_len)), shared = group_shared(a, group);
   const float v_scale = a.v_scale[a.per_head ? h : 0];
+  wait_for_launch_before();
+  const GroupRecord r0 = *at0, r1 = *at1;
   // (a pair without tokens has no record)
   const int n0 = len > 0 && shared > 0 ? r0.parts * p0.fold : 0, n1 = len > 0 && len > shared * 16 ? r1.parts : 0;
   // partial result i: its place, shared ones first
@@ -387,6 +400,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) group_join_kernel(const __gri
   }
 }
 
+// `early`: the launch may begin while the one before runs.
+cudaError_t launch_next(void (*kern)(const GroupArgs), const GroupArgs& a, dim3 grid, int threads, int smem, bool early, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = early ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <int D, int FMT>
 cudaError_t launch_rows16(const GroupArgs& a, cudaStream_t s) {
   constexpr int smem = GroupSmem<D>::BYTES;
@@ -397,8 +426,7 @@ cudaError_t launch_rows16(const GroupArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   int grid = device_sm_count() * per_sm;
   if (grid > kGroupMaxBlocks) grid = kGroupMaxBlocks;
-  kern<<<dim3(grid, a.kinds == 3 ? 2 : 1), 128, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_next(kern, a, dim3(grid, a.kinds == 3 ? 2 : 1), 128, smem, a.kinds != 3, s);
 }
 
 }  // namespace
@@ -423,9 +451,7 @@ cudaError_t launch_group_attention(const GroupArgs& args, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const long long rows = static_cast<long long>(a.batch) * a.q_heads;
   const unsigned grid = static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps);
-  if (a.head_dim == 128) group_join_kernel<128><<<grid, 32 * kJoinWarps, 0, s>>>(a);
-  else group_join_kernel<64><<<grid, 32 * kJoinWarps, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_next(a.head_dim == 128 ? group_join_kernel<128> : group_join_kernel<64>, a, dim3(grid), 32 * kJoinWarps, 0, true, s);
 }
 
 }  // namespace kvq

@@ -101,6 +101,8 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform for the compiler too
   const int gq = a.q_heads / a.kv_heads;
+  // the own pairs' kernel comes in where blocks of this one have left
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (tid == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
