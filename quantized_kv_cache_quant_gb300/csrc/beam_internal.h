@@ -105,6 +105,7 @@ struct GroupArgs {
   const int32_t* shared_blocks;
   int batch, width, q_heads, kv_heads, head_dim, max_blocks, num_blocks, max_seq_len, per_head, fmt;
   int kinds;         // bit 0: this launch takes the shared blocks, bit 1: the own ones
+  int blocks[2];     // thread blocks of the 16-row kernel that a kind can have work for
   float scale_log2;  // softmax scale * log2(e)
   void* out;
   int out_fp32;

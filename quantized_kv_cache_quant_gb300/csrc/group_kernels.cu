@@ -44,6 +44,11 @@ __global__ void __launch_bounds__(128) group_rows16_kernel(const __grid_constant
   using S = GroupSmem<D>;
   constexpr int KS = D / 16, NT = D / 8, CH = D / 32;
   let_next_in();
+  const int kind = a.kinds == 3 ? static_cast<int>(blockIdx.y) : a.kinds - 1;  // (shared pairs first: they are the long ones)
+  if (static_cast<int>(blockIdx.x) >= a.blocks[kind]) {
+    wait_for_launch_before();
+    return;
+  }
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ unsigned long long plan_s[36];
   // the arguments and the slice, for functions out of line (a reference to a kernel's parameters is read from global
@@ -69,7 +74,7 @@ __global__ void __launch_bounds__(128) group_rows16_kernel(const __grid_constant
   // would have nothing else if both kinds were cut as one (8 groups of 4 over 32K shared tokens: 267 us so, 121 apart).
   if (tid == 0) {
     args_s = a;
-    if (a.kinds == 3) args_s.kinds = 1 << blockIdx.y;
+    args_s.kinds = 1 << kind;
   }
   __syncthreads();
   const TreeSlice slice = tree_slice<kRows, kUnit>(
@@ -424,9 +429,21 @@ cudaError_t launch_rows16(const GroupArgs& a, cudaStream_t s) {
   int per_sm = 0;
   cudaError_t e = once.set(kern, smem, 128, &per_sm);
   if (e != cudaSuccess) return e;
-  int grid = device_sm_count() * per_sm;
-  if (grid > kGroupMaxBlocks) grid = kGroupMaxBlocks;
-  return launch_next(kern, a, dim3(grid, a.kinds == 3 ? 2 : 1), 128, smem, a.kinds != 3, s);
+  const int most = device_sm_count() * per_sm < kGroupMaxBlocks ? device_sm_count() * per_sm : kGroupMaxBlocks;
+  // no more thread blocks than the longest sequences would have work for (slices have two units at least), so that few
+  // requests' pairs of both kinds run side by side
+  GroupArgs b = a;
+  const int gq = a.q_heads / a.kv_heads;
+  const long long units = (a.max_seq_len + kUnit - 1ll) / kUnit;
+  const long long pairs[2] = {static_cast<long long>(a.batch / a.width) * a.kv_heads * ((a.width * gq + kRows - 1) / kRows),
+                              static_cast<long long>(a.batch) * a.kv_heads * ((gq + kRows - 1) / kRows)};
+  int grid = 0;
+  for (int kind = 0; kind < 2; ++kind) {
+    const long long want = (pairs[kind] * units + 1) / 2;
+    b.blocks[kind] = static_cast<int>(want < most ? want : most);
+    if ((a.kinds >> kind & 1) != 0 && b.blocks[kind] > grid) grid = b.blocks[kind];
+  }
+  return launch_next(kern, b, dim3(grid, a.kinds == 3 ? 2 : 1), 128, smem, a.kinds != 3, s);
 }
 
 }  // namespace
