@@ -10,8 +10,10 @@ constexpr int kBlock = 16;  // tokens of an FP8 pool block
 // ---------------------------------------------------------------------------
 // 16 query rows a tile on mma.sync m16n8k16, the rows on the MMA's 16-row side:
 // as tree attention's kernel of few rows, without a mask. Four warps; warp w
-// takes every fourth block of the segment through its own ring of bulk copies,
-// with its own running maximum, sum and outputs, joined at the segment's end.
+// takes every fourth block of the segment, with its own running maximum, sum and
+// outputs, joined at the segment's end. A block's bytes are in operand order, so
+// that each lane needs 16-byte units of its own: it copies them into its part of
+// a ring in shared memory, some blocks ahead, and nobody waits for anyone else.
 //   q.k^T: A = q (channels permuted as the keys' order), B = the keys as fp16
 //   p.V  : A = p rounded to fp16 and, on a second product, what the rounding
 //          left (2^-22 of p), B = the values as fp16
@@ -25,12 +27,11 @@ constexpr float kBias = 10.0f;
 
 template <int D>
 struct GroupSmem {
-  static constexpr int BAR_BYTES = 128;
   static constexpr int STAGE = 2 * kBlock * D;
   static constexpr int RING = 4 * kStages * STAGE;
   static constexpr int COMBINE = 4 * kRows * (D + 2) * 4;
   static constexpr int AREA = RING > COMBINE ? RING : COMBINE;
-  static constexpr int BYTES = BAR_BYTES + AREA;
+  static constexpr int BYTES = AREA;
 };
 
 // A launch lets the next one in at once: the own pairs start where the tcgen05 kernel's thread blocks have left, which
@@ -55,21 +56,14 @@ __global__ void __launch_bounds__(128) group_rows16_kernel(const __grid_constant
   // memory there)
   __shared__ GroupArgs args_s;
   __shared__ TreeSlice slice_s;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
-  uint8_t* area = smem + S::BAR_BYTES;
+  uint8_t* area = smem;
   float* o_s = reinterpret_cast<float*>(area);   // [4][16][D]
   float* m_s = o_s + 4 * kRows * D;              // [4][16]
   float* l_s = m_s + 4 * kRows;                  // [4][16]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
   const int gq = a.q_heads / a.kv_heads;
-  uint64_t* bar = bars + warp * kStages;
-  uint8_t* ring = area + warp * kStages * S::STAGE;
-  if (lane == 0) {
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) mbar_init(&bar[s], 1);
-    fence_mbar_init();
-  }
+  uint8_t* ring = area + warp * kStages * S::STAGE + lane * 16;  // this lane's units
   // Thread blocks of their own for each kind, cut into slices of their own: own pairs are many and short, and a few blocks
   // would have nothing else if both kinds were cut as one (8 groups of 4 over 32K shared tokens: 267 us so, 121 apart).
   if (tid == 0) {
@@ -88,8 +82,6 @@ __global__ void __launch_bounds__(128) group_rows16_kernel(const __grid_constant
   GroupWalk walk;
   walk.start(slice);
   const GroupSegment& seg = walk.seg;
-  unsigned it = 0;         // blocks this warp has taken through its ring
-  bool dead = false;       // a wait ran out: no more copies
   int turn = 0;            // the warp whose turn it is to take a short segment alone
   while (next_segment<kRows, kUnit>(args_s, slice_s, walk)) {
     const int h = seg.h, total = seg.r.len, row0 = seg.tile * kRows;
@@ -105,23 +97,31 @@ __global__ void __launch_bounds__(128) group_rows16_kernel(const __grid_constant
       if (turn != warp) continue;
     }
     const int first = alone ? 0 : warp, step = alone ? 1 : 4;
-    const int n_mine = (!dead && j_end - j_begin > first) ? (j_end - j_begin - first + step - 1) / step : 0;
+    const int n_mine = j_end - j_begin > first ? (j_end - j_begin - first + step - 1) / step : 0;
     const int32_t* table = a.block_table + static_cast<long long>(seg.r.seq) * a.max_blocks + seg.r.block0;
     auto phys = [&](int j) -> long long {
-      return min(max(table[j_begin + first + step * j], 0), a.num_blocks - 1);
+      return j < n_mine ? min(max(table[j_begin + first + step * j], 0), a.num_blocks - 1) : 0;
     };
     auto issue = [&](int j, long long blk) {
-      const long long off = (blk * a.kv_heads + h) * (kBlock * D);
-      const int s = (it + j) % kStages;
-      uint8_t* dst = ring + s * S::STAGE;
-      mbar_arrive_expect_tx(&bar[s], S::STAGE);
-      bulk_g2s(dst, a.k_pool + off, kBlock * D, &bar[s]);
-      bulk_g2s(dst + kBlock * D, a.v_pool + off, kBlock * D, &bar[s]);
+      if (j < n_mine) {
+        const long long off = (blk * a.kv_heads + h) * (kBlock * D) + lane * 16;
+        uint8_t* dst = ring + j % kStages * S::STAGE;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          cp_async16(dst + c * 512, a.k_pool + off + c * 512);
+          cp_async16(dst + kBlock * D + c * 512, a.v_pool + off + c * 512);
+        }
+      }
+      cp_async_commit();
     };
-    if (lane == 0) {
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      for (int j = 0; j < kStages && j < n_mine; ++j) issue(j, phys(j));
+    {
+      long long blk[kStages];
+#pragma unroll
+      for (int j = 0; j < kStages; ++j) blk[j] = phys(j);
+#pragma unroll
+      for (int j = 0; j < kStages; ++j) issue(j, blk[j]);
     }
+    long long next_blk = phys(kStages);
 
     // query rows g and g + 8 of the tile, A fragments of m16n8k16
     uint32_t qa[KS][4];
@@ -145,22 +145,15 @@ __global__ void __launch_bounds__(128) group_rows16_kernel(const __grid_constant
 #pragma unroll
     for (int i = 0; i < NT; ++i) o_acc[i][0] = o_acc[i][1] = o_acc[i][2] = o_acc[i][3] = 0.0f;
 
-    int j = 0;
-    bool timed_out = false;
-    for (; j < n_mine; ++j) {
-      const int s = (it + j) % kStages;
-      const long long next_blk = (lane == 0 && j + kStages < n_mine) ? phys(j + kStages) : 0;
-      if (__any_sync(0xffffffffu, !mbar_wait_bounded(&bar[s], ((it + j) / kStages) & 1))) {
-        timed_out = true;
-        break;
-      }
-      const uint4* kb = reinterpret_cast<const uint4*>(ring + s * S::STAGE);
-      const uint4* vb = reinterpret_cast<const uint4*>(ring + s * S::STAGE + kBlock * D);
+    for (int j = 0; j < n_mine; ++j) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      const uint8_t* kb = ring + j % kStages * S::STAGE;
+      const uint8_t* vb = kb + kBlock * D;
       const int tok_base = (j_begin + first + step * j) * kBlock;
       uint32_t kw[2 * KS];
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const uint4 x = kb[c * 32 + lane];
+        const uint4 x = *reinterpret_cast<const uint4*>(kb + c * 512);
         kw[4 * c] = x.x;
         kw[4 * c + 1] = x.y;
         kw[4 * c + 2] = x.z;
@@ -179,7 +172,7 @@ __global__ void __launch_bounds__(128) group_rows16_kernel(const __grid_constant
       uint32_t vw[NT];
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const uint4 x = vb[c * 32 + lane];
+        const uint4 x = *reinterpret_cast<const uint4*>(vb + c * 512);
         vw[4 * c] = x.x;
         vw[4 * c + 1] = x.y;
         vw[4 * c + 2] = x.z;
@@ -234,23 +227,10 @@ __global__ void __launch_bounds__(128) group_rows16_kernel(const __grid_constant
         mma16816(o_acc[nt], A[0], A[1], A[2], A[3], b0, b1);
         mma16816(o_acc[nt], L[0], L[1], L[2], L[3], b0, b1);
       }
-      __syncwarp();
-      if (lane == 0 && j + kStages < n_mine) {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        issue(j + kStages, next_blk);
-      }
+      // (the lane has used what it read there)
+      issue(j + kStages, next_blk);
+      next_blk = phys(j + kStages + 1);
     }
-    if (timed_out) {
-      if (lane == 0) report_timeout(a.status);
-      for (int jj = j; jj < n_mine && jj < j + kStages; ++jj)
-        (void)mbar_wait_bounded(&bar[(it + jj) % kStages], ((it + jj) / kStages) & 1);
-      dead = true;
-      m_run[0] = m_run[1] = -INFINITY;
-      l_run[0] = l_run[1] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < NT; ++i) o_acc[i][0] = o_acc[i][1] = o_acc[i][2] = o_acc[i][3] = 0.0f;
-    }
-    it += n_mine;
     l_run[0] = quad_sum(l_run[0]);
     l_run[1] = quad_sum(l_run[1]);
 
