@@ -68,7 +68,7 @@ struct BlocksCompactArgs {
   int32_t* copy_dst;
   int32_t* copy_count;
   int32_t* done;
-  uint32_t* bits;        // [ceil(num_blocks / 32)] free blocks; 0 between calls
+  uint32_t* bits;        // [ceil(num_blocks / 32)] free blocks
   int32_t* before;       // [ceil(num_blocks / 32)] free blocks below keep, used ones from keep on, in the words before
   CompactState* state;
   int batch, max_blocks, keep, num_blocks, max_copies;

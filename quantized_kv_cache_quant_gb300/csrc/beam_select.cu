@@ -12,18 +12,29 @@
 //          (fp32, rescaled when the maximum grows); they meet at the part's end
 //   best   within a row the order of the scores is that of the logits, so a part
 //          needs its k = n_out largest logits only. A value that k of the threads'
-//          maxima reach is one that at least k elements reach, and only the threads whose
-//          maximum reaches it have such elements, k of 256 but for ties: their elements
-//          are read once more, from L2, by a warp each.
-//          Every warp keeps a list of (value, token) keys, which is cut down to its k
-//          largest where it runs full; in the end the lists are ranked together.
+//          maxima reach is one that at least k elements reach, and only the threads
+//          whose maximum reaches it have such elements, some 3 k of 256: the 64 bytes
+//          with the maximum are read once more, from L2 (all of a thread's bytes where
+//          its next best step reaches it too). Every warp keeps a list of (value,
+//          token) keys, which is cut down to its k largest where it runs full; in the
+//          end the lists are ranked together.
 // Then the first block of the cluster has every part's maximum, sum and sorted
 // list (read through distributed shared memory), turns them into scores in fp64,
 // and one warp takes the largest head of all lists n_out times.
 //
 // (Lists that elements enter on the way cost more than the sums: one list a block,
 // with barriers between chunks of 32 KB in shared memory, 134 us for 512 rows of
-// 128000 bf16 logits, 67 with one barrier a chunk; a list a warp 184.)
+// 128000 bf16 logits, 67 with one barrier a chunk; a list a warp 184. Looking for the
+// k-th of the maxima, so that fewer steps are read again, 51.4 against 52, but with
+// fp32 logits 69.5 against 64.3 and 152 against 133 us for one request of 64 beams.)
+//
+// 512 rows of 128000 bf16 logits (one in five ended): 52 us, 2.1 TB/s; fp32 64 us,
+// 4.1 TB/s; one request of 4 x 32000: 12.4 us. The large calls are bound by instructions: 64
+// registers a thread and four blocks an SM do an exponential, a subtraction and a
+// product an element, some 22 us of the 52; the rest is the parts' ends (bound,
+// second look, ranking) and the first block's scores, which other clusters' reading
+// hides in part. The small ones are a chain of such steps, some 10 us of waits. One
+// request is one cluster, 16 blocks at most: alone with 64 beams it has a tenth of the SMs.
 #include <cfloat>
 #include <climits>
 #include <cooperative_groups.h>
@@ -134,11 +145,11 @@ __host__ __device__ constexpr int warp_list_bytes(int k) { return 2 * kWarps * l
 
 struct SelectShared {
   uint32_t top[kWarps], low[kWarps];  // codes of the warps' largest and j-th largest thread maxima
-  uint32_t near[kThreads];            // codes that may be among the k largest
-  uint8_t rich[kThreads];  // threads whose maximum reaches the bound
+  int ones[kThreads];      // first vectors of threads' only steps with elements that reach the bound
+  uint8_t rich[kThreads];  // threads that have several such steps
   unsigned long long sum;  // of the part
   uint32_t bound;          // code of a value that at least k of the part's elements reach
-  int nears, riches, count;  // codes in `near`; threads in `rich`; keys in the common list
+  int n_ones, riches, count;  // of `ones`, of `rich`; keys in the common list
   float score[kBeamMaxWidth];
   uint8_t kind[kBeamMaxWidth];  // of each beam
 };
@@ -212,7 +223,6 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
     const long long row = static_cast<long long>(group) * a.width + beam;
     // a beam that has ended or is dead: its candidates follow without a look at the logits
     if (sh.kind[beam] != kLive) continue;
-    unsigned long long* const out = lists + part * k;
     const uint8_t* base = static_cast<const uint8_t*>(a.logits) + row * a.row_stride * L::SIZE;
     // aligned vector i holds elements i * E - lead .. of the row; a thread's vector j is elements j * E .., from aligned
     // vectors j and, where the row does not start on 16 bytes, j + 1
@@ -222,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
     const int v0 = static_cast<int>(static_cast<long long>(nv) * split / splits);
     const int v1 = static_cast<int>(static_cast<long long>(nv) * (split + 1) / splits);
     if (tid == 0) {
-      sh.nears = sh.riches = sh.count = 0;
+      sh.n_ones = sh.riches = sh.count = 0;
       sh.sum = 0ull;
       sh.bound = 0u;
     }
@@ -292,6 +302,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
     };
 
     float m = -INFINITY, s = 0.0f;  // of this thread
+    float second = -INFINITY;       // the largest element of its steps but the one with the maximum,
+    int at = v1;                    // whose first vector (lane 0's) this is
     Step next;
     int c = v0 + warp * kStep;
     if (c < v1) load(c, next);
@@ -306,7 +318,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
       top = clean(top);
       if (top > m) {
         s = m == -INFINITY ? 0.0f : s * exp_below(m, top);
+        second = m;
         m = top;
+        at = c;
+      } else {
+        second = fmaxf(second, top);
       }
       if (m > -INFINITY) {
         // (a step's terms first: fewer roundings at the sum's size)
@@ -341,8 +357,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
     }
 
     // The largest of the threads' maxima, and a bound that k of them reach: each warp's j-th largest one (8 j >= k), the
-    // smallest of the warps' ones. Of the maxima that reach it, some 3 k, the k-th largest is the bound that is used.
-    // (Found by bisection over all, it took 1.8 us.)
+    // smallest of the warps' ones; some 3 k do. (The k-th itself took 1.8 us to find by bisection, 0.7 among these.)
     const uint32_t mine = m > -INFINITY ? float_code(m) : 0u;
     {
       uint32_t code = mine, best = __reduce_max_sync(0xffffffffu, code);
@@ -355,9 +370,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
       if (lane == 0) sh.low[warp] = best;
     }
     __syncthreads();
-    {
-      const uint32_t low = __reduce_min_sync(0xffffffffu, sh.low[lane % kWarps]);
-      if (mine != 0u && mine >= low) sh.near[atomicAdd(&sh.nears, 1)] = mine;
+    const uint32_t bound = __reduce_min_sync(0xffffffffu, sh.low[lane % kWarps]);
+    if (mine != 0u && mine >= bound) {
+      // (nearly all of them have one step with such elements)
+      if (second > -INFINITY && float_code(second) >= bound) sh.rich[atomicAdd(&sh.riches, 1)] = static_cast<uint8_t>(tid);
+      else sh.ones[atomicAdd(&sh.n_ones, 1)] = at + lane;
     }
     const uint32_t most = __reduce_max_sync(0xffffffffu, sh.top[lane % kWarps]);  // (0: nothing above -inf)
     const float part_max = most == 0u ? -INFINITY : code_float(most);
@@ -368,25 +385,9 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
       if (lane == 0) atomicAdd(&sh.sum, units);
     }
     __syncthreads();
-    {
-      const int near = sh.nears;
-      for (int i0 = 0; i0 + (warp << 2) < near; i0 += kThreads / 8) {
-        const int i = i0 + tid / 8;
-        const uint32_t code = i < near ? sh.near[i] : 0u;
-        int before = 0;
-        for (int j = tid % 8; j < near; j += 8) before += sh.near[j] > code || (sh.near[j] == code && j < i);
-        before += __shfl_xor_sync(0xffffffffu, before, 1);
-        before += __shfl_xor_sync(0xffffffffu, before, 2);
-        before += __shfl_xor_sync(0xffffffffu, before, 4);
-        if (tid % 8 == 0 && i < near && before == k - 1) sh.bound = code;  // (with fewer than k: 0, all of them)
-      }
-    }
-    __syncthreads();
-    const uint32_t bound = sh.bound;
-    if (mine != 0u && mine >= bound) sh.rich[atomicAdd(&sh.riches, 1)] = static_cast<uint8_t>(tid);
-    __syncthreads();
 
-    // their elements once more, a warp for a thread's
+    // their steps once more: eight threads' step with the maximum a warp and load, or all steps of one thread, 32 vectors a
+    // load
     unsigned long long* list = warp_lists + warp * cap;
     unsigned long long* other = warp_lists + (kWarps + warp) * cap;
     unsigned long long own = kNone;  // the warp's k-th largest key (kNone: fewer than k so far)
@@ -400,24 +401,30 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
       n = k;
       own = list[k - 1];
     };
-    // (32 of a thread's vectors at a time, the next ones on their way)
-    const int steps = (v1 - v0 + kWarps * kStep - 1) / (kWarps * kStep), riches = sh.riches;
-    int r = warp, q0 = 0;  // of the vectors that come next
+    const int steps = (v1 - v0 + kWarps * kStep - 1) / (kWarps * kStep), ones = (sh.n_ones + 7) / 8, riches = sh.riches;
+    int r = warp, q0 = 0;  // the load that comes next
     auto place = [&]() -> int {
-      if (r >= riches) return v1;
-      const int thread = sh.rich[r], q = q0 + lane;
-      q0 += 32;
-      if (q0 >= steps * kVecs) {
-        q0 = 0;
+      int j = v1;
+      if (r < ones) {
+        const int i = r * 8 + lane / kVecs;
+        if (i < sh.n_ones) j = sh.ones[i] + 32 * (lane % kVecs);
         r += kWarps;
+      } else if (r - ones < riches) {
+        const int thread = sh.rich[r - ones], q = q0 + lane;
+        if (q < steps * kVecs) j = v0 + (q / kVecs * kWarps + thread / 32) * kStep + q % kVecs * 32 + thread % 32;
+        q0 += 32;
+        if (q0 >= steps * kVecs) {
+          q0 = 0;
+          r += kWarps;
+        }
       }
-      return q < steps * kVecs ? v0 + (q / kVecs * kWarps + thread / 32) * kStep + q % kVecs * 32 + thread % 32 : v1;
+      return j;
     };
-    bool more = r < riches;
+    bool more = r < ones + riches;
     int j = place();
     uint4 w = vec(j);
     while (more) {
-      more = r < riches;
+      more = r < ones + riches;
       const int j_next = place();
       const uint4 w_next = vec(j_next);
       const float high = clean(L::largest(w));
@@ -457,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
     const int found = sh.count;
     if (!all_run) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     all_run = true;
+    unsigned long long* const out = lists + part * k;
     rank_list(warp_lists, found, k, out);
     if (tid == 0) sums[part] = PartSum{sh.sum, part_max};
     if (found < k) {  // tokens at -inf, by their index
@@ -605,7 +613,8 @@ struct SelectPlan {
 };
 
 // Blocks of a cluster (up to 16: one request is one cluster), as many as have room at once, and parts of a row, so that
-// the block with the most to do has little of it; a part costs what `fixed` bytes of logits do beside its own.
+// the block with the most to do has little of it; a part costs what `fixed` bytes of logits do beside its own. (64
+// requests of 8 rows of 128000: clusters of 2, 4, 8 and 16 blocks 88, 57, 51 and 67 us; four blocks an SM allow 8.)
 SelectPlan plan_select(const BeamSelectArgs& a, int size, int most_ranks) {
   SelectPlan best{1, 1, 0};
   const long long fixed = 16384;
