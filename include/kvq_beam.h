@@ -105,11 +105,12 @@ KVQ_API size_t kv_blocks_workspace_bytes(int32_t groups, int32_t num_blocks);
  * block_tokens) (blocks held beyond that are not inherited: grow again after the
  * call), the held entries are p's, those behind become -1. A block that loses
  * its last reference is freed; freed blocks are pushed in descending order, the
- * lowest on top. Then every sequence whose last block is partly filled and
- * has other references gets a block of its own from the top of the stack, in the
- * order of b, and a (copy_src, copy_dst) pair, except that where only such sequences of
- * its request share that block the first of them keeps it. When the stack runs
- * out, the sequences left go on sharing (granted 0) and must not be appended to.
+ * lowest on top. Then every sequence whose last block is partly filled and has
+ * other references gets a block of its own from the top of the stack, in the
+ * order of b, and a (copy_src, copy_dst) pair, except that where only such
+ * sequences of its request share that block the first of them keeps it. When the
+ * stack runs out, the sequences left go on sharing (granted 0) and must not be
+ * appended to.
  * A partly filled block is shared within a request only. Entries that name no
  * block of the pool are passed on and not counted.
  * The same inputs always give the same tables. KVQ_ERR_UNSUPPORTED for batch >
@@ -131,9 +132,9 @@ typedef struct {
 
 /* Copy block src[i] to block dst[i] for i < min(*count, n_pairs) in each of
  * n_buffers buffers (a host array, read before the call returns). Pairs that name
- * no block of [0, num_blocks) are skipped. No block may be the destination of two pairs, or the
- * source of one and the destination of another. count: device int32 [1], or NULL
- * for n_pairs. One launch. */
+ * no block of [0, num_blocks) are skipped. No block may be the destination of two
+ * pairs, or the source of one and the destination of another. count: device int32
+ * [1], or NULL for n_pairs. One launch. */
 KVQ_API kvq_status kv_blocks_copy(const kvq_block_buffer* buffers, int32_t n_buffers, int32_t num_blocks,
                                   const int32_t* src, const int32_t* dst, int32_t n_pairs, const int32_t* count,
                                   void* stream);
@@ -163,11 +164,11 @@ KVQ_API kvq_status kv_blocks_compact(int32_t* block_table, int32_t batch, int32_
 
 /* Workspace of fp8_group_attention: a status word at offset 0 (as
  * kv_decode_workspace_bytes) and the partial results that the call's kernels
- * hand over: at head_dim 128 between 17 and 59 MB, and 520 bytes for every query head of
- * every sequence, up to five times. Zero it once after allocating it (the status
- * word collects errors until it is cleared). One workspace serves one stream:
- * calls that overlap on the device (two captured graphs among them) must not
- * share it. 0 for shapes the call refuses. */
+ * hand over: at head_dim 128 some 34 to 38 MB, and 520 bytes for every query
+ * head of every sequence, two or three times. Zero it once after allocating it
+ * (the status word collects errors until it is cleared). One workspace serves one
+ * stream: calls that overlap on the device (two captured graphs among them) must
+ * not share it. 0 for shapes the call refuses. */
 KVQ_API size_t fp8_group_workspace_bytes(int32_t batch, int32_t width, int32_t kv_heads, int32_t q_heads,
                                          int32_t head_dim);
 
@@ -175,19 +176,21 @@ KVQ_API size_t fp8_group_workspace_bytes(int32_t batch, int32_t width, int32_t k
  * blocks: as fp8_decode_attention (q in fp16),
  *   out[b, hq] = softmax(q[b, hq] . (k_scale K)^T * softmax_scale) (v_scale V)
  * over tokens 0 .. seq_lens[b] - 1 of sequence b, zeros where seq_lens[b] <= 0,
- * but the blocks that a group's sequences share are read (and converted) once a group:
+ * but the blocks that a group's sequences share are read (and converted) once a
+ * group:
  *   q             : device fp16, row b at q + b * q_row_stride is [q_heads, D]
  *   block_table   : device int32 [batch, max_blocks]
  *   seq_lens      : device int32 [batch], the new tokens included
  *   shared_blocks : device int32 [batch / width]: the first shared_blocks[g] table
  *                   entries of all sequences of group g with a length above 0 are
- *                   the same, and each of those has at least 16 times as many tokens (kv_blocks_fork
- *                   writes such numbers; a smaller one, 0 included, only costs time)
+ *                   the same, and each of those has at least 16 times as many
+ *                   tokens (kv_blocks_fork writes such numbers; a smaller one, 0
+ *                   included, only costs time)
  *   out           : device [batch, q_heads, D], fp32 if out_fp32, else fp16
  * Rows of a block behind a sequence's last token do not reach it, NaN bytes
  * included. softmax_scale <= 0 selects 1/sqrt(D). max_seq_len bounds seq_lens[b];
- * max_seq_len <= max_blocks * 16. Lengths, counts and table entries are clamped on the
- * device: a bad one gives wrong numbers, never an access outside the buffers.
+ * max_seq_len <= max_blocks * 16. Lengths, counts and table entries are clamped on
+ * the device: a bad one gives wrong numbers, never an access outside the buffers.
  * The softmax weights go into the value product in two fp16 parts (2^-22
  * relative), but over shared blocks for fp16 output with width * (q_heads /
  * kv_heads) > 16 in one (2^-11 relative, as the output itself). Scores, sums and

@@ -118,12 +118,15 @@ constexpr int kGroupMaxBlocks = 1024;       // of the 16-row kernel
 constexpr int kGroupTcMaxBlocks = 160;      // of the tcgen05 kernel
 constexpr int kGroupRows16 = 16, kGroupTcRows = 128;
 // Query rows of a tile of shared blocks, as partial rows each: up to 16 rows a kv head the 16-row kernel, beyond the
-// tcgen05 kernel, whose 128 rows hold 32 or 64 rows 4 or 2 times where that is enough.
+// tcgen05 kernel, whose 128 rows hold 64 rows twice where that is enough. (us, 128 channels unless said otherwise:
+//   16 rows, 8 x 4 sequences over 32K tokens   113 on mma.sync, 136 on tcgen05; 64 channels, 16 x 4 over 16K: 74, 109
+//   32 rows, 32 x 4 sequences over 8K tokens   208 as two tiles on mma.sync, 163 held twice, 167 four times, 174 once
+//   64 rows, 4 x 8 sequences over 128K tokens  664 as four tiles on mma.sync, 253 held twice, 273 once)
 struct GroupTile {
   int rows, fold;
 };
 constexpr GroupTile group_tile(int rows_per_head) {
-  return rows_per_head <= 16 ? GroupTile{16, 1} : rows_per_head <= 32 ? GroupTile{32, 4} : rows_per_head <= 64 ? GroupTile{64, 2} : GroupTile{128, 1};
+  return rows_per_head <= 16 ? GroupTile{16, 1} : rows_per_head <= 64 ? GroupTile{64, 2} : GroupTile{128, 1};
 }
 cudaError_t launch_group_attention(const GroupArgs& a, cudaStream_t s);
 cudaError_t launch_group_tc(const GroupArgs& a, cudaStream_t s);  // the shared blocks on tcgen05

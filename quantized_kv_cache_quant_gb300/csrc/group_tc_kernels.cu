@@ -3,11 +3,11 @@
 //
 // A thread block per SM walks its slice of (group, kv head, row tile) pairs in
 // tiles of 64 tokens. The tensor core's 128 rows hold the query rows of a tile
-// once, or those of a group with up to 64 (32) of them two (four) times: copy f
-// of a row then has the weights of the f-th half (quarter) of a tile's tokens
-// and zeros elsewhere. The products cost what they did, each softmax thread has
-// a half (a quarter) of the work, and the copies are partial results like those
-// of different thread blocks. Two streams take alternate token tiles, each with
+// once, or those of a group with up to 64 of them twice: copy f of a row then has
+// the weights of the f-th half of a tile's tokens and zeros elsewhere. The
+// products cost what they did, each softmax thread has half of the work, and the
+// copies are partial results like those of different thread blocks.
+// Two streams take alternate token tiles, each with
 // its own scores, weights and outputs, so that the tensor core works for one
 // while the other one's softmax runs:
 //   S = Q K^T : A = Q (fp16, exact) in tensor memory (WIDE: in shared memory),
@@ -20,6 +20,15 @@
 // attention's kernel: one warp copies pool blocks, four turn FP8 bytes into fp16
 // operand tiles, three threads issue the MMAs, eight warps do the softmax, a
 // thread per row (and copy).
+//
+// 4 x 8 sequences over 128K tokens (64 rows a kv head): 253 us, 4.3 TB/s. What
+// bounds it is the loop through the four fp16 places: conversion (930 clocks),
+// scores (600), softmax (1390) and products (1400) of a tile take some 4300 / 4
+// clocks a tile with all of them at work; DRAM is at half its rate, the tensor core busy
+// 38 % of the time. Shared memory has no fifth place at D = 128; with 6 and 8 at
+// D = 64 the copies are what the conversion waits for. No faster: a second
+// copying warp (277 us), a place handed on through shared memory (274), weights
+// made before the wait for the products before (265).
 #include "group_plan.cuh"
 #include "tc_device.cuh"
 
@@ -76,17 +85,6 @@ struct TcShared {
 // Token of column c of a tile.
 __host__ __device__ constexpr int column_token(int c) {
   return (c & ~15) + 8 * ((c >> 1) & 1) + 2 * ((c >> 2) & 3) + (c & 1);
-}
-
-// COLS columns of tensor memory: 16, 32 or 64.
-template <int COLS>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r) {
-  if constexpr (COLS == 16) {
-    tmem_ld16(taddr, r);
-  } else {
-#pragma unroll
-    for (int c = 0; c < COLS; c += 32) tmem_ld32(taddr + c, r + c);
-  }
 }
 
 template <int D, int FMT, bool WIDE, int FOLD>
@@ -424,7 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         tc_fence_after();
         const bool pv_done = n > 0 && mbar_test(&sh.pdone[i], (n - 1) & 1);  // answers while the scores load
         uint32_t sr[COLS];
-        if (warp_live) tmem_ld_cols<COLS>(tm_s, sr);
+        if (warp_live) {
+#pragma unroll
+          for (int c = 0; c < COLS; c += 32) tmem_ld32(tm_s + c, sr + c);
+        }
         const int left = total - t * kTile;  // tokens from the tile's first on
         tmem_wait_ld();
         tc_fence_before();
@@ -472,12 +473,11 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
             }
             float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
             const float2 mul2 = make_float2(kmul, kmul), sub2 = make_float2(-msub, -msub);
-            constexpr int STEP = COLS < 32 ? COLS : 32;
 #pragma unroll
-            for (int c0 = 0; c0 < COLS; c0 += STEP) {
-              uint32_t hi[STEP / 2], lo[WIDE ? STEP / 2 : 1];
+            for (int c0 = 0; c0 < COLS; c0 += 32) {
+              uint32_t hi[16], lo[WIDE ? 16 : 1];
 #pragma unroll
-              for (int c = 0; c < STEP; c += 2) {
+              for (int c = 0; c < 32; c += 2) {
                 float2 p = __ffma2_rn(make_float2(__uint_as_float(sr[c0 + c]), __uint_as_float(sr[c0 + c + 1])), mul2, sub2);
                 p.x = fast_exp2(p.x);
                 p.y = fast_exp2(p.y);
@@ -490,13 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                 }
               }
               const uint32_t to = tm_p + (fold * COLS + c0) / 2;
-              if constexpr (STEP == 32) {
-                tmem_st16(to, hi);
-                if constexpr (WIDE) tmem_st16(to + kTile / 2, lo);
-              } else {
-                tmem_st8(to, hi);
-                if constexpr (WIDE) tmem_st8(to + kTile / 2, lo);
-              }
+              tmem_st16(to, hi);
+              if constexpr (WIDE) tmem_st16(to + kTile / 2, lo);
             }
             tile_sum = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             if (!__any_sync(0xffffffffu, m == -INFINITY || !(tile_sum <= kMostSum))) break;
@@ -601,7 +596,6 @@ cudaError_t launch_group_tc(const GroupArgs& a, cudaStream_t s) {
   switch (a.part[0].fold) {
     case 1: return dispatch_tc<1>(a, s);
     case 2: return dispatch_tc<2>(a, s);
-    case 4: return dispatch_tc<4>(a, s);
     default: return cudaErrorInvalidValue;
   }
 }
