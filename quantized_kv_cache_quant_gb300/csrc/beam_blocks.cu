@@ -285,10 +285,9 @@ __global__ void __launch_bounds__(kCopyThreads) blocks_copy_kernel(const __grid_
 // "targets" are the free blocks below keep, "movers" the used ones from keep on),
 // the lists (lists: mover r goes to target r, the targets left form the stack),
 // and what follows the moves (follow: map, shares, tables). Five launches, each
-// of which starts under the one before; a cluster that does all of it took as
-// long for 4096 blocks (12 us) and twice as long for 131072. 1M blocks and 512
-// tables: 32 us for 13 MB, of which the launches' dependences on each other are
-// some 11 and the scattered atomics, reads and writes the rest.
+// of which starts under the one before. 1M blocks and 512 tables: 32 us for 13 MB,
+// of which the launches' dependences on each other are some 11 and the scattered
+// atomics, reads and writes the rest.
 // ---------------------------------------------------------------------------
 constexpr int kCompactThreads = 256;
 
@@ -300,11 +299,17 @@ __device__ __forceinline__ uint32_t target_bits(const BlocksCompactArgs& a, int 
 __device__ __forceinline__ uint32_t mover_bits(const BlocksCompactArgs& a, int i, uint32_t word) {
   return ~word & low_bits(a.num_blocks - 32 * i) & ~low_bits(a.keep - 32 * i);
 }
+// What a pass of the same launch has written is read past L1 (SAME), that of a launch before through it.
+template <bool SAME, class T>
+__device__ __forceinline__ T passed(const T* p) {
+  return SAME ? __ldcg(p) : *p;
+}
 // Rank of mover x among the movers.
+template <bool SAME>
 __device__ __forceinline__ int mover_rank(const BlocksCompactArgs& a, int x, uint32_t word) {
   const int i = x >> 5;
   // (the word that keep cuts counts the targets before it; it is the first with movers)
-  return (i > a.keep >> 5 ? a.before[i] : 0) + __popc(mover_bits(a, i, word) & ((1u << (x & 31)) - 1u));
+  return (i > a.keep >> 5 ? passed<SAME>(a.before + i) : 0) + __popc(mover_bits(a, i, word) & ((1u << (x & 31)) - 1u));
 }
 
 // The four passes, by thread `me` of `threads`.
@@ -372,30 +377,32 @@ __device__ __forceinline__ void compact_rank(const BlocksCompactArgs& a, unsigne
   cluster.sync();  // (no block ends while another reads its sums)
 }
 
+template <bool SAME>
 __device__ __forceinline__ void compact_lists(const BlocksCompactArgs& a, long long me, long long threads) {
-  const int movers = a.state->movers, targets = a.state->targets;
-  if (a.state->done == 0) return;
+  const int movers = passed<SAME>(&a.state->movers), targets = passed<SAME>(&a.state->targets);
+  if (passed<SAME>(&a.state->done) == 0) return;
   const int lane = threadIdx.x & 31, words = (a.num_blocks + 31) / 32;
   const uint32_t below = (1u << lane) - 1u;
   for (long long i = me >> 5; i < words; i += threads >> 5) {
-    const uint32_t word = a.bits[i], to = target_bits(a, i, word), from = mover_bits(a, i, word);
+    const uint32_t word = passed<SAME>(a.bits + i), to = target_bits(a, i, word), from = mover_bits(a, i, word);
     const int x = 32 * static_cast<int>(i) + lane;
     if (to >> lane & 1u) {
-      const int r = a.before[i] + __popc(to & below);
+      const int r = passed<SAME>(a.before + i) + __popc(to & below);
       if (r < movers) a.copy_dst[r] = x;
       else a.free_blocks[targets - 1 - r] = x;
     }
-    if (from >> lane & 1u) a.copy_src[mover_rank(a, x, word)] = x;
+    if (from >> lane & 1u) a.copy_src[mover_rank<SAME>(a, x, word)] = x;
   }
 }
 
+template <bool SAME>
 __device__ __forceinline__ void compact_follow(const BlocksCompactArgs& a, long long me, long long threads) {
-  const bool done = a.state->done != 0;
+  const bool done = passed<SAME>(&a.state->done) != 0;
   // where block x is now
   auto now = [&](int x) -> int {
     if (!done || x < a.keep) return x;
-    const uint32_t word = a.bits[x >> 5];
-    return word >> (x & 31) & 1u ? x : a.copy_dst[mover_rank(a, x, word)];
+    const uint32_t word = passed<SAME>(a.bits + (x >> 5));
+    return word >> (x & 31) & 1u ? x : passed<SAME>(a.copy_dst + mover_rank<SAME>(a, x, word));
   };
   for (long long x = me; x < a.num_blocks; x += threads) {
     const int to = now(static_cast<int>(x));
@@ -447,13 +454,27 @@ __global__ void __launch_bounds__(1024) compact_rank_kernel(const BlocksCompactA
 }
 __global__ void __launch_bounds__(kCompactThreads) compact_lists_kernel(const BlocksCompactArgs a) {
   compact_begin();
-  compact_lists(a, grid_thread(), grid_threads());
+  compact_lists<false>(a, grid_thread(), grid_threads());
 }
 __global__ void __launch_bounds__(kCompactThreads) compact_follow_kernel(const BlocksCompactArgs a) {
   // (the last launch: what comes behind it may read the tables before it waits, so it is not let in early)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  compact_follow(a, grid_thread(), grid_threads());
+  compact_follow<false>(a, grid_thread(), grid_threads());
 }
+// Small pools: all of it in one cluster.
+__global__ void __launch_bounds__(1024) compact_cluster_kernel(const BlocksCompactArgs a) {
+  __shared__ unsigned long long scan_ws[32], sums_s;
+  cg::cluster_group cluster = cg::this_cluster();
+  for (long long i = grid_thread(); i < (a.num_blocks + 31) / 32; i += grid_threads()) a.bits[i] = 0u;
+  cluster.sync();
+  compact_mark(a, grid_thread(), grid_threads());
+  cluster.sync();
+  compact_rank(a, scan_ws, &sums_s);
+  compact_lists<true>(a, grid_thread(), grid_threads());
+  cluster.sync();
+  compact_follow<true>(a, grid_thread(), grid_threads());
+}
+
 int blocks_for(long long items, int per_block, int per_sm) {
   const long long want = (items + per_block - 1) / per_block, full = static_cast<long long>(per_sm) * device_sm_count();
   return static_cast<int>(want < 1 ? 1 : want < full ? want : full);
@@ -511,6 +532,9 @@ cudaError_t launch_blocks_copy(const BlocksCopyArgs& a, cudaStream_t s) {
 cudaError_t launch_blocks_compact(const BlocksCompactArgs& a, cudaStream_t s) {
   const int words = (a.num_blocks + 31) / 32;
   const long long entries = static_cast<long long>(a.batch) * a.max_blocks;
+  // (one launch or five, with the tables put back before it: 4096 blocks 16.5 us both on the device, 20 and 29 from the
+  // host; 16384 blocks 18.6 both; 65536 blocks 33 and 25)
+  if (a.num_blocks <= 16384 && entries <= 65536) return launch(compact_cluster_kernel, a, 8, 0, 1024, 0, false, s);
   auto grid = [&](long long items, int per_thread) { return blocks_for(items, per_thread * kCompactThreads, 8); };
   cudaError_t e = launch(compact_clear_kernel, a, 0, grid(words, 1), kCompactThreads, 0, false, s);
   if (e == cudaSuccess) e = launch(compact_mark_kernel, a, 0, grid(a.num_blocks, 4), kCompactThreads, 0, true, s);
