@@ -28,13 +28,13 @@
 // k-th of the maxima, so that fewer steps are read again, 51.4 against 52, but with
 // fp32 logits 69.5 against 64.3 and 152 against 133 us for one request of 64 beams.)
 //
-// 512 rows of 128000 bf16 logits (one in five ended): 52 us, 2.1 TB/s; fp32 64 us,
-// 4.1 TB/s; one request of 4 x 32000: 12.4 us. The large calls are bound by instructions: 64
-// registers a thread and four blocks an SM do an exponential, a subtraction and a
-// product an element, some 22 us of the 52; the rest is the parts' ends (bound,
-// second look, ranking) and the first block's scores, which other clusters' reading
-// hides in part. The small ones are a chain of such steps, some 10 us of waits. One
-// request is one cluster, 16 blocks at most: alone with 64 beams it has a tenth of the SMs.
+// 512 rows of 128000 bf16 logits (one in five ended): 45 us, 2.3 TB/s; fp32, all
+// alive, 63 us, 4.1 TB/s; one request of 4 x 32000: 12.4 us. The large calls are bound
+// by instructions on the SMs that have four rows at once (of 128000: some 28 us; the
+// mean row takes 18), then comes a part's end (bound, second look, ranking: 5 us)
+// and the first block's scores (5), which other clusters' reading hides in part. The
+// small ones are a chain of such steps, some 10 us of waits. One request is one
+// cluster, 16 blocks at most: alone with 64 beams it has a tenth of the SMs.
 #include <cfloat>
 #include <climits>
 #include <cooperative_groups.h>
@@ -327,22 +327,25 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
       if (m > -INFINITY) {
         // (a step's terms first: fewer roundings at the sum's size)
         float2 add = make_float2(0.0f, 0.0f);
-        const float2 m2 = make_float2(-m, -m), high = make_float2(kLog2e, kLog2e), low = make_float2(kLog2eLow, kLog2eLow);
+        // exp(x - m) is 2^(x log2(e) - m'), m' = m log2(e) rounded, times what that rounding left, which all terms have in
+        // common: one rounding a term, relative to its distance from m', and of log2(e)'s own error (1.3e-8) only the
+        // part at x - m counts. (A difference first, and log2(e) in two parts, were three operations.)
+        const float top2 = m * kLog2e, left = fabsf(m) < 65536.0f ? fast_exp2(-fmaf(m, kLog2e, -top2)) : NAN;
+        const float2 log2e = make_float2(kLog2e, kLog2e), less = make_float2(-top2, -top2);
 #pragma unroll
         for (int u = 0; u < kVecs; ++u) {
           float2 x[E / 2];
           L::unpack(v[u], x);
 #pragma unroll
           for (int e = 0; e < E / 2; ++e) {
-            const float2 d = __fadd2_rn(x[e], m2);
-            float2 p = __ffma2_rn(d, low, __fmul2_rn(d, high));
+            float2 p = __ffma2_rn(x[e], log2e, less);
             p.x = fast_exp2(p.x);
             p.y = fast_exp2(p.y);
             add = __fadd2_rn(add, p);
           }
         }
-        float sum = add.x + add.y;
-        if (infinite || sum != sum) {  // infinities and NaN, as their values count
+        float sum = (add.x + add.y) * left;
+        if (infinite || sum != sum) {  // infinities and NaN, as their values count; a maximum of any size
           sum = 0.0f;
 #pragma unroll
           for (int u = 0; u < kVecs; ++u) {
@@ -641,7 +644,11 @@ cudaError_t launch_select(const BeamSelectArgs& a, cudaStream_t s) {
   cudaError_t e = once.set(kern, kMostShared);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr;
+  cudaLaunchAttribute attrs[2];
+  cudaLaunchAttribute& attr = attrs[0];
+  // (ended beams leave blocks idle: SMs with fewer busy ones take the next cluster; 52 -> 48 us with one beam in five ended)
+  attrs[1].id = cudaLaunchAttributeClusterSchedulingPolicyPreference;
+  attrs[1].val.clusterSchedulingPolicyPreference = cudaClusterSchedulingPolicyLoadBalancing;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = 16;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
@@ -649,7 +656,7 @@ cudaError_t launch_select(const BeamSelectArgs& a, cudaStream_t s) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kMostShared;
   cfg.stream = s;
-  cfg.attrs = &attr;
+  cfg.attrs = attrs;
   cfg.numAttrs = 1;
   // clusters of 16 blocks, asked for once per device: 1 they fit, -1 they do not (8 are the portable most)
   static std::atomic<int> fits[SharedMemoryOnce::kDevices] = {};
@@ -669,6 +676,7 @@ cudaError_t launch_select(const BeamSelectArgs& a, cudaStream_t s) {
   attr.val.clusterDim.x = p.ranks;
   cfg.gridDim = dim3(static_cast<unsigned>(a.groups) * p.ranks);
   cfg.dynamicSmemBytes = p.smem;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, kern, a, p.splits);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -131,6 +131,16 @@ def test_select_infinities_and_signed_zeros(kind):
     assert np.array_equal(t, want[2]) and np.allclose(s, want[0], atol=1e-5)
 
 
+@pytest.mark.parametrize("at", [-65536.0, -1e6, 30000.0, 65000.0, 65536.0, 1e6, 1e30, 3e38])
+def test_select_of_large_logits(at):
+    """Rows far from zero, as a whole and from their middle on: a difference of logits stays exact."""
+    rng = np.random.default_rng(11)
+    x = rng.integers(-8, 8, (6, 30000)).astype(np.float32)
+    x[:3] += np.float32(at)
+    x[3:, 15000:] += np.float32(at)
+    check_select(dev(x), rng.uniform(-9, 0, (2, 3)).astype(np.float32), 5)
+
+
 @pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("order", ["equal", "rising", "falling", "steps"])
 def test_select_of_rows_that_fill_the_lists(kind, order):
