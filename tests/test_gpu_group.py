@@ -223,6 +223,27 @@ def test_group_bad_tables_and_lengths_stay_inside():
         assert int(ws[:4].view(torch.int32).item()) == 0
 
 
+@pytest.mark.parametrize("gq", [2, 8, 32])
+def test_group_pool_beyond_31_bits(gq):
+    """The same blocks at the end of pools of 2.3 GB each: the same bits."""
+    import torch
+    _, kvq, _ = _mods()
+    rng = np.random.default_rng(19)
+    p, table, lens = make_case(rng, 4, [40, 3], [5, 60, 0, 9, None, 3, 100, 1], 8, 128)
+    q = rng.standard_normal((8, 8 * gq, 128)).astype(np.float16)
+    want = run_group(p, table, lens, [40, 3], 4, q, False)
+    blocks, few = 140000, p.nat[0].shape[0]
+
+    class Large:
+        pool = [kvq.Fp8Pool(o.desc.role, blocks, 8, 128, kvq.FP8_FORMATS["e4m3"], False) for o in p.pool]
+        descs = pool[0].desc, pool[1].desc
+
+    for old, new in zip(p.pool, Large.pool):
+        new.scale.copy_(old.scale)
+        new.view()[blocks - few:].copy_(old.view())
+    assert np.array_equal(run_group(Large, np.where(table < 0, table, table + blocks - few), lens, [40, 3], 4, q, False), want)
+
+
 @pytest.mark.parametrize("width,gq,wide", [(4, 4, False), (4, 8, False), (8, 8, False), (8, 8, True), (16, 16, False)])
 def test_group_many_calls_give_the_same_bits(width, gq, wide):
     import torch
