@@ -329,8 +329,10 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
         float2 add = make_float2(0.0f, 0.0f);
         // exp(x - m) is 2^(x log2(e) - m'), m' = m log2(e) rounded, times what that rounding left, which all terms have in
         // common: one rounding a term, relative to its distance from m', and of log2(e)'s own error (1.3e-8) only the
-        // part at x - m counts. (A difference first, and log2(e) in two parts, were three operations.)
-        const float top2 = m * kLog2e, left = fabsf(m) < 65536.0f ? fast_exp2(-fmaf(m, kLog2e, -top2)) : NAN;
+        // part at x - m counts. (A difference first, and log2(e) in two parts, were three operations.) What is left is
+        // exp(y), |y| < 2^-8 below 65536: the series' next term is below 2^-26.
+        const float top2 = m * kLog2e, y = -0.693147181f * fmaf(m, kLog2e, -top2);
+        const float left = fabsf(m) < 65536.0f ? 1.0f + fmaf(0.5f * y, y, y) : NAN;
         const float2 log2e = make_float2(kLog2e, kLog2e), less = make_float2(-top2, -top2);
 #pragma unroll
         for (int u = 0; u < kVecs; ++u) {
