@@ -21,12 +21,15 @@ constexpr int kBlock = 16;  // tokens of an FP8 pool block
 // normal fp16 numbers.
 //
 // 8 x 4 sequences over 32K shared tokens (16 rows a kv head, 128 channels): 113 us
-// with the joining, 4.8 TB/s; 64 own sequences of 8K tokens 197 us, 5.4 TB/s; lengths of
-// all kinds with 64 channels 86 us, 3.0 TB/s. The pipes are at some 30 %: it is
-// the chain scores - maximum - exponentials - products of three blocks of four
-// warps an SM (64 channels: four blocks) that bounds it. Six stages (92 us instead of 86) and five blocks an
-// SM at 96 registers (96) cost more than they hide; bulk copies and barriers for
-// all four warps took 94.
+// with the joining, 4.8 TB/s; 64 own sequences of 8K tokens 197 us, 5.4 TB/s;
+// lengths of all kinds with 64 channels 84 us, 3.1 TB/s. Long segments run at the
+// memory's rate; what is added to that are each wave's start (3 us of plan, then
+// three dependent reads: request, table, block, some 5 us, which a thread block
+// has at every segment) and the waves' last thread blocks, which end 10 us after
+// the mean. Six stages (92 us in place of 86) and five blocks an SM at 96
+// registers (96) cost more than they hide; bulk copies and barriers for all four
+// warps took 94, cuts that keep off a pair's ends by 1 or 2 units in place of 4
+// the same or 2 us more.
 // ---------------------------------------------------------------------------
 constexpr int kRows = kGroupRows16;
 constexpr int kUnit = 64;    // tokens of a unit: one block a warp
@@ -36,6 +39,10 @@ constexpr float kBias = 10.0f;
 template <int D>
 struct GroupSmem {
   static constexpr int STAGE = 2 * kBlock * D;
+  // blocks a warp takes at a time: with 64 channels there are registers for two, which share a maximum and its shuffles
+  // (lengths of all kinds 86 -> 84 us; long segments alone as before)
+  static constexpr int AT_ONCE = D == 64 ? 2 : 1;
+  static_assert(kStages % AT_ONCE == 0, "the blocks taken at once lie behind each other in the ring");
   static constexpr int RING = 4 * kStages * STAGE;
   static constexpr int COMBINE = 4 * kRows * (D + 2) * 4;
   static constexpr int AREA = RING > COMBINE ? RING : COMBINE;
@@ -51,7 +58,7 @@ __device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddep
 template <int D, int FMT>
 __global__ void __launch_bounds__(128) group_rows16_kernel(const __grid_constant__ GroupArgs a) {
   using S = GroupSmem<D>;
-  constexpr int KS = D / 16, NT = D / 8, CH = D / 32;
+  constexpr int KS = D / 16, NT = D / 8, CH = D / 32, AT = S::AT_ONCE;
   let_next_in();
   const int kind = a.kinds == 3 ? static_cast<int>(blockIdx.y) : a.kinds - 1;  // (shared pairs first: they are the long ones)
   if (static_cast<int>(blockIdx.x) >= a.blocks[kind]) {
@@ -110,10 +117,9 @@ __global__ void __launch_bounds__(128) group_rows16_kernel(const __grid_constant
     auto phys = [&](int j) -> long long {
       return j < n_mine ? min(max(table[j_begin + first + step * j], 0), a.num_blocks - 1) : 0;
     };
-    auto issue = [&](int j, long long blk) {
+    auto issue = [&](int j, long long blk, uint8_t* dst) {
       if (j < n_mine) {
         const long long off = (blk * a.kv_heads + h) * (kBlock * D) + lane * 16;
-        uint8_t* dst = ring + j % kStages * S::STAGE;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           cp_async16(dst + c * 512, a.k_pool + off + c * 512);
@@ -127,9 +133,11 @@ __global__ void __launch_bounds__(128) group_rows16_kernel(const __grid_constant
 #pragma unroll
       for (int j = 0; j < kStages; ++j) blk[j] = phys(j);
 #pragma unroll
-      for (int j = 0; j < kStages; ++j) issue(j, blk[j]);
+      for (int j = 0; j < kStages; ++j) issue(j, blk[j], ring + j * S::STAGE);
     }
-    long long next_blk = phys(kStages);
+    long long next_blk[AT];
+#pragma unroll
+    for (int b = 0; b < AT; ++b) next_blk[b] = phys(kStages + b);
 
     // query rows g and g + 8 of the tile, A fragments of m16n8k16
     uint32_t qa[KS][4];
@@ -153,59 +161,70 @@ __global__ void __launch_bounds__(128) group_rows16_kernel(const __grid_constant
 #pragma unroll
     for (int i = 0; i < NT; ++i) o_acc[i][0] = o_acc[i][1] = o_acc[i][2] = o_acc[i][3] = 0.0f;
 
-    for (int j = 0; j < n_mine; ++j) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-      const uint8_t* kb = ring + j % kStages * S::STAGE;
-      const uint8_t* vb = kb + kBlock * D;
-      const int tok_base = (j_begin + first + step * j) * kBlock;
-      uint32_t kw[2 * KS];
+    for (int j = 0; j < n_mine; j += AT) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - AT) : "memory");
+      uint8_t* const here = ring + j % kStages * S::STAGE;
+      // scores of rows g (sc[0]) and g + 8 (sc[1]): tokens 2tig, 2tig + 1, 8 + 2tig, 9 + 2tig of each block
+      float sc[2][4 * AT];
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const uint4 x = *reinterpret_cast<const uint4*>(kb + c * 512);
-        kw[4 * c] = x.x;
-        kw[4 * c + 1] = x.y;
-        kw[4 * c + 2] = x.z;
-        kw[4 * c + 3] = x.w;
-      }
-      float sacc[2][4];
+      for (int b = 0; b < AT; ++b) {
+        const uint8_t* kb = here + b * S::STAGE;
+        uint32_t kw[2 * KS];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        sacc[nt][0] = sacc[nt][1] = sacc[nt][2] = sacc[nt][3] = 0.0f;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const uint32_t w = kw[nt * KS + ks];
-          mma16816(sacc[nt], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], fp8_lo_pair<FMT>(w), fp8_hi_pair<FMT>(w));
+        for (int c = 0; c < CH; ++c) {
+          const uint4 x = *reinterpret_cast<const uint4*>(kb + c * 512);
+          kw[4 * c] = x.x;
+          kw[4 * c + 1] = x.y;
+          kw[4 * c + 2] = x.z;
+          kw[4 * c + 3] = x.w;
         }
-      }
-      uint32_t vw[NT];
+        float sacc[2][4];
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const uint4 x = *reinterpret_cast<const uint4*>(vb + c * 512);
-        vw[4 * c] = x.x;
-        vw[4 * c + 1] = x.y;
-        vw[4 * c + 2] = x.z;
-        vw[4 * c + 3] = x.w;
-      }
-      // scores of rows g (sc[0]) and g + 8 (sc[1]): tokens 2tig, 2tig + 1, 8 + 2tig, 9 + 2tig
-      float sc[2][4];
+        for (int nt = 0; nt < 2; ++nt) {
+          sacc[nt][0] = sacc[nt][1] = sacc[nt][2] = sacc[nt][3] = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[e][i] = sacc[i >> 1][2 * e + (i & 1)] * kmul;
-      if (tree_beyond(tok_base, kBlock, total)) {  // rows of the block behind the last token: not seen, values as 0
-        uint32_t keep = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (tok_base + 8 * (i >> 1) + 2 * tig + (i & 1) < total) keep |= 0xFFu << (8 * i);
-          else sc[0][i] = sc[1][i] = -INFINITY;
+          for (int ks = 0; ks < KS; ++ks) {
+            const uint32_t w = kw[nt * KS + ks];
+            mma16816(sacc[nt], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], fp8_lo_pair<FMT>(w), fp8_hi_pair<FMT>(w));
+          }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) vw[nt] &= keep;
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[e][4 * b + i] = sacc[i >> 1][2 * e + (i & 1)] * kmul;
       }
-      uint32_t A[4], L[4];
+      uint32_t vw[AT][NT];
+#pragma unroll
+      for (int b = 0; b < AT; ++b) {
+        const uint8_t* vb = here + b * S::STAGE + kBlock * D;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const uint4 x = *reinterpret_cast<const uint4*>(vb + c * 512);
+          vw[b][4 * c] = x.x;
+          vw[b][4 * c + 1] = x.y;
+          vw[b][4 * c + 2] = x.z;
+          vw[b][4 * c + 3] = x.w;
+        }
+        // rows of the block behind the last token, and of a block that the warp does not have: not seen, values as 0
+        const int tok_base = j + b < n_mine ? (j_begin + first + step * (j + b)) * kBlock : total;
+        if (tree_beyond(tok_base, kBlock, total)) {
+          uint32_t keep = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (tok_base + 8 * (i >> 1) + 2 * tig + (i & 1) < total) keep |= 0xFFu << (8 * i);
+            else sc[0][4 * b + i] = sc[1][4 * b + i] = -INFINITY;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) vw[b][nt] &= keep;
+        }
+      }
+      uint32_t A[AT][4], L[AT][4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float mx = quad_max(fmaxf(fmaxf(sc[e][0], sc[e][1]), fmaxf(sc[e][2], sc[e][3])));
+        float mx = fmaxf(fmaxf(sc[e][0], sc[e][1]), fmaxf(sc[e][2], sc[e][3]));
+#pragma unroll
+        for (int i = 4; i < 4 * AT; i += 2) mx = fmaxf(mx, fmaxf(sc[e][i], sc[e][i + 1]));
+        mx = quad_max(mx);
         const float m_new = fmaxf(m_run[e], mx);
         if (m_new != m_run[e]) {
           const float alpha = fast_exp2(m_run[e] - m_new);
@@ -218,26 +237,34 @@ __global__ void __launch_bounds__(128) group_rows16_kernel(const __grid_constant
           m_run[e] = m_new;
         }
         const float sub = (m_new == -INFINITY ? 0.0f : m_new) - kBias;
-        float p[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = fast_exp2(sc[e][i] - sub);
-        l_run[e] += (p[0] + p[1]) + (p[2] + p[3]);
-        const __half2 h0 = __floats2half2_rn(p[0], p[1]), h1 = __floats2half2_rn(p[2], p[3]);
-        A[e] = h2_bits(h0);
-        A[2 + e] = h2_bits(h1);
-        const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-        L[e] = pack_rn_f16x2(p[0] - f0.x, p[1] - f0.y);
-        L[2 + e] = pack_rn_f16x2(p[2] - f1.x, p[3] - f1.y);
+        for (int b = 0; b < AT; ++b) {
+          float p[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[i] = fast_exp2(sc[e][4 * b + i] - sub);
+          l_run[e] += (p[0] + p[1]) + (p[2] + p[3]);
+          const __half2 h0 = __floats2half2_rn(p[0], p[1]), h1 = __floats2half2_rn(p[2], p[3]);
+          A[b][e] = h2_bits(h0);
+          A[b][2 + e] = h2_bits(h1);
+          const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+          L[b][e] = pack_rn_f16x2(p[0] - f0.x, p[1] - f0.y);
+          L[b][2 + e] = pack_rn_f16x2(p[2] - f1.x, p[3] - f1.y);
+        }
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const uint32_t b0 = fp8_lo_pair<FMT>(vw[nt]), b1 = fp8_hi_pair<FMT>(vw[nt]);
-        mma16816(o_acc[nt], A[0], A[1], A[2], A[3], b0, b1);
-        mma16816(o_acc[nt], L[0], L[1], L[2], L[3], b0, b1);
-      }
+      for (int b = 0; b < AT; ++b)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t b0 = fp8_lo_pair<FMT>(vw[b][nt]), b1 = fp8_hi_pair<FMT>(vw[b][nt]);
+          mma16816(o_acc[nt], A[b][0], A[b][1], A[b][2], A[b][3], b0, b1);
+          mma16816(o_acc[nt], L[b][0], L[b][1], L[b][2], L[b][3], b0, b1);
+        }
       // (the lane has used what it read there)
-      issue(j + kStages, next_blk);
-      next_blk = phys(j + kStages + 1);
+#pragma unroll
+      for (int b = 0; b < AT; ++b) {
+        issue(j + b + kStages, next_blk[b], here + b * S::STAGE);
+        next_blk[b] = phys(j + AT + b + kStages);
+      }
     }
     l_run[0] = quad_sum(l_run[0]);
     l_run[1] = quad_sum(l_run[1]);
