@@ -54,7 +54,8 @@ extern "C" {
  *                 elements of the type that logits_type names; row_stride >=
  *                 vocab (rows need no alignment beyond their type's)
  *   scores      : device float32 [groups * width]; a value that is not finite
- *                 makes the beam a dead one: all its candidates score -inf
+ *                 makes the beam a dead one, ended or not: all its candidates
+ *                 score -inf
  *   finished    : device uint8 [groups * width] or NULL; a beam that has ended
  *                 (not 0) offers (end_token, scores[i]) alone, its other tokens
  *                 score -inf and its logits are not read

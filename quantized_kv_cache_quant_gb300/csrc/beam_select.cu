@@ -214,7 +214,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
     const long long row = static_cast<long long>(group) * a.width + i;
     const float score = a.scores[row];
     sh.score[i] = isfinite(score) ? score : -INFINITY;
-    sh.kind[i] = a.finished != nullptr && a.finished[row] != 0 ? kEnded : isfinite(score) ? kLive : kDead;
+    // (a beam without a finite score is a dead one, ended or not: its tokens go by their index)
+    sh.kind[i] = !isfinite(score) ? kDead : a.finished != nullptr && a.finished[row] != 0 ? kEnded : kLive;
   }
   __syncthreads();
   bool all_run = false;

@@ -1,0 +1,72 @@
+"""Beam selection, candidate by candidate: which one stands at each place, and how far its score is from 64 bits."""
+import numpy as np
+import pytest
+
+from kvq_helpers import host
+from test_gpu_beam import TYPES, run_select
+
+pytestmark = pytest.mark.gpu
+
+LOG = 2.0**-18   # what the logarithm of a row's sum may be off by
+FP32_MAX = float(np.finfo(np.float32).max)
+
+
+def row_totals(x, scores, finished, end):
+    """Scores of all candidates in 64 bits [R, W, V], and the logits as they count."""
+    r, w = scores.shape
+    x = host(x.float()).astype(np.float64).reshape(r, w, -1)
+    x = np.minimum(np.where(np.isnan(x), -np.inf, x), FP32_MAX)
+    total = np.full(x.shape, -np.inf)
+    for g, i in np.ndindex(r, w):
+        s = float(scores[g, i])
+        if not np.isfinite(s):
+            continue
+        if finished is not None and finished[g, i]:
+            total[g, i, end] = s
+        elif x[g, i].max() > -np.inf:
+            d = x[g, i] - x[g, i].max()
+            total[g, i] = s + (d - np.log(np.exp(d).sum()))
+    return total, x
+
+
+def check_exactly(x, scores, n, finished=None, end=-1):
+    """Every place's candidate: those of one beam are its best ones in the order of their logits, equal ones by the token;
+    candidates at -inf come last, by their index; beams are interleaved by scores that 64 bits give, but where two are
+    closer than what the logarithms and the outputs' rounding (2^-24 of their size) leave."""
+    s, p, t = run_select(x, scores, n, finished, end)
+    total, x = row_totals(x, scores, finished, end)
+    r, w, v = total.shape
+    for g in range(r):
+        own = total[g, p[g], t[g]]
+        fin = np.isfinite(own)
+        k = int(min(n, np.isfinite(total[g]).sum()))
+        assert fin[:k].all() and not fin[k:].any()
+        off = LOG + 2.0**-24 * np.abs(own[:k])
+        assert (np.abs(s[g, :k] - own[:k]) <= off).all() and (s[g, k:] == -np.inf).all()
+        assert (np.diff(s[g, :k]) <= 0).all()
+        for i in range(w):
+            got = t[g, :k][p[g, :k] == i]
+            order = np.lexsort((np.arange(v), -x[g, i], -total[g, i]))[: len(got)]
+            assert np.array_equal(got, order), (g, i, got, order)
+        # what stands at a place is no worse than the best of what comes behind it, the candidates left out among them
+        best = np.sort(total[g].ravel())[::-1][:k]
+        assert (np.abs(own[:k] - best) <= 2 * LOG).all()
+        flat = np.flatnonzero(np.isneginf(total[g].ravel()))[: n - k]
+        assert np.array_equal(p[g, k:] * v + t[g, k:], flat)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("w,n", [(1, 3), (2, 9), (3, 16), (40, 20)])
+@pytest.mark.parametrize("score", [-np.inf, np.inf, np.nan])
+def test_select_ended_beams_without_a_finite_score(kind, w, n, score):
+    """They are dead beams: their tokens go by their index, the end token among them."""
+    import torch
+    rng = np.random.default_rng(w)
+    v, end = 300, 7
+    x = torch.full((2 * w, v), -float("inf"), dtype=getattr(torch, kind), device="cuda")
+    x[:, 5], x[:, 200] = 1.0, 3.0
+    scores = rng.uniform(-9, 0, (2, w)).astype(np.float32)
+    finished = rng.random((2, w)) < 0.3
+    scores[:, 0], finished[:, 0] = score, True
+    scores[1], finished[1] = score, True
+    check_exactly(x, scores, n, finished, end)
