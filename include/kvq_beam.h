@@ -49,7 +49,8 @@ extern "C" {
 
 /* The n_out best candidates (beam i, token t) of each request by
  *   score(i, t) = scores[i] + logits[i, t] - log(sum_u exp(logits[i, u])),
- * best first, equal scores by the lower i * vocab + t:
+ * best first, those of one beam in the order of their logits, equal logits by the
+ * lower t, equal scores of different beams by the lower i:
  *   logits      : device, row b at logits + b * row_stride elements, vocab
  *                 elements of the type that logits_type names; row_stride >=
  *                 vocab (rows need no alignment beyond their type's)
@@ -64,8 +65,8 @@ extern "C" {
  *   out_parents : device int32 [groups, n_out], i, the beam within its request
  *   out_tokens  : device int32 [groups, n_out], t
  * A NaN logit counts as -inf and +inf as the largest float32; a token at -inf
- * scores -inf, and candidates at -inf fill up what finite ones leave, by their
- * index. Candidates of one beam are ordered by their logits. Sums are float32
+ * scores -inf, and candidates at -inf fill up what finite ones leave, by the
+ * lower i * vocab + t. Sums are float32
  * within a thread (some hundred terms, relative to the thread's maximum) and
  * whole numbers beyond; the logarithm of a sum is off by some 2^-23. Scores are
  * compared in float64 and rounded once. A row gives the same wherever it starts,

@@ -58,8 +58,10 @@ def beam_select(logits, scores, out_scores, out_parents, out_tokens, finished=No
     """The best candidates of each request by scores[i] + log_softmax(logits[i])[t].
     logits fp16, fp32 or bf16 [R * W, V] (rows may lie apart), scores fp32 [R, W];
     writes out_scores fp32, out_parents int32 (i) and out_tokens int32 (t), each
-    [R, n]: best first, equal scores by the lower i * V + t. finished bool or
-    uint8 [R, W] or None: beams that have ended offer (end_token, scores[i])."""
+    [R, n]: best first, those of one beam in the order of their logits, equal
+    logits by the lower t, equal scores of different beams by the lower i.
+    finished bool or uint8 [R, W] or None: beams that have ended offer
+    (end_token, scores[i])."""
     d = _here(logits)
     if logits.dtype not in LOGITS:
         raise TypeError(f"logits: fp16, fp32 or bf16 expected, not {logits.dtype}")

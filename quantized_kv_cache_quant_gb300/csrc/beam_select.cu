@@ -54,6 +54,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kVecs = 4;                       // 16-byte vectors a thread holds of a warp's 2 KB
 constexpr int kStep = 32 * kVecs;              // vectors of them
 constexpr int kMaxParts = 128;                 // parts of a request: four heads a lane
+constexpr int kMaxSplits = 32;                 // parts of a row: a lane's heads, 32 parts apart, are of different beams
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLog2eLow = 1.925963033500e-8f;  // log2(e) - kLog2e
 constexpr unsigned long long kNone = 0ull;     // no key: below every one (a key's low half is never 0)
@@ -189,6 +190,63 @@ __device__ __noinline__ void cut_list(const unsigned long long* from, int n, int
     if (larger < k) to[larger] = key;
   }
   __syncwarp();
+}
+
+// The k best candidates where scores of different logits of one beam may have rounded to one number: a row's parts are cut
+// by the size of the call, so that in such a beam the keys decide and not the lists' order. By warp 0 of the first block.
+__device__ __noinline__ void put_by_keys(int parts, int splits, int k, float* out_scores, int32_t* out_parents, int32_t* out_tokens) {
+  extern __shared__ __align__(16) uint8_t dyn[];
+  const unsigned long long* lists = reinterpret_cast<const unsigned long long*>(dyn + parts * sizeof(PartSum));
+  const unsigned long long* code = reinterpret_cast<const unsigned long long*>(dyn + list_bytes(parts, k));
+  const int* token = reinterpret_cast<const int*>(code + parts * k);
+  const int lane = threadIdx.x & 31, beam_keys = splits * k;
+  auto put = [&](int o, int i) {  // candidate i is the o-th best
+    const unsigned long long u = code[i];
+    const double x = __longlong_as_double(static_cast<long long>(u >> 63 ? u & ~(1ull << 63) : ~u));
+    out_scores[o] = static_cast<float>(x);
+    out_parents[o] = i / k / splits;
+    out_tokens[o] = token[i];
+  };
+  // lane l's lists are l, l + 32, ...: a head each
+  constexpr int kLists = kMaxParts / 32;
+  int at[kLists];
+#pragma unroll
+  for (int q = 0; q < kLists; ++q) at[q] = 0;
+  for (int o = 0; o < k; ++o) {
+    unsigned long long best = 0ull;
+    int best_q = 0, best_at = INT_MAX;
+#pragma unroll
+    for (int q = 0; q < kLists; ++q) {
+      const int part = lane + 32 * q;
+      if (part >= parts || at[q] >= k) continue;
+      const unsigned long long c = code[part * k + at[q]];
+      if (c > best) {
+        best = c;
+        best_q = q;
+        best_at = part * k + at[q];
+      }
+    }
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(best >> 32));
+    const bool in_hi = static_cast<uint32_t>(best >> 32) == hi;
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, in_hi ? static_cast<uint32_t>(best) : 0u);
+    uint32_t who = __ballot_sync(0xffffffffu, in_hi && static_cast<uint32_t>(best) == lo && best != 0ull);
+    if (who & (who - 1)) {  // (a lane's own lists are of different beams, and it has the lower one)
+      const bool tie = who >> lane & 1u;
+      const uint32_t beam = tie ? best_at / beam_keys : 0xffffffffu, low_beam = __reduce_min_sync(0xffffffffu, beam);
+      const bool lowest = tie && beam == low_beam;
+      const unsigned long long key = lowest ? lists[best_at] : kNone;
+      const uint32_t key_hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(key >> 32));
+      const bool in_key = lowest && static_cast<uint32_t>(key >> 32) == key_hi;
+      const uint32_t key_lo = __reduce_max_sync(0xffffffffu, in_key ? static_cast<uint32_t>(key) : 0u);
+      who = __ballot_sync(0xffffffffu, in_key && static_cast<uint32_t>(key) == key_lo);
+    }
+    if (who >> lane & 1u) {
+      put(o, best_at);
+#pragma unroll
+      for (int q = 0; q < kLists; ++q) at[q] += q == best_q;
+    }
+    __syncwarp();
+  }
 }
 
 template <int TYPE>
@@ -521,6 +579,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
     row_max[beam] = most;
   }
   __syncthreads();
+  bool by_keys = false;
   for (int i = tid; i < parts * k; i += kThreads) {
     const int part = i / k, at = i % k, beam = part / splits;
     const float score = sh.score[beam];
@@ -538,6 +597,9 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
       if (key != kNone) {
         const float x = code_float(static_cast<uint32_t>(key >> 32));
         t = key_token(key);
+        // Two float32 x differ by 2^-24 of the larger one; where that is more than the roundings of a score (three, of 2^-53
+        // of what it is made of), their scores differ too.
+        by_keys |= fabsf(x) * 0x1p26f < fabsf(x - row_max[beam]) + fabsf(score) + fabsf(static_cast<float>(log_sum[beam]));
         c = score_code(x == -INFINITY ? -INFINITY
                                       : static_cast<double>(score) + ((static_cast<double>(x) - static_cast<double>(row_max[beam])) - log_sum[beam]));
       }
@@ -545,7 +607,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
     code[i] = c;
     token[i] = t;
   }
-  __syncthreads();
+  if (__syncthreads_or(by_keys)) {
+    const long long to = static_cast<long long>(group) * k;
+    if (warp == 0) put_by_keys(parts, splits, k, a.out_scores + to, a.out_parents + to, a.out_tokens + to);
+    return;
+  }
   auto put = [&](int o, int i) {  // candidate i is the o-th best
     const unsigned long long u = code[i];
     const double x = __longlong_as_double(static_cast<long long>(u >> 63 ? u & ~(1ull << 63) : ~u));
@@ -554,7 +620,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
     a.out_parents[to] = i / k / splits;
     a.out_tokens[to] = token[i];
   };
-  // Equal scores: the lower beam, then the lower token (the lists' order: parts of a row go up in tokens).
+  // Equal scores: the lower beam, then the lower token, as the logits are equal (the lists' order: parts of a row go up in
+  // tokens).
   const int total = parts * k;
   if (total <= kThreads) {
     // few: eight threads count those before a candidate
@@ -627,7 +694,7 @@ SelectPlan plan_select(const BeamSelectArgs& a, int size, int most_ranks) {
   int ranks = 1;
   while (ranks < most_ranks && static_cast<long long>(a.groups) * ranks * 2 <= 4ll * device_sm_count()) ranks *= 2;
   long long best_cost = LLONG_MAX;
-  for (int splits = 1; splits <= 32 && a.width * splits <= kMaxParts; ++splits) {
+  for (int splits = 1; splits <= kMaxSplits && a.width * splits <= kMaxParts; ++splits) {
     const int parts = a.width * splits;
     const long long rounds = (parts + ranks - 1) / ranks;
     const long long cost = rounds * (static_cast<long long>(a.vocab) * size / splits + fixed);

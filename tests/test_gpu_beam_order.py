@@ -70,3 +70,16 @@ def test_select_ended_beams_without_a_finite_score(kind, w, n, score):
     scores[:, 0], finished[:, 0] = score, True
     scores[1], finished[1] = score, True
     check_exactly(x, scores, n, finished, end)
+
+
+@pytest.mark.parametrize("kind", ["float32", "bfloat16"])
+@pytest.mark.parametrize("w,n", [(1, 2), (1, 3), (1, 128), (3, 5), (2, 100)])
+def test_select_orders_a_beam_by_its_logits(kind, w, n):
+    """Logits so near to one another that their scores are equal in 64 bits, the larger ones further back in the row."""
+    import torch
+    v = 64000
+    x = torch.full((w, v), -1.0, dtype=getattr(torch, kind), device="cuda")
+    x[:, 31] = 30.0
+    at = torch.arange(100, device="cuda") * 601 + 7
+    x[:, at] = (torch.arange(100, device="cuda") + 1).to(x.dtype) * 2.0**-80
+    check_exactly(x, np.zeros((1, w), np.float32), n)
