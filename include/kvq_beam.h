@@ -66,11 +66,10 @@ extern "C" {
  *   out_tokens  : device int32 [groups, n_out], t
  * A NaN logit counts as -inf and +inf as the largest float32; a token at -inf
  * scores -inf, and candidates at -inf fill up what finite ones leave, by the
- * lower i * vocab + t. Sums are float32
- * within a thread (some hundred terms, relative to the thread's maximum) and
- * whole numbers beyond; the logarithm of a sum is off by some 2^-23. Scores are
- * compared in float64 and rounded once. A row gives the same wherever it starts,
- * and the same call the same bits.
+ * lower i * vocab + t. Sums are float32 within a thread (at most 64 additions
+ * one after the other, of 16 or 32 terms each), float64 or whole numbers beyond.
+ * Scores are compared in float64 and rounded once. A row gives the same wherever
+ * it starts, and the same call the same bits.
  * One launch. KVQ_ERR_UNSUPPORTED for width > KVQ_BEAM_MAX_WIDTH or n_out >
  * KVQ_BEAM_MAX_OUT, KVQ_ERR_ARG for n_out > vocab. */
 KVQ_API kvq_status beam_select(const void* logits, int32_t logits_type, int64_t row_stride, const float* scores,

@@ -9,7 +9,8 @@
 // or 4 elements together from two of them, so that a row's sum does not depend on
 // where the row lies.
 //   sum    every thread keeps a maximum and a sum of exp(x - maximum) of its own
-//          (fp32, rescaled when the maximum grows); they meet at the part's end
+//          (fp32, rescaled when the maximum grows, with many steps folded into
+//          fp64); they meet at the part's end
 //   best   within a row the order of the scores is that of the logits, so a part
 //          needs its k = n_out largest logits only. A value that k of the threads'
 //          maxima reach is one that at least k elements reach, and only the threads
@@ -55,6 +56,7 @@ constexpr int kVecs = 4;                       // 16-byte vectors a thread holds
 constexpr int kStep = 32 * kVecs;              // vectors of them
 constexpr int kMaxParts = 128;                 // parts of a request: four heads a lane
 constexpr int kMaxSplits = 32;                 // parts of a row: a lane's heads, 32 parts apart, are of different beams
+constexpr int kFold = 64;                      // steps whose terms a thread adds up in float32
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLog2eLow = 1.925963033500e-8f;  // log2(e) - kLog2e
 constexpr unsigned long long kNone = 0ull;     // no key: below every one (a key's low half is never 0)
@@ -154,6 +156,11 @@ struct SelectShared {
   float score[kBeamMaxWidth];
   uint8_t kind[kBeamMaxWidth];  // of each beam
 };
+// Each thread's sum of the steps folded so far, relative to the maximum then.
+struct LongSums {
+  double sum[kThreads];
+  float max[kThreads];
+};
 constexpr uint8_t kLive = 0, kDead = 1, kEnded = 2;
 
 // exp(x - m) for x <= m: d = x - m rounds relative to d alone, and log2(e) in two parts keeps the product's
@@ -161,6 +168,18 @@ constexpr uint8_t kLive = 0, kDead = 1, kEnded = 2;
 __device__ __forceinline__ float exp_below(float x, float m) {
   const float d = x - m;
   return fast_exp2(fmaf(d, kLog2eLow, d * kLog2e));
+}
+
+// A thread's sum s of exp(x - m) joins that of its steps before. Out of line: seldom called, and in fp64.
+__device__ __noinline__ void fold_sum(LongSums& sums, float s, float m) {
+  const int tid = threadIdx.x;
+  if (m == -INFINITY) return;
+  const float before = sums.max[tid];
+  if (before < m) {
+    sums.sum[tid] = before == -INFINITY ? 0.0 : sums.sum[tid] * exp(static_cast<double>(before) - static_cast<double>(m));
+    sums.max[tid] = m;
+  }
+  sums.sum[tid] += static_cast<double>(s);
 }
 
 // The k largest keys of list[0, n) to out[0, k), largest first (kNone behind the n-th): eight threads count those above a
@@ -249,12 +268,17 @@ __device__ __noinline__ void put_by_keys(int parts, int splits, int k, float* ou
   }
 }
 
-template <int TYPE>
+// LONG: some part has more than kFold steps (rows of 262144 float32 logits and more). A sum of so many terms would drift, by
+// up to 2^-24 of it at each addition (a row of 2^22 equal logits but for every fourth: 1.5e-5), so these threads fold theirs
+// into fp64 every kFold steps. A kernel of its own: the other one has no registers for it (45 us with 64 x 8 x 128000 bf16
+// logits, 48 with the fold in the same loop).
+template <int TYPE, bool LONG>
 __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSelectArgs a, int splits) {
   using L = Logits<TYPE>;
   constexpr int E = 16 / L::SIZE;  // elements of a vector
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ SelectShared sh;
+  __shared__ LongSums folded;
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
   const int group = blockIdx.x / ranks, k = a.n_out, parts = a.width * splits;
@@ -363,6 +387,10 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
     float m = -INFINITY, s = 0.0f;  // of this thread
     float second = -INFINITY;       // the largest element of its steps but the one with the maximum,
     int at = v1;                    // whose first vector (lane 0's) this is
+    if constexpr (LONG) {
+      folded.sum[tid] = 0.0;
+      folded.max[tid] = -INFINITY;
+    }
     Step next;
     int c = v0 + warp * kStep;
     if (c < v1) load(c, next);
@@ -418,7 +446,14 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
         }
         s += sum;
       }
+      if constexpr (LONG) {
+        if ((c - v0) / (kWarps * kStep) % kFold == kFold - 1) {
+          fold_sum(folded, s, m);
+          s = 0.0f;
+        }
+      }
     }
+    if constexpr (LONG) fold_sum(folded, s, m);
 
     // The largest of the threads' maxima, and a bound that k of them reach: each warp's j-th largest one (8 j >= k), the
     // smallest of the warps' ones; some 3 k do. (The k-th itself took 1.8 us to find by bisection, 0.7 among these.)
@@ -443,7 +478,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
     const uint32_t most = __reduce_max_sync(0xffffffffu, sh.top[lane % kWarps]);  // (0: nothing above -inf)
     const float part_max = most == 0u ? -INFINITY : code_float(most);
     {
-      unsigned long long units = mine != 0u ? __float2ull_rn(s * exp_below(m, part_max) * kSumUnits) : 0ull;
+      unsigned long long units;
+      if constexpr (LONG)
+        units = mine != 0u ? __double2ull_rn(folded.sum[tid] * static_cast<double>(exp_below(m, part_max)) * kSumUnits) : 0ull;
+      else
+        units = mine != 0u ? __float2ull_rn(s * exp_below(m, part_max) * kSumUnits) : 0ull;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
       if (lane == 0) atomicAdd(&sh.sum, units);
@@ -679,7 +718,7 @@ constexpr int shared_bytes(int parts, int k) {
 // Of the widest request with the most candidates in one block, rows whole.
 constexpr int kMostShared = shared_bytes(kBeamMaxWidth, kBeamMaxOut);
 static_assert(kWarps * kBeamMaxOut <= 2 * kWarps * list_cap(kBeamMaxOut), "the keys of all warps, cut down, fit where their lists were");
-static_assert(kMostShared + sizeof(SelectShared) + 2048 <= 232448, "shared memory of a thread block");
+static_assert(kMostShared + sizeof(SelectShared) + sizeof(LongSums) + 2048 <= 232448, "shared memory of a thread block");
 
 struct SelectPlan {
   int ranks, splits, smem;
@@ -707,9 +746,15 @@ SelectPlan plan_select(const BeamSelectArgs& a, int size, int most_ranks) {
   return best;
 }
 
-template <int TYPE>
+// Steps of the longest part.
+int most_steps(const BeamSelectArgs& a, int size, int splits) {
+  const int nv = static_cast<int>((static_cast<long long>(a.vocab) * size + 15) / 16);
+  return ((nv + splits - 1) / splits + kWarps * kStep - 1) / (kWarps * kStep);
+}
+
+template <int TYPE, bool LONG>
 cudaError_t launch_select(const BeamSelectArgs& a, cudaStream_t s) {
-  auto kern = beam_select_kernel<TYPE>;
+  auto kern = beam_select_kernel<TYPE, LONG>;
   static SharedMemoryOnce once;
   cudaError_t e = once.set(kern, kMostShared);
   if (e != cudaSuccess) return e;
@@ -743,6 +788,9 @@ cudaError_t launch_select(const BeamSelectArgs& a, cudaStream_t s) {
     if (dev < SharedMemoryOnce::kDevices) fits[dev].store(f, std::memory_order_relaxed);
   }
   const SelectPlan p = plan_select(a, Logits<TYPE>::SIZE, f > 0 ? 16 : 8);
+  if constexpr (!LONG) {
+    if (most_steps(a, Logits<TYPE>::SIZE, p.splits) > kFold) return launch_select<TYPE, true>(a, s);
+  }
   attr.val.clusterDim.x = p.ranks;
   cfg.gridDim = dim3(static_cast<unsigned>(a.groups) * p.ranks);
   cfg.dynamicSmemBytes = p.smem;
@@ -755,9 +803,9 @@ cudaError_t launch_select(const BeamSelectArgs& a, cudaStream_t s) {
 
 cudaError_t launch_beam_select(const BeamSelectArgs& a, cudaStream_t s) {
   switch (a.type) {
-    case 0: return launch_select<0>(a, s);
-    case 1: return launch_select<1>(a, s);
-    case 2: return launch_select<2>(a, s);
+    case 0: return launch_select<0, false>(a, s);
+    case 1: return launch_select<1, false>(a, s);
+    case 2: return launch_select<2, false>(a, s);
     default: return cudaErrorInvalidValue;
   }
 }

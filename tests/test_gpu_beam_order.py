@@ -83,3 +83,21 @@ def test_select_orders_a_beam_by_its_logits(kind, w, n):
     at = torch.arange(100, device="cuda") * 601 + 7
     x[:, at] = (torch.arange(100, device="cuda") + 1).to(x.dtype) * 2.0**-80
     check_exactly(x, np.zeros((1, w), np.float32), n)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("below", [3.6875, 4.125, 6.1875])
+def test_select_sums_of_long_rows(kind, below):
+    """Four million tokens, one in four of them the largest: additions to a long sum whose roundings all point one way. The
+    beam's score takes the logarithm off, so that the output's rounding hides nothing."""
+    import torch
+    v, w = 1 << 22, 64
+    x = torch.empty((w, v), dtype=getattr(torch, kind), device="cuda")
+    x[0] = -below
+    x[0, ::4] = 0.0
+    log = np.log(v / 4 * (1 + 3 * np.exp(-below)))
+    scores = np.full((1, w), -np.inf, np.float32)
+    scores[0, 0] = log
+    s, p, t = run_select(x, scores, 3)
+    assert p.tolist() == [[0, 0, 0]] and t.tolist() == [[0, 4, 8]]
+    assert np.abs(s - (float(scores[0, 0]) - log)).max() <= LOG
