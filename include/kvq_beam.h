@@ -68,8 +68,12 @@ extern "C" {
  * scores -inf, and candidates at -inf fill up what finite ones leave, by the
  * lower i * vocab + t. Sums are float32 within a thread (at most 64 additions
  * one after the other, of 16 or 32 terms each), float64 or whole numbers beyond.
- * Scores are compared in float64 and rounded once. A row gives the same wherever
- * it starts, and the same call the same bits.
+ * The logarithm of a sum is off by less than 2^-18, in rows of up to 160000
+ * tokens by 2^-20 at most in what was tried (a constant tail: every term carries
+ * the same rounding of its exponent); scores of two beams that are closer may
+ * come in the other order than exact ones. Scores are compared in float64 and
+ * rounded once. A row gives the same wherever it starts, and the same call the
+ * same bits.
  * One launch. KVQ_ERR_UNSUPPORTED for width > KVQ_BEAM_MAX_WIDTH or n_out >
  * KVQ_BEAM_MAX_OUT, KVQ_ERR_ARG for n_out > vocab. */
 KVQ_API kvq_status beam_select(const void* logits, int32_t logits_type, int64_t row_stride, const float* scores,
