@@ -7,7 +7,8 @@
  *   kv_blocks_fork       the block tables follow the parents: full blocks are
  *                        shared, a partly filled last one is given a copy
  *   kv_blocks_copy       those copies, in every layer's pools
- *   kv_blocks_resize, kv_slot_map, fp8_kv_append   (kvq_spec.h) the new tokens
+ *   kv_blocks_resize_shared, and kv_slot_map and fp8_kv_append of kvq_spec.h
+ *                        the new tokens
  *   fp8_group_attention  decode attention that reads the blocks a request's
  *                        beams share once
  * and, now and then, kv_blocks_compact, after which the pool's end is unused.
@@ -21,10 +22,11 @@
  * and a request with fewer continuations leaves the others empty (length 0).
  * Several table entries may name one block. shares[block], device int32
  * [num_blocks], counts the references beyond the first: 0 for a free block and
- * for one that a single entry names, so that blocks which kv_blocks_resize
- * grants need no care (and a resize that shrinks has to give up unshared blocks
- * only). A holder outside the tables, such as a prefix cache, counts itself in
- * shares.
+ * for one that a single entry names, so that blocks which a resize grants need
+ * no care. A holder outside the tables, such as a prefix cache, counts itself in
+ * shares. kv_blocks_resize (kvq_spec.h) knows no shares: what it takes from a
+ * sequence is free for everyone, so that on tables whose blocks may be shared
+ * kv_blocks_resize_shared stands for it.
  */
 #ifndef KVQ_BEAM_H_
 #define KVQ_BEAM_H_
@@ -126,6 +128,18 @@ KVQ_API kvq_status kv_blocks_fork(int32_t* block_table, int32_t batch, int32_t m
                                   int32_t* shares, int32_t* free_blocks, int32_t* free_count, int32_t num_blocks,
                                   int32_t* copy_src, int32_t* copy_dst, int32_t* copy_count, int32_t* granted,
                                   int32_t* shared_blocks, void* ws, size_t ws_bytes, void* stream);
+
+/* kv_blocks_resize (kvq_spec.h) for such tables: a sequence that would release a
+ * block with other references (shares above 0, device int32 [num_blocks], read
+ * alone) is refused like a target outside the table: granted 0, left as it was.
+ * All else is as there. To shorten a sequence that shares blocks, lower
+ * seq_lens and call kv_blocks_fork with every sequence its own parent: it keeps
+ * the counts, frees what nobody holds any more, and copies a block that others
+ * hold in full and the shorter one in part. */
+KVQ_API kvq_status kv_blocks_resize_shared(int32_t* block_table, int32_t batch, int32_t max_blocks, int32_t* n_held,
+                                           const int32_t* target_tokens, int32_t block_tokens, const int32_t* shares,
+                                           int32_t* free_blocks, int32_t* free_count, int32_t num_blocks,
+                                           int32_t* granted, void* stream);
 
 /* One buffer of blocks: block i is the block_bytes bytes at base + i *
  * block_bytes (a multiple of 16). For an fp8_pool or nvfp4_pool: its memory, and

@@ -3,7 +3,7 @@
 One step that keeps several continuations of each request: ``beam_select`` (the
 best candidates from the logits), ``kv_blocks_fork`` (the block tables follow
 the parents; full blocks are shared), ``kv_blocks_copy`` (partly filled last
-blocks, in every layer's pools), then ``spec.kv_blocks_resize``,
+blocks, in every layer's pools), then ``kv_blocks_resize_shared``,
 ``spec.kv_slot_map`` and ``spec.fp8_kv_append`` for the new tokens and
 ``fp8_group_attention`` (decode attention that reads the blocks a request's
 sequences share once). ``kv_blocks_compact`` empties the end of a pool.
@@ -27,8 +27,8 @@ MAX_OUT = 128         # candidates of a request
 COPY_MAX_BUFFERS = 160
 LOGITS = {torch.float16: 0, torch.float32: 1, torch.bfloat16: 2}
 
-EXPORTED = ("beam_select", "kv_blocks_workspace_bytes", "kv_blocks_fork", "kv_blocks_copy", "kv_blocks_compact",
-            "fp8_group_workspace_bytes", "fp8_group_attention")
+EXPORTED = ("beam_select", "kv_blocks_workspace_bytes", "kv_blocks_fork", "kv_blocks_resize_shared", "kv_blocks_copy",
+            "kv_blocks_compact", "fp8_group_workspace_bytes", "fp8_group_attention")
 
 
 class block_buffer(ctypes.Structure):
@@ -40,6 +40,7 @@ _SIG = {
     "kv_blocks_workspace_bytes": ([c_i32, c_i32], c_sz),
     "kv_blocks_fork": ([c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp,
                         c_vp, c_vp, c_sz, c_vp], ctypes.c_int),
+    "kv_blocks_resize_shared": ([c_vp, c_i32, c_i32, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp], ctypes.c_int),
     "kv_blocks_copy": ([ctypes.POINTER(block_buffer), c_i32, c_i32, c_vp, c_vp, c_i32, c_vp, c_vp], ctypes.c_int),
     "kv_blocks_compact": ([c_vp, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp,
                            c_sz, c_vp], ctypes.c_int),
@@ -118,6 +119,24 @@ def kv_blocks_fork(block_table, n_held, seq_lens, parents, width: int, block_tok
         _arg("ws", ws, torch.uint8, size, d), size, _on(stream, d))
     if code:
         _check(code, "kv_blocks_fork")
+
+
+def kv_blocks_resize_shared(block_table, n_held, target_tokens, block_tokens: int, shares, free_blocks, free_count,
+                            granted=None, stream=None) -> None:
+    """``spec.kv_blocks_resize`` on tables that may share blocks: a sequence that
+    would release a block with shares above 0 (int32 [num_blocks]) is refused
+    (granted 0) and left as it was. Shortened sequences: lower seq_lens, then
+    kv_blocks_fork with every sequence its own parent."""
+    d = _here(block_table)
+    b, width = _table(block_table)
+    blocks = free_blocks.numel()
+    code = _lib.kv_blocks_resize_shared(
+        _arg("block_table", block_table, _I32, b * width, d), b, width, _arg("n_held", n_held, _I32, b, d),
+        _arg("target_tokens", target_tokens, _I32, b, d), block_tokens, _arg("shares", shares, _I32, blocks, d),
+        _arg("free_blocks", free_blocks, _I32, blocks, d), _arg("free_count", free_count, _I32, 1, d), blocks,
+        None if granted is None else _arg("granted", granted, _I32, b, d), _on(stream, d))
+    if code:
+        _check(code, "kv_blocks_resize_shared")
 
 
 class BlockBuffers:
@@ -216,8 +235,8 @@ def fp8_group_attention(q, k_pool, v_pool, block_table, seq_lens, shared_blocks,
 
 class BeamTables(BlockTables):
     """Block tables of requests with ``width`` sequences each, which may share blocks: BlockTables with the counts of
-    references, the lists of blocks to copy and what fp8_group_attention goes by. ``resize`` grows as before; it must
-    not shrink shared blocks (``fork`` does that)."""
+    references, the lists of blocks to copy and what fp8_group_attention goes by. ``resize`` refuses a sequence that would
+    release a block that others hold: lower ``seq_lens`` and ``fork`` every sequence to itself."""
 
     def __init__(self, requests: int, width: int, max_blocks: int, num_blocks: int, block_tokens: int = 16, device="cuda"):
         super().__init__(requests * width, max_blocks, num_blocks, block_tokens, device)
@@ -231,6 +250,12 @@ class BeamTables(BlockTables):
         self.copy_count, self.done = torch.zeros(1, **i32), torch.zeros(1, **i32)
         self.moved_to = torch.empty(num_blocks, **i32)
         self.ws = blocks_workspace(requests, num_blocks, device)
+
+    def resize(self, target_tokens, stream=None):
+        """Hold what target_tokens int32 [B] tokens need; returns `granted` (the instance's own buffer)."""
+        kv_blocks_resize_shared(self.table, self.n_held, target_tokens, self.block_tokens, self.shares, self.free_blocks,
+                                self.free_count, self.granted, stream)
+        return self.granted
 
     def fork(self, parents, stream=None):
         """Sequences follow their parents (int32 [requests * width]); copy() has to follow before the next append.

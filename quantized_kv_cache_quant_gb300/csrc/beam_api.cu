@@ -143,6 +143,31 @@ kvq_status kv_blocks_fork(int32_t* block_table, int32_t batch, int32_t max_block
   return from_cuda(kvq::launch_blocks_fork(a, static_cast<cudaStream_t>(stream)));
 }
 
+kvq_status kv_blocks_resize_shared(int32_t* block_table, int32_t batch, int32_t max_blocks, int32_t* n_held,
+                                   const int32_t* target_tokens, int32_t block_tokens, const int32_t* shares,
+                                   int32_t* free_blocks, int32_t* free_count, int32_t num_blocks, int32_t* granted,
+                                   void* stream) {
+  if (!block_table || !n_held || !target_tokens || !shares || !free_blocks || !free_count) return KVQ_ERR_NULL;
+  if (batch <= 0 || max_blocks <= 0 || block_tokens <= 0 || num_blocks <= 0) return KVQ_ERR_ARG;
+  if (batch > KVQ_SPEC_MAX_BATCH || static_cast<long long>(batch) * max_blocks > INT_MAX) return KVQ_ERR_UNSUPPORTED;
+  if (!aligned(block_table) || !aligned(n_held) || !aligned(target_tokens) || !aligned(shares) || !aligned(free_blocks) ||
+      !aligned(free_count) || !aligned(granted))
+    return KVQ_ERR_ALIGN;
+  kvq::BlocksResizeArgs a{};
+  a.block_table = block_table;
+  a.n_held = n_held;
+  a.target_tokens = target_tokens;
+  a.free_blocks = free_blocks;
+  a.free_count = free_count;
+  a.granted = granted;
+  a.shares = shares;
+  a.batch = batch;
+  a.max_blocks = max_blocks;
+  a.block_tokens = block_tokens;
+  a.num_blocks = num_blocks;
+  return from_cuda(kvq::launch_blocks_resize(a, static_cast<cudaStream_t>(stream)));
+}
+
 kvq_status kv_blocks_copy(const kvq_block_buffer* buffers, int32_t n_buffers, int32_t num_blocks, const int32_t* src,
                           const int32_t* dst, int32_t n_pairs, const int32_t* count, void* stream) {
   if (!buffers || !src || !dst) return KVQ_ERR_NULL;

@@ -46,6 +46,7 @@ struct BlocksResizeArgs {
   int32_t* free_blocks;
   int32_t* free_count;
   int32_t* granted;  // or null
+  const int32_t* shares;  // references of each block beyond the first, or null: every block has one
   int batch, max_blocks, block_tokens, num_blocks;
 };
 cudaError_t launch_blocks_resize(const BlocksResizeArgs& a, cudaStream_t s);
