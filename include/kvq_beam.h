@@ -87,9 +87,9 @@ KVQ_API kvq_status beam_select(const void* logits, int32_t logits_type, int64_t 
 /* ------------------------------------------------------------------------ */
 
 /* Workspace of kv_blocks_fork (groups requests) and kv_blocks_compact (any
- * number) for a pool of num_blocks blocks. Zero it once after allocating it: the
- * calls leave it as they need it. Calls that overlap on the device must not
- * share it. 0 for sizes the calls refuse. */
+ * number) for pools of up to num_blocks blocks. Zero it once after allocating it:
+ * the calls leave it as they need it, for pools of other sizes too. Calls that
+ * overlap on the device must not share it. 0 for sizes the calls refuse. */
 KVQ_API size_t kv_blocks_workspace_bytes(int32_t groups, int32_t num_blocks);
 
 /* Every sequence becomes a copy of its parent, in place:

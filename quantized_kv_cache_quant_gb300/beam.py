@@ -89,7 +89,7 @@ def kv_blocks_workspace_bytes(groups: int, num_blocks: int) -> int:
 
 
 def blocks_workspace(groups: int, num_blocks: int, device="cuda"):
-    """A zeroed workspace of kv_blocks_fork (this many requests) and kv_blocks_compact."""
+    """A zeroed workspace of kv_blocks_fork (this many requests) and kv_blocks_compact, for pools of up to num_blocks blocks."""
     n = kv_blocks_workspace_bytes(groups, num_blocks)
     if n == 0:
         raise kvq.KvqError(6, "kv_blocks_workspace_bytes")

@@ -18,10 +18,10 @@ static_assert(kvq::kBeamMaxWidth == KVQ_BEAM_MAX_WIDTH, "the kernels' arrays hol
 static_assert(kvq::kBeamMaxOut == KVQ_BEAM_MAX_OUT, "the same");
 static_assert(kvq::kCopyMaxBuffers == KVQ_COPY_MAX_BUFFERS, "the same");
 
-// Workspace of the block calls: [what compaction knows | 256 B][words of freed blocks][words of free blocks][ranks before
-// each word][per request].
 size_t padded(size_t n) { return (n + 255) / 256 * 256; }
-size_t words_bytes(int32_t num_blocks) { return padded((static_cast<size_t>(num_blocks) + 31) / 32 * sizeof(uint32_t)); }
+// Offsets in the workspace of the block calls (beam_internal.h).
+constexpr size_t kAlikeOffset = kvq::kWsHeader, kWordsOffset = kAlikeOffset + KVQ_SPEC_MAX_BATCH * sizeof(int32_t);
+static_assert(kWordsOffset % 256 == 0, "the words are read 16 bytes at a time");
 
 kvq_status check_workspace(const void* ws, size_t ws_bytes, int32_t groups, int32_t num_blocks) {
   if (ws == nullptr) return KVQ_ERR_WORKSPACE;
@@ -98,7 +98,8 @@ kvq_status beam_select(const void* logits, int32_t logits_type, int64_t row_stri
 
 size_t kv_blocks_workspace_bytes(int32_t groups, int32_t num_blocks) {
   if (groups <= 0 || groups > KVQ_SPEC_MAX_BATCH || num_blocks <= 0 || num_blocks > INT_MAX - 31) return 0;
-  return kvq::kWsHeader + 3 * words_bytes(num_blocks) + padded(static_cast<size_t>(groups) * sizeof(int32_t));
+  const size_t words = (static_cast<size_t>(num_blocks) + 31) / 32;
+  return kWordsOffset + (words + kvq::kWordChunk - 1) / kvq::kWordChunk * kvq::kChunkStride * sizeof(uint32_t);
 }
 
 kvq_status kv_blocks_fork(int32_t* block_table, int32_t batch, int32_t max_blocks, int32_t* n_held, int32_t* seq_lens,
@@ -132,9 +133,9 @@ kvq_status kv_blocks_fork(int32_t* block_table, int32_t batch, int32_t max_block
   a.copy_count = copy_count;
   a.granted = granted;
   a.shared_blocks = shared_blocks;
-  uint8_t* const base = static_cast<uint8_t*>(ws) + kvq::kWsHeader;
-  a.bits = reinterpret_cast<uint32_t*>(base);
-  a.alike = reinterpret_cast<int32_t*>(base + 3 * words_bytes(num_blocks));
+  uint8_t* const base = static_cast<uint8_t*>(ws);
+  a.alike = reinterpret_cast<int32_t*>(base + kAlikeOffset);
+  a.bits = reinterpret_cast<uint32_t*>(base + kWordsOffset);
   a.batch = batch;
   a.max_blocks = max_blocks;
   a.width = width;
@@ -226,8 +227,8 @@ kvq_status kv_blocks_compact(int32_t* block_table, int32_t batch, int32_t max_bl
   a.done = done;
   uint8_t* const base = static_cast<uint8_t*>(ws);
   a.state = reinterpret_cast<kvq::CompactState*>(base);
-  a.bits = reinterpret_cast<uint32_t*>(base + kvq::kWsHeader + words_bytes(num_blocks));
-  a.before = reinterpret_cast<int32_t*>(base + kvq::kWsHeader + 2 * words_bytes(num_blocks));
+  a.bits = reinterpret_cast<uint32_t*>(base + kWordsOffset) + kvq::kWordChunk;
+  a.before = reinterpret_cast<int32_t*>(base + kWordsOffset) + 2 * kvq::kWordChunk;
   a.batch = batch;
   a.max_blocks = max_blocks;
   a.keep = keep_blocks;

@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(32 * kForkWarps) fork_entries_kernel(const Blo
       const int old = old_s[i * 32 + lane], now = c < want_s[i] ? old_s[parent_s[i] * 32 + lane] : -1;
       if (now != old && counted(old) && atomicSub(a.shares + old, 1) == 0) {
         a.shares[old] = 0;
-        atomicOr(a.bits + (old >> 5), 1u << (old & 31));
+        atomicOr(a.bits + word_at(old >> 5), 1u << (old & 31));
       }
     }
     if (!alike && c < full) first_differing = min(first_differing, c);
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(1024) fork_tails_kernel(const BlocksForkArgs a
     }
   }
   unsigned long long mine = 0, ignore;
-  for (int i = w0 + threadIdx.x; i < w1; i += blockDim.x) mine += __popc(__ldcg(a.bits + i));
+  for (int i = w0 + threadIdx.x; i < w1; i += blockDim.x) mine += __popc(__ldcg(a.bits + word_at(i)));
   (void)block_scan(mine, scan_ws, ignore);
   long long before = 0, freed = static_cast<long long>(ignore);
   if (ranks > 1) {
@@ -162,12 +162,12 @@ __global__ void __launch_bounds__(1024) fork_tails_kernel(const BlocksForkArgs a
   if (freed > 0) {
     for (int i0 = w0; i0 < w1; i0 += blockDim.x) {
       const int i = i0 + threadIdx.x;
-      uint32_t word = i < w1 ? __ldcg(a.bits + i) : 0u;
+      uint32_t word = i < w1 ? __ldcg(a.bits + word_at(i)) : 0u;
       __syncthreads();
       unsigned long long total;
       long long e = before + static_cast<long long>(block_scan(__popc(word), scan_ws, total));
       before += static_cast<long long>(total);
-      if (word != 0) a.bits[i] = 0u;
+      if (word != 0) a.bits[word_at(i)] = 0u;
       for (; word != 0; word &= word - 1, ++e) {
         const long long place = count + freed - 1 - e;
         if (place >= 0 && place < a.num_blocks) a.free_blocks[place] = 32 * i + __ffs(word) - 1;
@@ -309,7 +309,7 @@ template <bool SAME>
 __device__ __forceinline__ int mover_rank(const BlocksCompactArgs& a, int x, uint32_t word) {
   const int i = x >> 5;
   // (the word that keep cuts counts the targets before it; it is the first with movers)
-  return (i > a.keep >> 5 ? passed<SAME>(a.before + i) : 0) + __popc(mover_bits(a, i, word) & ((1u << (x & 31)) - 1u));
+  return (i > a.keep >> 5 ? passed<SAME>(a.before + word_at(i)) : 0) + __popc(mover_bits(a, i, word) & ((1u << (x & 31)) - 1u));
 }
 
 // The four passes, by thread `me` of `threads`.
@@ -317,7 +317,7 @@ __device__ __forceinline__ void compact_mark(const BlocksCompactArgs& a, long lo
   const int count = min(max(*a.free_count, 0), a.num_blocks);
   for (long long i = me; i < count; i += threads) {
     const int x = a.free_blocks[i];
-    if (x >= 0 && x < a.num_blocks) atomicOr(a.bits + (x >> 5), 1u << (x & 31));
+    if (x >= 0 && x < a.num_blocks) atomicOr(a.bits + word_at(x >> 5), 1u << (x & 31));
   }
 }
 
@@ -332,10 +332,10 @@ __device__ __forceinline__ void compact_rank(const BlocksCompactArgs& a, unsigne
     return static_cast<unsigned long long>(__popc(target_bits(a, i, word))) |
            (static_cast<unsigned long long>(__popc(mover_bits(a, i, word))) << 32);
   };
-  // a thread's four words from i on (the bits' memory is a multiple of 256 bytes), and their counts
+  // a thread's four words from i on (i a multiple of 4: they lie side by side), and their counts
   auto four = [&](int i, unsigned long long (&n)[4]) -> unsigned long long {
     uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (i < w1) w = __ldcg(reinterpret_cast<const uint4*>(a.bits + i));
+    if (i < w1) w = __ldcg(reinterpret_cast<const uint4*>(a.bits + word_at(i)));
     const uint32_t word[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) n[e] = i + e < w1 ? both(i + e, word[e]) : 0ull;
@@ -359,7 +359,7 @@ __device__ __forceinline__ void compact_rank(const BlocksCompactArgs& a, unsigne
     unsigned long long at = before + block_scan(sum, scan_ws, total);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      if (i + e < w1) a.before[i + e] = static_cast<int32_t>(i + e <= cut ? at & 0xffffffffu : at >> 32);
+      if (i + e < w1) a.before[word_at(i) + e] = static_cast<int32_t>(i + e <= cut ? at & 0xffffffffu : at >> 32);
       at += n[e];
     }
     before += total;
@@ -384,10 +384,10 @@ __device__ __forceinline__ void compact_lists(const BlocksCompactArgs& a, long l
   const int lane = threadIdx.x & 31, words = (a.num_blocks + 31) / 32;
   const uint32_t below = (1u << lane) - 1u;
   for (long long i = me >> 5; i < words; i += threads >> 5) {
-    const uint32_t word = passed<SAME>(a.bits + i), to = target_bits(a, i, word), from = mover_bits(a, i, word);
+    const uint32_t word = passed<SAME>(a.bits + word_at(static_cast<int>(i))), to = target_bits(a, i, word), from = mover_bits(a, i, word);
     const int x = 32 * static_cast<int>(i) + lane;
     if (to >> lane & 1u) {
-      const int r = passed<SAME>(a.before + i) + __popc(to & below);
+      const int r = passed<SAME>(a.before + word_at(static_cast<int>(i))) + __popc(to & below);
       if (r < movers) a.copy_dst[r] = x;
       else a.free_blocks[targets - 1 - r] = x;
     }
@@ -401,7 +401,7 @@ __device__ __forceinline__ void compact_follow(const BlocksCompactArgs& a, long 
   // where block x is now
   auto now = [&](int x) -> int {
     if (!done || x < a.keep) return x;
-    const uint32_t word = passed<SAME>(a.bits + (x >> 5));
+    const uint32_t word = passed<SAME>(a.bits + word_at(x >> 5));
     return word >> (x & 31) & 1u ? x : passed<SAME>(a.copy_dst + mover_rank<SAME>(a, x, word));
   };
   for (long long x = me; x < a.num_blocks; x += threads) {
@@ -441,7 +441,7 @@ __device__ __forceinline__ long long grid_threads() { return static_cast<long lo
 
 __global__ void __launch_bounds__(kCompactThreads) compact_clear_kernel(const BlocksCompactArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  for (long long i = grid_thread(); i < (a.num_blocks + 31) / 32; i += grid_threads()) a.bits[i] = 0u;
+  for (long long i = grid_thread(); i < (a.num_blocks + 31) / 32; i += grid_threads()) a.bits[word_at(static_cast<int>(i))] = 0u;
 }
 __global__ void __launch_bounds__(kCompactThreads) compact_mark_kernel(const BlocksCompactArgs a) {
   compact_begin();
@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kCompactThreads) compact_follow_kernel(const B
 __global__ void __launch_bounds__(1024) compact_cluster_kernel(const BlocksCompactArgs a) {
   __shared__ unsigned long long scan_ws[32], sums_s;
   cg::cluster_group cluster = cg::this_cluster();
-  for (long long i = grid_thread(); i < (a.num_blocks + 31) / 32; i += grid_threads()) a.bits[i] = 0u;
+  for (long long i = grid_thread(); i < (a.num_blocks + 31) / 32; i += grid_threads()) a.bits[word_at(static_cast<int>(i))] = 0u;
   cluster.sync();
   compact_mark(a, grid_thread(), grid_threads());
   cluster.sync();

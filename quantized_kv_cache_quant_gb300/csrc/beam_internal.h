@@ -23,6 +23,15 @@ struct BeamSelectArgs {
 };
 cudaError_t launch_beam_select(const BeamSelectArgs& a, cudaStream_t s);
 
+// Workspace of the block calls: [what compaction knows | 256 B][per request, 16 KB][by 64 words of 32 blocks each: words of
+// freed blocks, words of free blocks, ranks before each word]. The place of a word is the same for pools of all sizes, so
+// that what one call needs at 0 is never what another one left.
+constexpr int kWordChunk = 64;
+constexpr int kChunkStride = 3 * kWordChunk;
+__host__ __device__ constexpr long long word_at(int i) {
+  return static_cast<long long>(i / kWordChunk) * kChunkStride + i % kWordChunk;
+}
+
 struct BlocksForkArgs {
   int32_t* block_table;
   int32_t* n_held;
@@ -36,7 +45,7 @@ struct BlocksForkArgs {
   int32_t* copy_count;
   int32_t* granted;        // or null
   int32_t* shared_blocks;  // or null
-  uint32_t* bits;          // [ceil(num_blocks / 32)] blocks freed; 0 between calls
+  uint32_t* bits;          // word_at(0 .. ceil(num_blocks / 32) - 1): blocks freed; 0 between calls
   int32_t* alike;          // [batch / width] max_blocks - first column that differs; 0 between calls
   int batch, max_blocks, width, block_tokens, num_blocks;
 };
@@ -68,8 +77,8 @@ struct BlocksCompactArgs {
   int32_t* copy_dst;
   int32_t* copy_count;
   int32_t* done;
-  uint32_t* bits;        // [ceil(num_blocks / 32)] free blocks
-  int32_t* before;       // [ceil(num_blocks / 32)] free blocks below keep, used ones from keep on, in the words before
+  uint32_t* bits;        // word_at(0 .. ceil(num_blocks / 32) - 1): free blocks
+  int32_t* before;       // the same: free blocks below keep, used ones from keep on, in the words before
   CompactState* state;
   int batch, max_blocks, keep, num_blocks, max_copies;
 };
