@@ -10,7 +10,7 @@
  *   kv_blocks_resize_shared, and kv_slot_map and fp8_kv_append of kvq_spec.h
  *                        the new tokens
  *   fp8_group_attention  decode attention that reads the blocks a request's
- *                        beams share once
+ *                        beams share once (for up to 128 query rows a kv head)
  * and, now and then, kv_blocks_compact, after which the pool's end is unused.
  * Everything that changes from step to step is read on the device: no call
  * copies to the host or waits, so a step captures into a CUDA graph. The
@@ -195,8 +195,9 @@ KVQ_API size_t fp8_group_workspace_bytes(int32_t batch, int32_t width, int32_t k
  * blocks: as fp8_decode_attention (q in fp16),
  *   out[b, hq] = softmax(q[b, hq] . (k_scale K)^T * softmax_scale) (v_scale V)
  * over tokens 0 .. seq_lens[b] - 1 of sequence b, zeros where seq_lens[b] <= 0,
- * but the blocks that a group's sequences share are read (and converted) once a
- * group:
+ * but the blocks that a group's sequences share are read (and converted) once for
+ * all of the group's query rows of a kv head, width * (q_heads / kv_heads), up to
+ * 128 of them, and once for every 128 beyond:
  *   q             : device fp16, row b at q + b * q_row_stride is [q_heads, D]
  *   block_table   : device int32 [batch, max_blocks]
  *   seq_lens      : device int32 [batch], the new tokens included
@@ -212,8 +213,11 @@ KVQ_API size_t fp8_group_workspace_bytes(int32_t batch, int32_t width, int32_t k
  * the device: a bad one gives wrong numbers, never an access outside the buffers.
  * The softmax weights go into the value product in two fp16 parts (2^-22
  * relative), but over shared blocks for fp16 output with width * (q_heads /
- * kv_heads) > 16 in one (2^-11 relative, as the output itself). Scores, sums and
- * outputs accumulate in fp32. The same call gives the same bits.
+ * kv_heads) > 16 in one (2^-11 relative, as the output itself, so that an output
+ * that is small beside the values it is made of may be off by several steps):
+ * two would take such calls 1.2 to 1.7 times as long, as fp32 output, which has
+ * them, does. Scores, sums and outputs accumulate in fp32. The same call gives
+ * the same bits.
  * KVQ_ERR_UNSUPPORTED for batch > KVQ_SPEC_MAX_BATCH, width >
  * KVQ_BEAM_MAX_WIDTH, q_heads / kv_heads > KVQ_TREE_MAX_GQA or batch * q_heads >=
  * 2^31; KVQ_ERR_SHAPE for batch % width != 0. */

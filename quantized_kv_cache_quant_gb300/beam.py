@@ -209,10 +209,11 @@ def fp8_group_attention(q, k_pool, v_pool, block_table, seq_lens, shared_blocks,
                         softmax_scale: float, ws, stream=None) -> None:
     """Decode attention of sequences in groups of ``width`` whose first
     shared_blocks int32 [B / width] table entries are the same: these blocks are
-    read once a group. q fp16 [B, Hq, D] (rows may lie apart); out fp16 or fp32
-    [B, Hq, D]; block_table int32 [B, max_blocks]; seq_lens int32 [B] (0: an empty
-    sequence, whose output is 0); ws uint8, zeroed once, at least
-    fp8_group_workspace_bytes."""
+    read once a group (once for every 128 query rows, width * Hq / H, of a kv
+    head). q fp16 [B, Hq, D] (rows may lie apart); out fp16 or fp32 [B, Hq, D]
+    (fp32 is the more exact, and slower above 16 such rows); block_table int32
+    [B, max_blocks]; seq_lens int32 [B] (0: an empty sequence, whose output is 0);
+    ws uint8, zeroed once, at least fp8_group_workspace_bytes."""
     d = _here(q)
     if q.dim() != 3:
         raise ValueError(f"q: [B, Hq, D] expected, not {tuple(q.shape)}")

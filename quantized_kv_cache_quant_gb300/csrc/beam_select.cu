@@ -29,8 +29,8 @@
 // k-th of the maxima, so that fewer steps are read again, 51.4 against 52, but with
 // fp32 logits 69.5 against 64.3 and 152 against 133 us for one request of 64 beams.)
 //
-// 512 rows of 128000 bf16 logits (one in five ended): 45 us, 2.3 TB/s; fp32, all
-// alive, 63 us, 4.1 TB/s; one request of 4 x 32000: 12.4 us. The large calls are bound
+// Called in a row: 512 rows of 128000 bf16 logits (one in five ended) 46 us, 2.3
+// TB/s; fp32, all alive, 64 us, 4.1 TB/s; one request of 4 x 32000 9.8 us. The large calls are bound
 // by instructions on the SMs that have four rows at once (of 128000: some 28 us; the
 // mean row takes 18), then comes a part's end (bound, second look, ranking: 5 us)
 // and the first block's scores (5), which other clusters' reading hides in part. The
@@ -724,9 +724,12 @@ struct SelectPlan {
   int ranks, splits, smem;
 };
 
-// Blocks of a cluster (up to 16: one request is one cluster), as many as have room at once, and parts of a row, so that
-// the block with the most to do has little of it; a part costs what `fixed` bytes of logits do beside its own. (64
-// requests of 8 rows of 128000: clusters of 2, 4, 8 and 16 blocks 88, 57, 51 and 67 us; four blocks an SM allow 8.)
+// Blocks of a cluster (up to 16: one request is one cluster), as many as have room at once where four fit an SM, and parts
+// of a row, so that the block with the most to do has little of it; a part costs what `fixed` bytes of logits do beside its
+// own. (64 requests of 8 rows of 128000: clusters of 2, 4, 8 and 16 blocks 88, 57, 51 and 67 us; four blocks an SM allow 8.)
+// Four blocks fit while a request's lists are small. Those of 64 beams with 128 candidates take 161 KB, which the other
+// blocks of its cluster hold too without a use for it: one block an SM, and many such requests run in several waves (64
+// requests of 64 rows of 32000 fp16 logits: 126 us with 16 candidates, 981 with 128).
 SelectPlan plan_select(const BeamSelectArgs& a, int size, int most_ranks) {
   SelectPlan best{1, 1, 0};
   const long long fixed = 16384;

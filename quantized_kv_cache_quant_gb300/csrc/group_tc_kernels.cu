@@ -29,6 +29,10 @@
 // D = 64 the copies are what the conversion waits for. No faster: a second
 // copying warp (277 us), a place handed on through shared memory (274), weights
 // made before the wait for the products before (265).
+// WIDE, by fp32 output: 347 us (1.37 times as long; 1.2 to 1.3 with 64 channels and
+// up to 64 rows, 1.7 with 128 channels and rows): twice the value products and, with
+// 128 channels, two places for the copies in place of four. With fp16 output one part leaves 2.24e-4
+// of error against 64 bits there, of which the output's rounding is 2.05e-4.
 #include "group_plan.cuh"
 #include "tc_device.cuh"
 
