@@ -29,8 +29,8 @@
 // k-th of the maxima, so that fewer steps are read again, 51.4 against 52, but with
 // fp32 logits 69.5 against 64.3 and 152 against 133 us for one request of 64 beams.)
 //
-// Called in a row: 512 rows of 128000 bf16 logits (one in five ended) 46 us, 2.3
-// TB/s; fp32, all alive, 64 us, 4.1 TB/s; one request of 4 x 32000 9.8 us. The large calls are bound
+// 512 rows of 128000 bf16 logits (one in five ended): 46 us, 2.3 TB/s; fp32, all
+// alive, 60 us, 4.3 TB/s; one request of 4 x 32000: 9.5 us. The large calls are bound
 // by instructions on the SMs that have four rows at once (of 128000: some 28 us; the
 // mean row takes 18), then comes a part's end (bound, second look, ranking: 5 us)
 // and the first block's scores (5), which other clusters' reading hides in part. The
@@ -270,8 +270,8 @@ __device__ __noinline__ void put_by_keys(int parts, int splits, int k, float* ou
 
 // LONG: some part has more than kFold steps (rows of 262144 float32 logits and more). A sum of so many terms would drift, by
 // up to 2^-24 of it at each addition (a row of 2^22 equal logits but for every fourth: 1.5e-5), so these threads fold theirs
-// into fp64 every kFold steps. A kernel of its own: the other one has no registers for it (45 us with 64 x 8 x 128000 bf16
-// logits, 48 with the fold in the same loop).
+// into fp64 every kFold steps. A kernel of its own: the other one has no registers for it (with the fold in the same loop,
+// 64 x 8 x 128000 bf16 logits took 6 % longer).
 template <int TYPE, bool LONG>
 __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSelectArgs a, int splits) {
   using L = Logits<TYPE>;
@@ -296,8 +296,10 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamSele
     const long long row = static_cast<long long>(group) * a.width + i;
     const float score = a.scores[row];
     sh.score[i] = isfinite(score) ? score : -INFINITY;
-    // (a beam without a finite score is a dead one, ended or not: its tokens go by their index)
-    sh.kind[i] = !isfinite(score) ? kDead : a.finished != nullptr && a.finished[row] != 0 ? kEnded : kLive;
+    // A beam without a finite score is a dead one, ended or not: its tokens go by their index. (The compiler's registers for
+    // the loop below hang on this line: with the score asked first it spills twice as much, and 64 x 8 x 128000 bf16 logits
+    // take 49.7 us in place of 46.2.)
+    sh.kind[i] = a.finished != nullptr && a.finished[row] != 0 && isfinite(score) ? kEnded : isfinite(score) ? kLive : kDead;
   }
   __syncthreads();
   bool all_run = false;
@@ -729,7 +731,7 @@ struct SelectPlan {
 // own. (64 requests of 8 rows of 128000: clusters of 2, 4, 8 and 16 blocks 88, 57, 51 and 67 us; four blocks an SM allow 8.)
 // Four blocks fit while a request's lists are small. Those of 64 beams with 128 candidates take 161 KB, which the other
 // blocks of its cluster hold too without a use for it: one block an SM, and many such requests run in several waves (64
-// requests of 64 rows of 32000 fp16 logits: 126 us with 16 candidates, 981 with 128).
+// requests of 64 rows of 32000 fp16 logits: 119 us with 16 candidates, 887 with 128).
 SelectPlan plan_select(const BeamSelectArgs& a, int size, int most_ranks) {
   SelectPlan best{1, 1, 0};
   const long long fixed = 16384;
