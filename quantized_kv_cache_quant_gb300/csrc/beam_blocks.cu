@@ -23,9 +23,9 @@ namespace cg = cooperative_groups;
 // adds a reference to a block without holding one itself, so a count falls below
 // 0 only when the last reference has gone, and for one thread only: that thread
 // marks the block as free.
-// Both launches: 64 requests of 8 sequences over 32K tokens 18.5 us, 8 requests
-// of 4 over 1000 tokens 12.4. That is latency, a chain of loads, atomics and
-// barriers in each of them.
+// Both launches, called in a row: 64 requests of 8 sequences over 32K tokens 15.9
+// us, 8 requests of 4 over 1000 tokens 9.0. That is latency, a chain of loads,
+// atomics and barriers in each of them.
 // ---------------------------------------------------------------------------
 constexpr int kForkWarps = 4;
 
