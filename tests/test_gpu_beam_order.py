@@ -165,3 +165,41 @@ def test_select_every_place_of_large_logits(at):
     x[:3] += np.float32(at)
     x[3:, 15000:] += np.float32(at)
     check_exactly(dev(x), rng.uniform(-9, 0, (2, 3)).astype(np.float32), 5)
+
+
+@pytest.mark.parametrize("kind,v", [("float32", 300003), ("float16", 600001), ("bfloat16", 600001)])
+@pytest.mark.parametrize("shift", [0, 3])
+def test_select_every_place_of_long_rows(kind, v, shift):
+    """Rows whose sums are folded on the way: banned, rising, with NaN and infinities, on any boundary."""
+    import torch
+    rng = np.random.default_rng(shift)
+    w = 16
+    whole = torch.full((w, v + 5), float("nan"), dtype=getattr(torch, kind), device="cuda")
+    x = whole[:, shift:shift + v]
+    x.copy_(logits(rng, w, v, kind))
+    ramp = torch.arange(v, device="cuda") / v
+    x[1] = (3 * ramp).to(x.dtype)
+    x[2] = (0.01 * ramp - 70000 * (kind != "float16")).to(x.dtype)
+    x[3] = -float("inf")
+    x[4, : v - 4] = float("nan")
+    x[5, : v // 2] = -float("inf")
+    x[6, v // 3] = float("inf")
+    scores = rng.uniform(-14, -10, (1, w)).astype(np.float32)
+    scores[0, 7] = -np.inf
+    check_exactly(x, scores, 40)
+    finished = rng.random((1, w)) < 0.3
+    check_exactly(x, scores, 128, finished, v - 1)
+
+
+def test_select_of_many_small_requests():
+    import torch
+    rng = np.random.default_rng(3)
+    x = logits(rng, 70000 * 2, 21, "float16")
+    scores = rng.uniform(-9, 0, (70000, 2)).astype(np.float32)
+    s, p, t = run_select(x, scores, 5)
+    y = x.double().view(70000, 2, 21)
+    y = torch.log_softmax(y, 2) + dev(scores).double()[..., None]
+    best = y.view(70000, 42).sort(dim=1, descending=True).values
+    assert np.abs(s - host(best[:, :5])).max() <= LOG + 2.0**-24 * float(best.abs().max())
+    own = host(y.view(70000, 42).gather(1, dev((p * 21 + t).astype(np.int64))))
+    assert np.abs(own - host(best[:, :5])).max() <= 2 * LOG
